@@ -19,6 +19,9 @@ __all__ = [
     "CODEBOOK_NF4", "CODEBOOK_FP4", "CODEBOOK_INT4", "CODEBOOKS", "qlora_quantize_workspace",
     "qlora_fwd_workspace", "qlora_bwd_workspace", "qlora_quantize_nf4", "qlora_dequant", "qlora_linear_fwd",
     "qlora_linear_bwd", "qlora_merge_adapter", "qlora_adamw_step", "qlora_profile_enable", "qlora_profile_read", "lib",
+    "KVCache", "KVBatch", "kv_alloc", "qlora_qk_norm_rope", "qlora_qk_norm_rope_bwd_workspace",
+    "qlora_qk_norm_rope_bwd", "qlora_kv_sizes", "qlora_kv_write", "qlora_kv_read", "qlora_kv_attn_workspace",
+    "qlora_kv_attn",
 ]
 
 
@@ -266,6 +269,318 @@ def qlora_state_page_in(host: torch.Tensor, dev: torch.Tensor, stream=None) -> t
     _page_args(dev, host)
     _check(lib().qlora_state_page_in(_ptr(host), _ptr(dev), dev.nbytes, _stream(stream)), "qlora_state_page_in")
     return dev
+
+
+# ---- between the projections: head norms and rotation, the 4-bit key/value cache, its attention --------
+class _on:
+    """The device a call's tensors live on, its stream, and (in `ptr`) the stream's handle.  Everything
+    the call allocates belongs to that stream, so it is not reused before the kernels are done."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        self.device = t.device
+        self.stream = stream
+        self.guards = []
+
+    def __enter__(self):
+        if self.device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(self.device))
+            self.guards[-1].__enter__()
+        if self.stream is None:
+            self.stream = torch.cuda.current_stream(self.device)
+        else:
+            if self.stream.device != self.device:
+                for g in reversed(self.guards):
+                    g.__exit__(None, None, None)
+                raise QLoRAError(f"the stream is on {self.stream.device}, the tensors on {self.device}")
+            self.guards.append(torch.cuda.stream(self.stream))
+            self.guards[-1].__enter__()
+        self.ptr = C.c_void_p(self.stream.cuda_stream)
+        return self
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _need(t, dtype, device, name, shape=None):
+    """A contiguous tensor of `dtype` on `device` (and of `shape`)."""
+    if t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise QLoRAError(f"{name} must be a contiguous {dtype} tensor on {device}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise QLoRAError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
+    return t
+
+
+def _heads(t: torch.Tensor, name: str, device=None, shape=None) -> _lib.qlora_heads:
+    """The view of a bf16 [rows][heads][head_dim] tensor, any strides with a dense last dimension."""
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+        raise QLoRAError(f"{name} must be a bf16 [rows][heads][head_dim] tensor on the GPU, dense along head_dim")
+    if device is not None and t.device != device:
+        raise QLoRAError(f"{name} must be on {device}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise QLoRAError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
+    return _lib.qlora_heads(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1], 0)
+
+
+def _ref(x):
+    return None if x is None else C.byref(x)
+
+
+def _bytes(ws, nbytes: int, device):
+    """The caller's workspace, checked, or a new one."""
+    if ws is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    if ws.device != device or not ws.is_contiguous():
+        raise QLoRAError(f"workspace must be a contiguous tensor on {device}")
+    return ws
+
+
+@dataclass(frozen=True)
+class KVCache:
+    """A key/value cache in 4 bits: caller-owned device buffers, laid out as include/qlora.h says."""
+    k_codes: torch.Tensor    # uint8 [pages][heads][page_size][head_dim / 2]
+    k_scale: torch.Tensor    # bf16 [pages][heads][page_size][head_dim / block]
+    v_codes: torch.Tensor
+    v_scale: torch.Tensor
+    block: int = 64          # elements per scale: 32, 64 or 128
+    codebook: int = CODEBOOK_NF4
+
+    def __post_init__(self):
+        c = self.k_codes
+        if c.dim() != 4 or not c.is_cuda or c.dtype != torch.uint8:
+            raise QLoRAError("k_codes must be a uint8 [pages][heads][page_size][head_dim / 2] tensor on the GPU")
+        pages, heads, page_size, half = c.shape
+        if self.block not in (32, 64, 128) or 2 * half % self.block:
+            raise QLoRAError(f"block must be 32, 64 or 128 and divide head_dim, not {self.block}")
+        scales = (pages, heads, page_size, 2 * half // self.block)
+        _need(c, torch.uint8, c.device, "k_codes")
+        _need(self.v_codes, torch.uint8, c.device, "v_codes", tuple(c.shape))
+        _need(self.k_scale, torch.bfloat16, c.device, "k_scale", scales)
+        _need(self.v_scale, torch.bfloat16, c.device, "v_scale", scales)
+        # the fields are frozen, so the descriptor is made once
+        object.__setattr__(self, "_desc", _lib.qlora_kv_cache(
+            pages, page_size, heads, 2 * half, int(self.block), int(self.codebook), 0, self.k_codes.data_ptr(),
+            self.k_scale.data_ptr(), self.v_codes.data_ptr(), self.v_scale.data_ptr()))
+
+    @property
+    def pages(self) -> int:
+        return self.k_codes.shape[0]
+
+    @property
+    def heads(self) -> int:
+        return self.k_codes.shape[1]
+
+    @property
+    def page_size(self) -> int:
+        return self.k_codes.shape[2]
+
+    @property
+    def head_dim(self) -> int:
+        return 2 * self.k_codes.shape[3]
+
+    def desc(self) -> _lib.qlora_kv_cache:
+        return self._desc
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.k_codes, self.k_scale, self.v_codes, self.v_scale))
+
+
+def qlora_kv_sizes(pages: int, page_size: int, heads: int, head_dim: int, block: int = 64):
+    """(bytes of one codes buffer, bytes of one scale buffer) of a cache."""
+    d = _lib.qlora_kv_cache(pages, page_size, heads, head_dim, int(block), 0, 0, None, None, None, None)
+    out = [C.c_size_t(), C.c_size_t()]
+    _check(lib().qlora_kv_sizes(C.byref(d), *[C.byref(o) for o in out]), "qlora_kv_sizes")
+    return tuple(o.value for o in out)
+
+
+def kv_alloc(pages: int, page_size: int, heads: int, head_dim: int, block: int = 64, codebook: int = CODEBOOK_NF4,
+             device="cuda") -> KVCache:
+    """An empty cache (its contents are undefined until written)."""
+    qlora_kv_sizes(pages, page_size, heads, head_dim, block)   # checks the sizes
+    bufs = []
+    for _ in range(2):
+        bufs.append(torch.empty((pages, heads, page_size, head_dim // 2), dtype=torch.uint8, device=device))
+        bufs.append(torch.empty((pages, heads, page_size, head_dim // block), dtype=torch.bfloat16, device=device))
+    return KVCache(*bufs, block, codebook)
+
+
+@dataclass(frozen=True)
+class KVBatch:
+    """The tokens a call is about: rows start[b] .. start[b + 1] - 1 are the last ones of sequence b, whose
+    length[b] tokens lie in the pages table[b].  Device tensors that the kernels read, so their contents may
+    change between calls (and between replays of a captured call)."""
+    start: torch.Tensor               # int32 [batch + 1]
+    length: torch.Tensor              # int32 [batch]
+    table: torch.Tensor               # int32 [batch][max_pages]
+    fault: torch.Tensor | None = None   # int32 [1]: bits of wrong entries are OR-ed in (see include/qlora.h)
+
+    def __post_init__(self):
+        n, dev = self.length.numel(), self.length.device
+        if not self.length.is_cuda or self.table.dim() != 2:
+            raise QLoRAError("start, length and table must be on the GPU, table [batch][max_pages]")
+        _need(self.length, torch.int32, dev, "length", (n,))
+        _need(self.start, torch.int32, dev, "start", (n + 1,))
+        _need(self.table, torch.int32, dev, "table", (n, self.table.shape[1]))
+        if self.fault is not None:
+            _need(self.fault, torch.int32, dev, "fault", (1,))
+        object.__setattr__(self, "_desc", _lib.qlora_kv_batch(
+            n, self.table.shape[1], self.start.data_ptr(), self.length.data_ptr(), self.table.data_ptr(),
+            None if self.fault is None else self.fault.data_ptr()))
+
+    def desc(self) -> _lib.qlora_kv_batch:
+        return self._desc
+
+
+def _same_device(cache: KVCache, batch: KVBatch):
+    if cache.k_codes.device != batch.length.device:
+        raise QLoRAError("the cache and the batch must be on one device")
+    return cache.k_codes.device
+
+
+def _qk_inputs(q, k, positions, inv_freq, q_weight, k_weight):
+    rows, _, dim = q.shape
+    dev = q.device
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _need(inv_freq, torch.float32, dev, "inv_freq", (inv_freq.numel(),))
+    if rot:
+        if positions is None:
+            raise QLoRAError("inv_freq needs positions")
+        _need(positions, torch.int64, dev, "positions", (rows,))
+    if k is None and k_weight is not None:
+        raise QLoRAError("k_weight needs k")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, torch.bfloat16, dev, name, (dim,))
+    return rows, dim, rot, dev
+
+
+def qlora_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor | None,
+                       inv_freq: torch.Tensor | None, q_weight: torch.Tensor | None = None,
+                       k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                       q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """Norm of each head (where its weight is given) and rotation by positions [rows] (int64) * inv_freq
+    [rot_dim / 2] (fp32) of q, k [rows][heads][head_dim] bf16, any strides.  The outputs may be the inputs.
+    Returns (q_out, k_out or None)."""
+    hq = _heads(q, "q")
+    hk = None if k is None else _heads(k, "k", q.device, (q.shape[0], k.shape[1], q.shape[2]))
+    rows, dim, rot, dev = _qk_inputs(q, k, positions, inv_freq, q_weight, k_weight)
+    with _on(q, stream) as on:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+        oq = _heads(q_out, "q_out", dev, tuple(q.shape))
+        ok = None if k_out is None else _heads(k_out, "k_out", dev, None if k is None else tuple(k.shape))
+        _check(lib().qlora_qk_norm_rope(_ref(hq), _ref(hk), rows, dim, _ptr(q_weight), _ptr(k_weight), float(eps),
+                                        _ptr(positions), _ptr(inv_freq), rot, int(interleaved), _ref(oq), _ref(ok),
+                                        on.ptr), "qlora_qk_norm_rope")
+    return q_out, k_out
+
+
+def qlora_qk_norm_rope_bwd_workspace(rows: int, q_heads: int, k_heads: int, head_dim: int) -> int:
+    return lib().qlora_qk_norm_rope_bwd_workspace(rows, q_heads, k_heads, head_dim)
+
+
+def qlora_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q: torch.Tensor | None,
+                           k: torch.Tensor | None, positions: torch.Tensor | None, inv_freq: torch.Tensor | None,
+                           q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                           eps: float = 1e-6, interleaved: bool = False, dq: torch.Tensor | None = None,
+                           dk: torch.Tensor | None = None, dq_weight: torch.Tensor | None = None,
+                           dk_weight: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of qlora_qk_norm_rope's inputs from those of its outputs; q, k are the forward's inputs
+    (needed where there is a weight).  dq may be dq_out and dk may be dk_out.  Returns (dq, dk or None,
+    dq_weight or None, dk_weight or None), the weights' fp32 [head_dim]."""
+    gq = _heads(dq_out, "dq_out")
+    gk = None if dk_out is None else _heads(dk_out, "dk_out", dq_out.device,
+                                            (dq_out.shape[0], dk_out.shape[1], dq_out.shape[2]))
+    rows, dim, rot, dev = _qk_inputs(dq_out, dk_out, positions, inv_freq, q_weight, k_weight)
+    if (q_weight is not None and q is None) or (k_weight is not None and k is None):
+        raise QLoRAError("a weight's gradient needs the forward's input")
+    xq = _heads(q, "q", dev, tuple(dq_out.shape)) if q_weight is not None else None
+    xk = _heads(k, "k", dev, tuple(dk_out.shape)) if k_weight is not None else None
+    with _on(dq_out, stream) as on:
+        if dq is None:
+            dq = torch.empty(dq_out.shape, dtype=torch.bfloat16, device=dev)
+        if dk_out is not None and dk is None:
+            dk = torch.empty(dk_out.shape, dtype=torch.bfloat16, device=dev)
+        if q_weight is not None and dq_weight is None:
+            dq_weight = torch.empty(dim, dtype=torch.float32, device=dev)
+        if k_weight is not None and dk_weight is None:
+            dk_weight = torch.empty(dim, dtype=torch.float32, device=dev)
+        for w, name in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
+            if w is not None:
+                _need(w, torch.float32, dev, name, (dim,))
+        oq = _heads(dq, "dq", dev, tuple(dq_out.shape))
+        ok = None if dk is None else _heads(dk, "dk", dev, None if dk_out is None else tuple(dk_out.shape))
+        ws = None
+        if q_weight is not None or k_weight is not None:
+            ws = _bytes(workspace, qlora_qk_norm_rope_bwd_workspace(rows, gq.heads, 0 if gk is None else gk.heads, dim),
+                        dev)
+        _check(lib().qlora_qk_norm_rope_bwd(_ref(gq), _ref(gk), _ref(xq), _ref(xk), rows, dim, _ptr(q_weight),
+                                            _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), rot,
+                                            int(interleaved), _ref(oq), _ref(ok), _ptr(dq_weight), _ptr(dk_weight),
+                                            _ptr(ws), 0 if ws is None else ws.nbytes, on.ptr),
+               "qlora_qk_norm_rope_bwd")
+    return dq, dk, dq_weight, dk_weight
+
+
+def qlora_kv_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, batch: KVBatch, stream=None):
+    """Quantize the rows k, v [rows][heads][head_dim] (bf16, any strides) into the cache."""
+    dev = _same_device(cache, batch)
+    shape = (k.shape[0], cache.heads, cache.head_dim)
+    hk, hv = _heads(k, "k", dev, shape), _heads(v, "v", dev, shape)
+    with _on(k, stream) as on:
+        _check(lib().qlora_kv_write(_ref(hk), _ref(hv), shape[0], _ref(cache.desc()), _ref(batch.desc()), on.ptr),
+               "qlora_kv_write")
+
+
+def qlora_kv_read(cache: KVCache, batch: KVBatch, rows: int, k: torch.Tensor | None = None,
+                  v: torch.Tensor | None = None, stream=None):
+    """The batch's rows read back from the cache: (k, v) [rows][heads][head_dim] bf16.  Rows of no sequence
+    keep what k and v hold (undefined if they are not given)."""
+    dev = _same_device(cache, batch)
+    shape = (rows, cache.heads, cache.head_dim)
+    with _on(cache.k_codes, stream) as on:
+        if k is None:
+            k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        if v is None:
+            v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        hk, hv = _heads(k, "k", dev, shape), _heads(v, "v", dev, shape)
+        _check(lib().qlora_kv_read(_ref(cache.desc()), _ref(batch.desc()), rows, _ref(hk), _ref(hv), on.ptr),
+               "qlora_kv_read")
+    return k, v
+
+
+def qlora_kv_attn_workspace(cache: KVCache, batch: KVBatch, rows: int, q_heads: int) -> int:
+    return lib().qlora_kv_attn_workspace(_ref(cache.desc()), _ref(batch.desc()), rows, q_heads)
+
+
+def qlora_kv_attn(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float | None = None, causal: bool = True,
+                  window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | bool = False,
+                  workspace: torch.Tensor | None = None, stream=None):
+    """Attention of q [rows][q_heads][head_dim] (bf16, any strides) over the cache; scale defaults to
+    head_dim ** -0.5.  lse: True for a new fp32 [rows][q_heads], or a tensor to fill.  Returns (out, lse or
+    None).  Rows of no sequence keep what out and lse hold (undefined if they are not given)."""
+    dev = _same_device(cache, batch)
+    hq = _heads(q, "q", dev, (q.shape[0], q.shape[1], cache.head_dim))
+    rows, heads = q.shape[0], q.shape[1]
+    with _on(q, stream) as on:
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        if lse is True:
+            lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
+        elif lse is False:
+            lse = None
+        if lse is not None:
+            _need(lse, torch.float32, dev, "lse", (rows, heads))
+        ho = _heads(out, "out", dev, tuple(q.shape))
+        ws = _bytes(workspace, 0 if workspace is not None else qlora_kv_attn_workspace(cache, batch, rows, heads), dev)
+        _check(lib().qlora_kv_attn(_ref(hq), rows, _ref(cache.desc()), _ref(batch.desc()),
+                                   float(cache.head_dim ** -0.5 if scale is None else scale), int(causal), int(window),
+                                   _ref(ho), _ptr(lse), _ptr(ws), ws.nbytes, on.ptr), "qlora_kv_attn")
+    return out, lse
 
 
 def qlora_profile_enable(enable: bool = True):

@@ -36,6 +36,22 @@ class qlora_nf4(C.Structure):
     ]
 
 
+class qlora_heads(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("row_stride", C.c_int64), ("head_stride", C.c_int64), ("heads", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
+class qlora_kv_cache(C.Structure):
+    _fields_ = [("pages", C.c_int64), ("page_size", C.c_int32), ("heads", C.c_int32), ("head_dim", C.c_int32),
+                ("block_size", C.c_int32), ("codebook", C.c_int32), ("reserved", C.c_int32), ("k_codes", C.c_void_p),
+                ("k_scale", C.c_void_p), ("v_codes", C.c_void_p), ("v_scale", C.c_void_p)]
+
+
+class qlora_kv_batch(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("max_pages", C.c_int32), ("start", C.c_void_p), ("length", C.c_void_p),
+                ("table", C.c_void_p), ("fault", C.c_void_p)]
+
+
 class qlora_kernel_time(C.Structure):
     _fields_ = [("name", C.c_char * 48), ("launches", C.c_int64), ("total_ms", C.c_double)]
 
@@ -67,6 +83,25 @@ SIGNATURES = {
                                    C.c_size_t, C.c_void_p]),
     "qlora_state_page_out": (C.c_int, [C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
     "qlora_state_page_in": (C.c_int, [C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qlora_qk_norm_rope": (C.c_int, [C.POINTER(qlora_heads), C.POINTER(qlora_heads), C.c_int64, C.c_int32, C.c_void_p,
+                                     C.c_void_p, C.c_float, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
+                                     C.POINTER(qlora_heads), C.POINTER(qlora_heads), C.c_void_p]),
+    "qlora_qk_norm_rope_bwd_workspace": (C.c_size_t, [C.c_int64, C.c_int32, C.c_int32, C.c_int32]),
+    "qlora_qk_norm_rope_bwd": (C.c_int, [C.POINTER(qlora_heads), C.POINTER(qlora_heads), C.POINTER(qlora_heads),
+                                         C.POINTER(qlora_heads), C.c_int64, C.c_int32, C.c_void_p, C.c_void_p,
+                                         C.c_float, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
+                                         C.POINTER(qlora_heads), C.POINTER(qlora_heads), C.c_void_p, C.c_void_p,
+                                         C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qlora_kv_sizes": (C.c_int, [C.POINTER(qlora_kv_cache), C.POINTER(C.c_size_t), C.POINTER(C.c_size_t)]),
+    "qlora_kv_write": (C.c_int, [C.POINTER(qlora_heads), C.POINTER(qlora_heads), C.c_int64, C.POINTER(qlora_kv_cache),
+                                 C.POINTER(qlora_kv_batch), C.c_void_p]),
+    "qlora_kv_read": (C.c_int, [C.POINTER(qlora_kv_cache), C.POINTER(qlora_kv_batch), C.c_int64,
+                                C.POINTER(qlora_heads), C.POINTER(qlora_heads), C.c_void_p]),
+    "qlora_kv_attn_workspace": (C.c_size_t, [C.POINTER(qlora_kv_cache), C.POINTER(qlora_kv_batch), C.c_int64,
+                                             C.c_int32]),
+    "qlora_kv_attn": (C.c_int, [C.POINTER(qlora_heads), C.c_int64, C.POINTER(qlora_kv_cache),
+                                C.POINTER(qlora_kv_batch), C.c_float, C.c_int32, C.c_int32, C.POINTER(qlora_heads),
+                                C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
     "qlora_profile_enable": (C.c_int, [C.c_int32]),
     "qlora_profile_read": (C.c_int32, [C.POINTER(qlora_kernel_time), C.c_int32, C.c_int32]),
 }

@@ -11,6 +11,7 @@
 #include <string>
 #include <vector>
 
+#include "host.h"
 #include "kernels.h"
 #include "qlora.h"
 
@@ -67,24 +68,7 @@ namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 31;
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 inline int64_t rank_pad(int64_t r) { return (r + 63) / 64 * 64; }
-
-// Sequential carving of a workspace into 256-byte aligned pieces.
-struct Carve {
-  char* base;
-  size_t off = 0;
-  explicit Carve(void* b) : base(static_cast<char*>(b)) {}
-  template <class T>
-  T* take(size_t count) {
-    off = round_up(off, 256);
-    T* p = base ? reinterpret_cast<T*>(base + off) : nullptr;
-    off += count * sizeof(T);
-    return p;
-  }
-};
 
 // Weights per constant (0 in the descriptor means 64) and its log2; 0 for an unknown size.
 int block_of(int32_t b) { return b == 0 ? 64 : b; }
@@ -114,11 +98,6 @@ NF4View view_of(const qlora_nf4* w) {
   v.bshift = block_shift(w->block_size);
   return v;
 }
-
-#define QL_HIP(call)                              \
-  do {                                            \
-    if ((call) != hipSuccess) return QLORA_ERR_HIP; \
-  } while (0)
 
 qlora_status check_nf4(const qlora_nf4* w) {
   if (!w || !w->codes || !w->absmax) return QLORA_ERR_NULL;

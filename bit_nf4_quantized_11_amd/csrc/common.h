@@ -49,6 +49,13 @@ __host__ __device__ __forceinline__ int lut_bin(float x) {
   return (int)__builtin_floorf(y);
 }
 
+// Code of a normalized weight: the number of thresholds below x, read off the encoder's bin
+// table held in LDS as {threshold, base} pairs.
+__device__ __forceinline__ uint32_t lut_encode(float x, const float2* __restrict__ lut) {
+  const float2 e = lut[lut_bin(x)];
+  return __float_as_uint(e.y) + (x > e.x ? 1u : 0u);
+}
+
 // Describes a quantized weight inside kernels.
 struct NF4View {
   const uint8_t* codes;   // 32 bytes per 64 weights (code layout of qlora.h)

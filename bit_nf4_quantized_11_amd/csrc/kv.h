@@ -1,0 +1,107 @@
+// Device views of the head tensors, the 4-bit key/value cache and the batch description
+// (qlora_heads, qlora_kv_cache, qlora_kv_batch), and the internal launch interface of the kernels
+// behind them.  Launchers validate nothing: kv_api.cpp has already.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.h"
+#include "qlora.h"
+
+namespace qlora {
+
+// bf16 [rows][heads][head_dim]
+struct Heads {
+  uint16_t* data;
+  int64_t rs, hs;   // row and head strides in elements
+  int32_t n;        // heads
+};
+
+struct KvView {
+  uint8_t* kc;
+  uint16_t* ks;
+  uint8_t* vc;
+  uint16_t* vs;
+  int64_t pages;
+  int32_t heads;
+  int32_t pshift;   // log2 of the page size
+  int32_t cb;
+};
+
+struct BatchView {
+  const int32_t* start;
+  const int32_t* length;
+  const int32_t* table;
+  int32_t* fault;
+  int64_t rows;
+  int32_t batch;
+  int32_t max_pages;
+  int32_t max_len;   // max_pages << pshift
+};
+
+enum : int32_t { kFaultStart = 1, kFaultLength = 2, kFaultPage = 4 };
+constexpr uint32_t kBf16NaN = 0x7FC0u;
+
+#ifdef __HIPCC__
+__device__ __forceinline__ void raise_fault(const BatchView& b, int bit) {
+  if (b.fault) atomicOr(b.fault, bit);
+}
+
+// Dword position of dword e (elements 8e..8e+7) in a key row of D elements: e = 4k + g of its
+// section of 32 n elements sits at n g + k.
+template <int D>
+__device__ __forceinline__ int key_dword(int e) {
+  constexpr int N = D == 64 ? 2 : 4;
+  const int r = e & (4 * N - 1);
+  return (e & ~(4 * N - 1)) + (r & 3) * N + (r >> 2);
+}
+#endif
+
+// ---- head norms and rotation (qk_rope.hip) --------------------------------------------------
+struct QkArgs {
+  Heads q, k, qo, ko;             // inputs and outputs (backward: the gradients of the outputs and of the inputs)
+  Heads xq, xk;                   // backward: the forward's inputs
+  const uint16_t* wq;
+  const uint16_t* wk;
+  const int64_t* pos;
+  const float* freq;
+  int64_t rows;
+  float eps;
+  int32_t rot;
+  int32_t slices;                 // wave items per row
+  float* part;                    // backward: weight gradient partials [workgroup][2][D]
+};
+hipError_t launch_qk(const QkArgs& a, int D, bool interleaved, hipStream_t s);
+// workgroups of the backward launch = partial sums of each weight gradient
+int qk_bwd_grid(int64_t rows, int32_t q_heads, int32_t k_heads, int D);
+hipError_t launch_qk_bwd(const QkArgs& a, int D, bool interleaved, float* dwq, float* dwk, hipStream_t s);
+
+// ---- cache write and read (kv_cache.hip) ------------------------------------------------------
+hipError_t launch_kv_write(const Heads& k, const Heads& v, const KvView& c, const BatchView& b, int D, int block,
+                           hipStream_t s);
+hipError_t launch_kv_read(const Heads& k, const Heads& v, const KvView& c, const BatchView& b, int D, int block,
+                          hipStream_t s);
+
+// ---- attention over the cache (kv_attn.hip) -----------------------------------------------------
+struct AttnArgs {
+  Heads q, o;
+  float* lse;                     // [rows][q.n] or NULL
+  KvView c;
+  BatchView b;
+  int32_t group;                  // query heads per cache head
+  float scale;
+  int32_t causal, window;
+  float* part;                    // partial sums of ranges that end inside an item
+  int32_t* meta;                  // [workgroups][kMetaInts]
+};
+// Sizes of a launch, from what the host knows.
+struct AttnPlan {
+  int tile;                       // query rows per tile (row = token and query head of one cache head)
+  int64_t wgs;                    // workgroups of the ranges
+  size_t part_floats, meta_ints;
+};
+AttnPlan attn_plan(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t batch, int64_t max_len, int D);
+hipError_t launch_kv_attn(const AttnArgs& a, const AttnPlan& pl, int D, int block, hipStream_t s);
+
+}  // namespace qlora

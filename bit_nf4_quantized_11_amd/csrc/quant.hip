@@ -19,13 +19,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kQuantThreads = 1024;   // quantize workgroups: at most kQuantSlots of them
 
-// Code of a normalized weight: the number of thresholds below x, read off the encoder's bin
-// table (see ThrLut in common.h) held in LDS as {threshold, base} pairs.
-__device__ __forceinline__ uint32_t lut_encode(float x, const float2* __restrict__ lut) {
-  const float2 e = lut[lut_bin(x)];
-  return __float_as_uint(e.y) + (x > e.x ? 1u : 0u);
-}
-
 // L = block / 8 lanes per block, eight consecutive weights per lane (one 16-byte load, one
 // code dword).  Lane 0 of each group writes the fp32 block constant and, for double
 // quantization, adds its significand to a per-exponent histogram in LDS.  At the end the

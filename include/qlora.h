@@ -242,6 +242,140 @@ qlora_status qlora_adamw_step(float* param, uint16_t* param_bf16, const float* g
 qlora_status qlora_state_page_out(const void* device, void* host, size_t bytes, hipStream_t stream);
 qlora_status qlora_state_page_in(const void* host, void* device, size_t bytes, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Between the projections of a layer: norms and positions of the heads, the key/value cache in
+ * 4 bits, and the attention that reads it.
+ * ------------------------------------------------------------------------------------------- */
+
+/* A bf16 tensor [rows][heads][head_dim], as a projection leaves it: element (row, head, d) is
+ * data[row * row_stride + head * head_stride + d].  Strides in elements, multiples of 8, >= 0;
+ * data 16-byte aligned.  So the queries and keys of one joint projection are two views of one
+ * buffer, and [heads][rows][head_dim] is a view too.  An output's rows must not overlap: either
+ * head_stride >= head_dim and row_stride >= (heads - 1) * head_stride + head_dim, or row_stride >=
+ * head_dim and head_stride >= (rows - 1) * row_stride + head_dim (a stride that is never used, of
+ * one head or one row, may be anything).                                                          */
+typedef struct {
+  uint16_t* data;
+  int64_t row_stride;
+  int64_t head_stride;
+  int32_t heads;
+  int32_t reserved; /* 0 */
+} qlora_heads;
+
+/* Norm of every head of q and k over head_dim, then rotation by position, in one pass over memory:
+ *   u = x * w / sqrt(mean(x^2) + eps)          (u = x where the weight is NULL)
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = positions[row] * inv_freq[i],
+ * for the pairs i < rot_dim / 2: (u[i], u[i + rot_dim / 2]), or (u[2i], u[2i + 1]) with `interleaved`;
+ * elements from rot_dim on are not rotated.  fp32 arithmetic, angles reduced in float64, one rounding
+ * to bf16 at the end.  k may be NULL (then k_out too).
+ * Outputs may be the inputs themselves (same data and strides); they must not overlap otherwise.
+ * Requires: head_dim 64, 128 or 256; rot_dim % 16 == 0, 0 <= rot_dim <= head_dim; q_weight, k_weight
+ * bf16 [head_dim], 16-byte aligned; positions [rows], inv_freq [rot_dim / 2] (both may be NULL when
+ * rot_dim is 0); eps >= 0 and finite; 0 <= rows < 2^26; 1..1024 heads.  rows = 0 is a no-op.            */
+qlora_status qlora_qk_norm_rope(const qlora_heads* q, const qlora_heads* k, int64_t rows, int32_t head_dim,
+                                const uint16_t* q_weight, const uint16_t* k_weight, float eps,
+                                const int64_t* positions, const float* inv_freq, int32_t rot_dim,
+                                int32_t interleaved, const qlora_heads* q_out, const qlora_heads* k_out,
+                                hipStream_t stream);
+
+/* Its backward: from the gradients of the two outputs and the inputs q, k of the forward, the
+ * gradients of q, k and of the two weights (fp32 [head_dim], overwritten; summed in a fixed order):
+ *   g = rotation by -t of d_out;  d_weight = sum over rows and heads of g x r,  r = 1/sqrt(mean(x^2) + eps)
+ *   d_x = r (w g - x r^2 mean(w g x))          (d_x = g where the weight is NULL)
+ * Where a weight is NULL, its input (q or k) may be NULL and its weight gradient must be NULL.
+ * dq may be dq_out and dk may be dk_out (same data and strides); no other overlap.  With rows = 0 the
+ * weight gradients are set to zero.  ws of qlora_qk_norm_rope_bwd_workspace bytes (needed only with
+ * a weight).  dk_out NULL: no keys (k, dk, k_weight, dk_weight NULL too).                          */
+size_t qlora_qk_norm_rope_bwd_workspace(int64_t rows, int32_t q_heads, int32_t k_heads, int32_t head_dim);
+qlora_status qlora_qk_norm_rope_bwd(const qlora_heads* dq_out, const qlora_heads* dk_out, const qlora_heads* q,
+                                    const qlora_heads* k, int64_t rows, int32_t head_dim, const uint16_t* q_weight,
+                                    const uint16_t* k_weight, float eps, const int64_t* positions,
+                                    const float* inv_freq, int32_t rot_dim, int32_t interleaved,
+                                    const qlora_heads* dq, const qlora_heads* dk, float* dq_weight,
+                                    float* dk_weight, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* A key/value cache in 4 bits: caller-owned device buffers.  Pages of page_size tokens, any page of
+ * any sequence anywhere; the block format of qlora_nf4 along head_dim, with the block's absmax itself
+ * (a bf16 value, so exact) as its scale:
+ *   codes : [pages][heads][page_size][head_dim / 2] bytes, 8 elements to a dword in the nibble order of
+ *           qlora_nf4.  The dwords of a value row are in element order.  Those of a key row are
+ *           transposed in sections of 32 n elements (n = 4; 2 where head_dim is 64): dword n g + k of a
+ *           section holds its elements 8 (4 k + g) .. + 7, g < 4, k < n, so that the one load of a lane
+ *           brings what it feeds to n consecutive matrix instructions, each of which reduces over one
+ *           run of 32 elements (no run crosses a block).
+ *   scale : [pages][heads][page_size][head_dim / block_size] bf16.
+ * An element stands for level[code] * scale.  A block that holds an infinity or a NaN is stored with
+ * a NaN scale; one whose absmax is below 2^-126 as zeros.
+ * Requires: head_dim 64, 128 or 256; block_size 32, 64 or 128 (0 = 64), at most head_dim; page_size a
+ * power of two from 16 to 2^20; pages >= 1; heads 1..1024; buffers 16-byte aligned.                    */
+typedef struct {
+  int64_t pages;
+  int32_t page_size;
+  int32_t heads;
+  int32_t head_dim;
+  int32_t block_size;
+  int32_t codebook; /* qlora_codebook */
+  int32_t reserved; /* 0 */
+  uint8_t* k_codes;
+  uint16_t* k_scale;
+  uint8_t* v_codes;
+  uint16_t* v_scale;
+} qlora_kv_cache;
+
+/* Host only.  Bytes of one codes buffer and of one scale buffer of a cache. */
+qlora_status qlora_kv_sizes(const qlora_kv_cache* cache, size_t* codes_bytes, size_t* scale_bytes);
+
+/* Which tokens a call is about, for a batch of sequences (device arrays, read by the kernels, so a
+ * captured call follows their contents).  Rows start[b] .. start[b + 1] - 1 of the call's tensors are
+ * the last tokens of sequence b: with n = start[b + 1] - start[b], row start[b] + i is its position
+ * length[b] - n + i.  Position p lives in page table[b * max_pages + p / page_size], slot p % page_size.
+ * Rows that belong to no sequence (before start[0], from start[batch] on) are left alone.  A row with a
+ * negative position (length[b] < n) has no token: it is not written, reads zeros, attends nothing.
+ * The kernels check every entry and read and write nothing out of range; where one is wrong,
+ *   - a sequence whose start entries are out of order or past `rows`: its rows are left alone (bit 0);
+ *   - a length outside 0 .. max_pages * page_size: nothing is written, rows read and attend NaN (bit 1);
+ *   - a page outside 0 .. pages - 1: not written, reads NaN, every row that sees it attends NaN (bit 2);
+ * and the bit is OR-ed into *fault if that is not NULL (the caller clears it).
+ * Requires: batch 0..65536, max_pages >= 1, max_pages * page_size < 2^31, 4-byte aligned arrays.      */
+typedef struct {
+  int32_t batch;
+  int32_t max_pages;
+  const int32_t* start;  /* [batch + 1] */
+  const int32_t* length; /* [batch]     */
+  const int32_t* table;  /* [batch][max_pages] */
+  int32_t* fault;        /* NULL, or one word  */
+} qlora_kv_batch;
+
+/* Quantize the rows of k and v [rows][heads][head_dim] into the cache, at their positions.  Codes as
+ * qlora_quantize_nf4 gives them (a = max|x| of a block; nearest level of fl32(x fl32(1/a)), ties to the
+ * lower index).  No two rows of a call may share a slot (which of them a shared one would hold is not
+ * defined).  rows = 0 or batch = 0 is a no-op.  k.heads = v.heads = cache.heads.  rows < 2^26.           */
+qlora_status qlora_kv_write(const qlora_heads* k, const qlora_heads* v, int64_t rows, const qlora_kv_cache* cache,
+                            const qlora_kv_batch* batch, hipStream_t stream);
+
+/* The same rows read back: bf16_RNE(fl32(level[code] * scale)). */
+qlora_status qlora_kv_read(const qlora_kv_cache* cache, const qlora_kv_batch* batch, int64_t rows,
+                           const qlora_heads* k, const qlora_heads* v, hipStream_t stream);
+
+/* Attention of the rows of q [rows][q_heads][head_dim] over the cache (their own tokens already
+ * written):
+ *   o[row][h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q . k_j),
+ * over the positions j that row sees: j <= its own position (causal) or all below length[b], and with
+ * window > 0 (causal only) j > position - window.  Query head h reads cache head h / (q_heads / heads).
+ * A row that sees nothing gives zeros and lse = -infinity.  What a row does not see does not reach it,
+ * NaN included.  lse (or NULL): fp32 [rows][q_heads], the natural logarithm of sum_j p_j.
+ * bf16 products with fp32 accumulation; maximum, sum and output held in fp32; the levels (times a
+ * constant per codebook) and the probabilities (times the value scales) are rounded to bf16 for the
+ * matrix instructions.  Deterministic.
+ * Requires: q_heads a multiple of cache.heads, at most 1024; scale finite and > 0; window >= 0, 0 if not
+ * causal; o like q; ws of qlora_kv_attn_workspace bytes (which reads the sizes of `cache` and `batch`
+ * only, not their arrays).                                                                             */
+size_t qlora_kv_attn_workspace(const qlora_kv_cache* cache, const qlora_kv_batch* batch, int64_t rows,
+                               int32_t q_heads);
+qlora_status qlora_kv_attn(const qlora_heads* q, int64_t rows, const qlora_kv_cache* cache,
+                           const qlora_kv_batch* batch, float scale, int32_t causal, int32_t window,
+                           const qlora_heads* o, float* lse, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* Optional per-kernel timing, for benchmarking.  While enabled, every kernel
  * launch of this library is bracketed by HIP events on its stream.
  * qlora_profile_read synchronizes those events and returns, per kernel name,

@@ -218,3 +218,114 @@ def test_version_names_the_sources_it_was_built_from(lib):
 
     v = lib.qlora_version().decode()
     assert f"src {build.source_hash()})" in v, v
+
+
+# ---- head norms and rotation, the 4-bit cache, its attention --------------------------------------------
+def _hv(heads=4, data=0x100000, rs=None, hs=128, dim=128):
+    return _lib.qlora_heads(data, heads * dim if rs is None else rs, hs, heads, 0)
+
+
+def _cache(pages=4, page=16, heads=4, dim=128, block=64, cb=0, kc=0x1000, ks=0x2000, vc=0x3000, vs=0x4000):
+    return _lib.qlora_kv_cache(pages, page, heads, dim, block, cb, 0, kc, ks, vc, vs)
+
+
+def _batch(batch=2, max_pages=2, start=0x5000, length=0x6000, table=0x7000, fault=0):
+    return _lib.qlora_kv_batch(batch, max_pages, start, length, table, fault)
+
+
+def test_qk_norm_rope_validation(lib):
+    f = lambda q=_hv(), k=_hv(2), rows=3, dim=128, wq=0x9000, wk=0x9000, eps=1e-6, pos=0x8000, fr=0x8000, rot=128, \
+        inter=0, qo=_hv(), ko=_hv(2): lib.qlora_qk_norm_rope(
+            None if q is None else C.byref(q), None if k is None else C.byref(k), rows, dim, wq, wk, eps, pos, fr, rot,
+            inter, None if qo is None else C.byref(qo), None if ko is None else C.byref(ko), None)
+    assert f(rows=0) == 0
+    assert f(q=None) == 1 and f(qo=None) == 1 and f(k=None) == 1 and f(ko=None) == 1 and f(pos=None) == 1 and f(fr=None) == 1
+    assert f(q=_hv(data=0)) == 1
+    assert f(rows=-1) == 2 and f(rows=1 << 26) == 2 and f(rot=8) == 2 and f(rot=144) == 2 and f(rot=-16) == 2
+    assert f(q=_hv(0)) == 2 and f(q=_hv(1025)) == 2 and f(qo=_hv(3)) == 2 and f(q=_hv(hs=-8)) == 2
+    assert f(q=_hv(data=0x100008)) == 3 and f(q=_hv(hs=132)) == 3 and f(wq=0x9008) == 3 and f(pos=0x8004) == 3
+    for dim in (0, 32, 80, 96, 512):
+        assert f(dim=dim) == 4
+    assert f(inter=2) == 4
+    for eps in (-1.0, float("nan"), float("inf")):
+        assert f(eps=eps) == 4
+    # outputs whose rows overlap: neither row-major nor head-major
+    for o in (_hv(hs=120), _hv(rs=256, hs=128), _hv(rs=0), _hv(hs=0)):
+        assert f(qo=o) == 2
+        assert f(q=o, rows=0) == 0
+    assert lib.qlora_qk_norm_rope_bwd_workspace(16, 4, 2, 128) > 0
+    assert lib.qlora_qk_norm_rope_bwd_workspace(0, 4, 0, 64) > 0
+    for bad in ((-1, 4, 2, 128), (16, 0, 2, 128), (16, 4, -1, 128), (16, 4, 2, 96), (1 << 26, 4, 2, 128)):
+        assert lib.qlora_qk_norm_rope_bwd_workspace(*bad) == 0
+
+
+def test_qk_norm_rope_bwd_validation(lib):
+    need = lib.qlora_qk_norm_rope_bwd_workspace(3, 4, 2, 128)
+    f = lambda gq=_hv(), gk=_hv(2), q=_hv(), k=_hv(2), wq=0x9000, wk=0x9000, dq=_hv(), dk=_hv(2), dwq=0x9000, dwk=0x9000, \
+        ws=0xA000, n=need, dim=128: lib.qlora_qk_norm_rope_bwd(
+            *[None if x is None else C.byref(x) for x in (gq, gk, q, k)], 3, dim, wq, wk, 1e-6, 0x8000, 0x8000, 64, 0,
+            *[None if x is None else C.byref(x) for x in (dq, dk)], dwq, dwk, ws, n, None)
+    assert f(gq=None) == 1 and f(q=None) == 1 and f(k=None) == 1 and f(dq=None) == 1 and f(dk=None) == 1
+    assert f(dwq=None) == 1 and f(dwk=None) == 1 and f(wq=None) == 1            # a weight and its gradient go together
+    assert f(gk=None, dk=None) == 1                                             # keys' arguments without keys
+    assert f(q=_hv(3)) == 2 and f(dk=_hv(3)) == 2 and f(dq=_hv(hs=64)) == 2
+    assert f(dwq=0x9002) == 3 and f(ws=0xA008) == 3
+    assert f(dim=48) == 4
+    assert f(n=need - 1) == 5 and f(ws=None) == 5
+
+
+def test_kv_validation(lib):
+    ok = dict(k=_hv(), v=_hv(), rows=3, c=_cache(), b=_batch())
+
+    def call(fn, **kw):
+        a = {**ok, **kw}
+        r = {n: None if x is None else C.byref(x) for n, x in a.items() if n != "rows"}
+        if fn == "write":
+            return lib.qlora_kv_write(r["k"], r["v"], a["rows"], r["c"], r["b"], None)
+        return lib.qlora_kv_read(r["c"], r["b"], a["rows"], r["k"], r["v"], None)
+
+    for fn in ("write", "read"):
+        assert call(fn, rows=0) == 0 and call(fn, b=_batch(batch=0, start=0, length=0, table=0)) == 0
+        for n in "kvcb":
+            assert call(fn, **{n: None}) == 1
+        assert call(fn, c=_cache(kc=0)) == 1 and call(fn, c=_cache(vs=0)) == 1 and call(fn, k=_hv(data=0)) == 1
+        for n in ("start", "length", "table"):
+            assert call(fn, b=_batch(**{n: 0})) == 1 and call(fn, b=_batch(**{n: 0x5002})) == 3
+        assert call(fn, b=_batch(fault=0x5002)) == 3 and call(fn, c=_cache(ks=0x2008)) == 3
+        assert call(fn, k=_hv(3)) == 2 and call(fn, v=_hv(8)) == 2 and call(fn, rows=-1) == 2 and call(fn, rows=1 << 26) == 2
+        assert call(fn, c=_cache(pages=0)) == 2 and call(fn, c=_cache(heads=0)) == 2 and call(fn, c=_cache(pages=1 << 31)) == 2
+        assert call(fn, b=_batch(batch=-1)) == 2 and call(fn, b=_batch(batch=65537)) == 2
+        assert call(fn, b=_batch(max_pages=0)) == 2 and call(fn, b=_batch(max_pages=1 << 27)) == 2
+        for c in (_cache(dim=32), _cache(dim=96), _cache(block=16), _cache(block=256), _cache(dim=64, block=128), _cache(cb=3),
+                  _cache(cb=-1), _cache(page=8), _cache(page=48), _cache(page=1 << 21), _cache(page=0)):
+            assert call(fn, c=c) == 4
+    assert call("read", k=_hv(hs=64)) == 2                                      # outputs that overlap
+    a, s = C.c_size_t(), C.c_size_t()
+    assert lib.qlora_kv_sizes(C.byref(_cache(kc=0)), C.byref(a), C.byref(s)) == 0
+    assert (a.value, s.value) == (4 * 4 * 16 * 64, 4 * 4 * 16 * 2 * 2)
+    assert lib.qlora_kv_sizes(C.byref(_cache(block=0)), None, C.byref(s)) == 0 and s.value == 1024   # 0 means 64
+    assert lib.qlora_kv_sizes(None, None, None) == 1 and lib.qlora_kv_sizes(C.byref(_cache(dim=100)), None, None) == 4
+
+
+def test_kv_attn_validation(lib):
+    c, b = _cache(), _batch()
+    need = lib.qlora_kv_attn_workspace(C.byref(c), C.byref(b), 3, 8)
+    assert need > 0 and need % 256 == 0
+    assert lib.qlora_kv_attn_workspace(C.byref(c), C.byref(b), 0, 8) > 0
+    # the query reads sizes alone
+    assert lib.qlora_kv_attn_workspace(C.byref(_cache(kc=0, vs=0)), C.byref(_batch(start=0, table=0)), 3, 8) == need
+    for bad in ((c, b, -1, 8), (c, b, 3, 6), (c, b, 3, 0), (_cache(dim=80), b, 3, 8), (c, _batch(max_pages=0), 3, 8),
+                (c, b, (1 << 26) - 1, 1024)):
+        assert lib.qlora_kv_attn_workspace(C.byref(bad[0]), C.byref(bad[1]), *bad[2:]) == 0
+    f = lambda q=_hv(8), rows=3, c=c, b=b, scale=0.1, causal=1, window=0, o=_hv(8), lse=None, ws=0xA000, n=need: \
+        lib.qlora_kv_attn(None if q is None else C.byref(q), rows, None if c is None else C.byref(c),
+                          None if b is None else C.byref(b), scale, causal, window, None if o is None else C.byref(o), lse,
+                          ws, n, None)
+    assert f(rows=0) == 0 and f(b=_batch(batch=0)) == 0
+    assert f(q=None) == 1 and f(c=None) == 1 and f(b=None) == 1 and f(o=None) == 1 and f(b=_batch(table=0)) == 1
+    assert f(q=_hv(6)) == 2 and f(o=_hv(4)) == 2 and f(window=-1) == 2 and f(o=_hv(8, hs=64)) == 2
+    assert f(lse=0x1002) == 3 and f(ws=0xA008) == 3 and f(q=_hv(8, data=0x100004)) == 3
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        assert f(scale=scale) == 4
+    assert f(causal=2) == 4 and f(causal=0, window=5) == 4 and f(c=_cache(dim=192)) == 4
+    assert f(n=need - 1) == 5 and f(ws=None) == 5
