@@ -272,64 +272,50 @@ def qlora_state_page_in(host: torch.Tensor, dev: torch.Tensor, stream=None) -> t
 
 
 # ---- between the projections: head norms and rotation, the 4-bit key/value cache, its attention --------
-class _on:
-    """The device a call's tensors live on, its stream, and (in `ptr`) the stream's handle.  Everything
-    the call allocates belongs to that stream, so it is not reused before the kernels are done."""
-
-    def __init__(self, t: torch.Tensor, stream):
-        self.device = t.device
-        self.stream = stream
-        self.guards = []
-
-    def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(self.device))
-            self.guards[-1].__enter__()
-        if self.stream is None:
-            self.stream = torch.cuda.current_stream(self.device)
-        else:
-            if self.stream.device != self.device:
-                for g in reversed(self.guards):
-                    g.__exit__(None, None, None)
-                raise QLoRAError(f"the stream is on {self.stream.device}, the tensors on {self.device}")
-            self.guards.append(torch.cuda.stream(self.stream))
-            self.guards[-1].__enter__()
-        self.ptr = C.c_void_p(self.stream.cuda_stream)
-        return self
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+# These calls' kernels can take less time than a few lines of Python, so what every call does is kept short: the
+# stream's handle alone (a torch Stream object costs 2 us to make), and no context where none is needed.
+def _launch(t: torch.Tensor, stream, run):
+    """run(handle of the stream), with the tensor's device current and, where the caller named a stream, that
+    stream current too, so that what `run` allocates belongs to it and is not reused before its kernels are done."""
+    dev = t.device
+    index = dev.index
+    if stream is None and index == torch._C._cuda_getDevice():
+        return run(C.c_void_p(torch._C._cuda_getCurrentRawStream(index)))
+    if stream is not None and stream.device != dev:
+        raise QLoRAError(f"the stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return run(C.c_void_p(torch._C._cuda_getCurrentRawStream(index)))
 
 
 def _need(t, dtype, device, name, shape=None):
     """A contiguous tensor of `dtype` on `device` (and of `shape`)."""
-    if t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise QLoRAError(f"{name} must be a contiguous {dtype} tensor on {device}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise QLoRAError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
+    if shape is not None and t.shape != shape:
+        raise QLoRAError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
     return t
 
 
 def _heads(t: torch.Tensor, name: str, device=None, shape=None) -> _lib.qlora_heads:
     """The view of a bf16 [rows][heads][head_dim] tensor, any strides with a dense last dimension."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+    strides = t.stride()
+    if t.dtype is not torch.bfloat16 or len(strides) != 3 or strides[2] != 1 or not t.is_cuda:
         raise QLoRAError(f"{name} must be a bf16 [rows][heads][head_dim] tensor on the GPU, dense along head_dim")
     if device is not None and t.device != device:
         raise QLoRAError(f"{name} must be on {device}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise QLoRAError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
-    return _lib.qlora_heads(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1], 0)
+    if shape is not None and t.shape != shape:
+        raise QLoRAError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    return _lib.qlora_heads(t.data_ptr(), strides[0], strides[1], t.shape[1], 0)
 
 
 def _ref(x):
     return None if x is None else C.byref(x)
 
 
-def _bytes(ws, nbytes: int, device):
-    """The caller's workspace, checked, or a new one."""
+def _bytes(ws, device, need):
+    """The caller's workspace, checked, or a new one of need() bytes."""
     if ws is None:
-        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+        return torch.empty(max(need(), 1), dtype=torch.uint8, device=device)
     if ws.device != device or not ws.is_contiguous():
         raise QLoRAError(f"workspace must be a contiguous tensor on {device}")
     return ws
@@ -357,26 +343,13 @@ class KVCache:
         _need(self.v_codes, torch.uint8, c.device, "v_codes", tuple(c.shape))
         _need(self.k_scale, torch.bfloat16, c.device, "k_scale", scales)
         _need(self.v_scale, torch.bfloat16, c.device, "v_scale", scales)
-        # the fields are frozen, so the descriptor is made once
+        # the fields are frozen, so the descriptor and the sizes are taken once
+        for name, value in (("pages", pages), ("heads", heads), ("page_size", page_size), ("head_dim", 2 * half),
+                            ("device", c.device)):
+            object.__setattr__(self, name, value)
         object.__setattr__(self, "_desc", _lib.qlora_kv_cache(
             pages, page_size, heads, 2 * half, int(self.block), int(self.codebook), 0, self.k_codes.data_ptr(),
             self.k_scale.data_ptr(), self.v_codes.data_ptr(), self.v_scale.data_ptr()))
-
-    @property
-    def pages(self) -> int:
-        return self.k_codes.shape[0]
-
-    @property
-    def heads(self) -> int:
-        return self.k_codes.shape[1]
-
-    @property
-    def page_size(self) -> int:
-        return self.k_codes.shape[2]
-
-    @property
-    def head_dim(self) -> int:
-        return 2 * self.k_codes.shape[3]
 
     def desc(self) -> _lib.qlora_kv_cache:
         return self._desc
@@ -423,6 +396,7 @@ class KVBatch:
         _need(self.table, torch.int32, dev, "table", (n, self.table.shape[1]))
         if self.fault is not None:
             _need(self.fault, torch.int32, dev, "fault", (1,))
+        object.__setattr__(self, "device", dev)
         object.__setattr__(self, "_desc", _lib.qlora_kv_batch(
             n, self.table.shape[1], self.start.data_ptr(), self.length.data_ptr(), self.table.data_ptr(),
             None if self.fault is None else self.fault.data_ptr()))
@@ -432,9 +406,9 @@ class KVBatch:
 
 
 def _same_device(cache: KVCache, batch: KVBatch):
-    if cache.k_codes.device != batch.length.device:
+    if cache.device != batch.device:
         raise QLoRAError("the cache and the batch must be on one device")
-    return cache.k_codes.device
+    return cache.device
 
 
 def _qk_inputs(q, k, positions, inv_freq, q_weight, k_weight):
@@ -466,17 +440,20 @@ def qlora_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch
     hq = _heads(q, "q")
     hk = None if k is None else _heads(k, "k", q.device, (q.shape[0], k.shape[1], q.shape[2]))
     rows, dim, rot, dev = _qk_inputs(q, k, positions, inv_freq, q_weight, k_weight)
-    with _on(q, stream) as on:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
-        oq = _heads(q_out, "q_out", dev, tuple(q.shape))
-        ok = None if k_out is None else _heads(k_out, "k_out", dev, None if k is None else tuple(k.shape))
-        _check(lib().qlora_qk_norm_rope(_ref(hq), _ref(hk), rows, dim, _ptr(q_weight), _ptr(k_weight), float(eps),
-                                        _ptr(positions), _ptr(inv_freq), rot, int(interleaved), _ref(oq), _ref(ok),
-                                        on.ptr), "qlora_qk_norm_rope")
-    return q_out, k_out
+    if k is None and k_out is not None:
+        raise QLoRAError("k_out needs k")
+
+    def run(stream):
+        qo = q.new_empty(q.shape) if q_out is None else q_out
+        ko = k_out if k is None or k_out is not None else k.new_empty(k.shape)
+        oq = _heads(qo, "q_out", dev, q.shape)
+        ok = None if k is None else _heads(ko, "k_out", dev, k.shape)
+        _check(lib().qlora_qk_norm_rope(_ref(hq), _ref(hk), rows, dim, _ptr(q_weight), _ptr(k_weight), eps,
+                                        _ptr(positions), _ptr(inv_freq), rot, interleaved, _ref(oq), _ref(ok), stream),
+               "qlora_qk_norm_rope")
+        return qo, ko
+
+    return _launch(q, stream, run)
 
 
 def qlora_qk_norm_rope_bwd_workspace(rows: int, q_heads: int, k_heads: int, head_dim: int) -> int:
@@ -498,32 +475,36 @@ def qlora_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q:
     rows, dim, rot, dev = _qk_inputs(dq_out, dk_out, positions, inv_freq, q_weight, k_weight)
     if (q_weight is not None and q is None) or (k_weight is not None and k is None):
         raise QLoRAError("a weight's gradient needs the forward's input")
-    xq = _heads(q, "q", dev, tuple(dq_out.shape)) if q_weight is not None else None
-    xk = _heads(k, "k", dev, tuple(dk_out.shape)) if k_weight is not None else None
-    with _on(dq_out, stream) as on:
-        if dq is None:
-            dq = torch.empty(dq_out.shape, dtype=torch.bfloat16, device=dev)
-        if dk_out is not None and dk is None:
-            dk = torch.empty(dk_out.shape, dtype=torch.bfloat16, device=dev)
-        if q_weight is not None and dq_weight is None:
-            dq_weight = torch.empty(dim, dtype=torch.float32, device=dev)
-        if k_weight is not None and dk_weight is None:
-            dk_weight = torch.empty(dim, dtype=torch.float32, device=dev)
-        for w, name in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
-            if w is not None:
-                _need(w, torch.float32, dev, name, (dim,))
-        oq = _heads(dq, "dq", dev, tuple(dq_out.shape))
-        ok = None if dk is None else _heads(dk, "dk", dev, None if dk_out is None else tuple(dk_out.shape))
+    xq = _heads(q, "q", dev, dq_out.shape) if q_weight is not None else None
+    xk = _heads(k, "k", dev, dk_out.shape) if k_weight is not None else None
+    if dk_out is None and dk is not None:
+        raise QLoRAError("dk needs dk_out")
+    if (q_weight is None and dq_weight is not None) or (k_weight is None and dk_weight is not None):
+        raise QLoRAError("a weight's gradient needs the weight")
+
+    def run(stream):
+        oq = dq_out.new_empty(dq_out.shape) if dq is None else dq
+        ok = dk if dk_out is None or dk is not None else dk_out.new_empty(dk_out.shape)
+        gwq, gwk = dq_weight, dk_weight
+        if q_weight is not None:
+            gwq = torch.empty(dim, dtype=torch.float32, device=dev) if gwq is None else \
+                _need(gwq, torch.float32, dev, "dq_weight", (dim,))
+        if k_weight is not None:
+            gwk = torch.empty(dim, dtype=torch.float32, device=dev) if gwk is None else \
+                _need(gwk, torch.float32, dev, "dk_weight", (dim,))
+        hq = _heads(oq, "dq", dev, dq_out.shape)
+        hk = None if dk_out is None else _heads(ok, "dk", dev, dk_out.shape)
         ws = None
         if q_weight is not None or k_weight is not None:
-            ws = _bytes(workspace, qlora_qk_norm_rope_bwd_workspace(rows, gq.heads, 0 if gk is None else gk.heads, dim),
-                        dev)
+            ws = _bytes(workspace, dev, lambda: qlora_qk_norm_rope_bwd_workspace(
+                rows, gq.heads, 0 if gk is None else gk.heads, dim))
         _check(lib().qlora_qk_norm_rope_bwd(_ref(gq), _ref(gk), _ref(xq), _ref(xk), rows, dim, _ptr(q_weight),
-                                            _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), rot,
-                                            int(interleaved), _ref(oq), _ref(ok), _ptr(dq_weight), _ptr(dk_weight),
-                                            _ptr(ws), 0 if ws is None else ws.nbytes, on.ptr),
-               "qlora_qk_norm_rope_bwd")
-    return dq, dk, dq_weight, dk_weight
+                                            _ptr(k_weight), eps, _ptr(positions), _ptr(inv_freq), rot, interleaved,
+                                            _ref(hq), _ref(hk), _ptr(gwq), _ptr(gwk), _ptr(ws),
+                                            0 if ws is None else ws.nbytes, stream), "qlora_qk_norm_rope_bwd")
+        return oq, ok, gwq, gwk
+
+    return _launch(dq_out, stream, run)
 
 
 def qlora_kv_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, batch: KVBatch, stream=None):
@@ -531,9 +512,9 @@ def qlora_kv_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, batch: KVBa
     dev = _same_device(cache, batch)
     shape = (k.shape[0], cache.heads, cache.head_dim)
     hk, hv = _heads(k, "k", dev, shape), _heads(v, "v", dev, shape)
-    with _on(k, stream) as on:
-        _check(lib().qlora_kv_write(_ref(hk), _ref(hv), shape[0], _ref(cache.desc()), _ref(batch.desc()), on.ptr),
-               "qlora_kv_write")
+    _launch(k, stream, lambda stream: _check(
+        lib().qlora_kv_write(_ref(hk), _ref(hv), shape[0], _ref(cache.desc()), _ref(batch.desc()), stream),
+        "qlora_kv_write"))
 
 
 def qlora_kv_read(cache: KVCache, batch: KVBatch, rows: int, k: torch.Tensor | None = None,
@@ -542,15 +523,16 @@ def qlora_kv_read(cache: KVCache, batch: KVBatch, rows: int, k: torch.Tensor | N
     keep what k and v hold (undefined if they are not given)."""
     dev = _same_device(cache, batch)
     shape = (rows, cache.heads, cache.head_dim)
-    with _on(cache.k_codes, stream) as on:
-        if k is None:
-            k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        if v is None:
-            v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        hk, hv = _heads(k, "k", dev, shape), _heads(v, "v", dev, shape)
-        _check(lib().qlora_kv_read(_ref(cache.desc()), _ref(batch.desc()), rows, _ref(hk), _ref(hv), on.ptr),
+
+    def run(stream):
+        ko = cache.k_scale.new_empty(shape) if k is None else k
+        vo = cache.k_scale.new_empty(shape) if v is None else v
+        hk, hv = _heads(ko, "k", dev, shape), _heads(vo, "v", dev, shape)
+        _check(lib().qlora_kv_read(_ref(cache.desc()), _ref(batch.desc()), rows, _ref(hk), _ref(hv), stream),
                "qlora_kv_read")
-    return k, v
+        return ko, vo
+
+    return _launch(cache.k_codes, stream, run)
 
 
 def qlora_kv_attn_workspace(cache: KVCache, batch: KVBatch, rows: int, q_heads: int) -> int:
@@ -566,21 +548,22 @@ def qlora_kv_attn(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float 
     dev = _same_device(cache, batch)
     hq = _heads(q, "q", dev, (q.shape[0], q.shape[1], cache.head_dim))
     rows, heads = q.shape[0], q.shape[1]
-    with _on(q, stream) as on:
-        if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+
+    def run(stream):
+        o = q.new_empty(q.shape) if out is None else out
+        ho = _heads(o, "out", dev, q.shape)
+        sums = None
         if lse is True:
-            lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
-        elif lse is False:
-            lse = None
-        if lse is not None:
-            _need(lse, torch.float32, dev, "lse", (rows, heads))
-        ho = _heads(out, "out", dev, tuple(q.shape))
-        ws = _bytes(workspace, 0 if workspace is not None else qlora_kv_attn_workspace(cache, batch, rows, heads), dev)
+            sums = torch.empty((rows, heads), dtype=torch.float32, device=dev)
+        elif lse is not False and lse is not None:
+            sums = _need(lse, torch.float32, dev, "lse", (rows, heads))
+        ws = _bytes(workspace, dev, lambda: qlora_kv_attn_workspace(cache, batch, rows, heads))
         _check(lib().qlora_kv_attn(_ref(hq), rows, _ref(cache.desc()), _ref(batch.desc()),
-                                   float(cache.head_dim ** -0.5 if scale is None else scale), int(causal), int(window),
-                                   _ref(ho), _ptr(lse), _ptr(ws), ws.nbytes, on.ptr), "qlora_kv_attn")
-    return out, lse
+                                   cache.head_dim ** -0.5 if scale is None else scale, causal, window, _ref(ho),
+                                   _ptr(sums), _ptr(ws), ws.nbytes, stream), "qlora_kv_attn")
+        return o, sums
+
+    return _launch(q, stream, run)
 
 
 def qlora_profile_enable(enable: bool = True):

@@ -92,12 +92,14 @@ struct AttnArgs {
   int32_t group;                  // query heads per cache head
   float scale;
   int32_t causal, window;
+  int32_t ushift;                 // log2 of the unit of work in steps of every wave
   float* part;                    // partial sums of ranges that end inside an item
   int32_t* meta;                  // [workgroups][kMetaInts]
 };
 // Sizes of a launch, from what the host knows.
 struct AttnPlan {
   int tile;                       // query rows per tile (row = token and query head of one cache head)
+  int ushift;
   int64_t wgs;                    // workgroups of the ranges
   size_t part_floats, meta_ints;
 };

@@ -52,6 +52,8 @@ qlora_status check_cache_sizes(const qlora_kv_cache* c) {
   if (c->codebook < 0 || c->codebook >= kNumCodebooks) return QLORA_ERR_UNSUPPORTED;
   if (c->page_size < 16 || c->page_size > (1 << 20) || (c->page_size & (c->page_size - 1))) return QLORA_ERR_UNSUPPORTED;
   if (c->heads < 1 || c->heads > kMaxHeads || c->pages < 1 || c->pages >= (int64_t(1) << 31)) return QLORA_ERR_SHAPE;
+  // a page's offsets are 32-bit
+  if ((int64_t)c->heads * c->page_size * c->head_dim >= (int64_t(1) << 32)) return QLORA_ERR_SHAPE;
   return QLORA_OK;
 }
 
@@ -141,7 +143,9 @@ qlora_status check_attn_sizes(const qlora_kv_cache* c, const qlora_kv_batch* b, 
   if ((st = check_batch_sizes(b, c)) != QLORA_OK) return st;
   if (rows < 0 || rows >= kMaxRows || q_heads < 1 || q_heads > kMaxHeads || q_heads % c->heads != 0)
     return QLORA_ERR_SHAPE;
-  if (rows * (q_heads / c->heads) >= (int64_t(1) << 30)) return QLORA_ERR_SHAPE;   // rows of one cache head: 32-bit indexes
+  // rows of one cache head, and their tiles of 16 over all heads: 32-bit indexes
+  const int64_t rows_h = rows * (q_heads / c->heads);
+  if (rows_h >= (int64_t(1) << 30) || (rows_h / 16 + 1 + b->batch) * c->heads >= (int64_t(1) << 29)) return QLORA_ERR_SHAPE;
   return QLORA_OK;
 }
 

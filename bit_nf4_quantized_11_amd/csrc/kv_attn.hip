@@ -21,8 +21,12 @@
 //     (ds_read_b64_tr_b4: a lane gets 16 tokens of one element), so 4 bits per element cross LDS instead
 //     of 16; the scale of a value depends on the token, the reduction index here, so it is multiplied
 //     into P, once per block.
-// The tables hold level * kLevelScale: FP4 (x 6) and Int4 (x 7) levels are then exact in bf16, NF4's
-// (x 1.43675) off by 2^-10.2 rms instead of 2^-9.5.
+// The products are in fp16, not bf16: its 11 bits bring the level tables (times 6 for FP4 and 7 for Int4, which
+// makes them exact) and the probabilities 8 times closer, and the output's error down to little more than
+// its own rounding to bf16 (with bf16 operands it was twice that).  What fp16 lacks is range, so every operand is
+// brought to about 1 by a power of two first: a row of q by its own largest element (all 8 bits of elements down to
+// 2^-17 of it stay), the scaled probabilities of a step by the largest scale so far of that
+// block of elements (a running exponent, like the running maximum, that all rows share).
 #include "kernels.h"
 #include "kv.h"
 
@@ -32,14 +36,67 @@ namespace {
 
 constexpr int AT = 256, AW = AT / 64;
 constexpr int kStep = 64;              // tokens per wave step
-constexpr int kUnit = kStep * AW;      // tokens per unit of work
+constexpr int kUnitShift = 8;          // log2 of the tokens per unit of work: one step of every wave
+static_assert(kStep * AW == 1 << kUnitShift, "a unit is one step of every wave");
 constexpr int kMetaInts = 8;
+// Waves per SIMD, and the workgroups of a launch: as many as are resident then.  The registers of a step's loads,
+// operands and sums decide: D = 64 fits three without spilling (16 sequences of 16 k tokens, 8 cache heads: 45 us, 48
+// with two waves), 128 and 256 two (82 and 153 us; 84 and 348 with three and the spills, 98 and 184 with one).
+template <int D>
+constexpr int kWaves = D == 64 ? 3 : 2;
+constexpr int64_t kCUs = 256;
+int64_t resident_wgs(int D) { return kCUs * (D == 64 ? kWaves<64> : kWaves<128>); }
+
+// Probabilities are held times 2^13 (with a scale, up to twice its power of two, below fp16's 65504), so that ones
+// down to 2^-27 of the largest keep all their bits and ones below 2^-38 of it are lost.
+constexpr float kPBits = 13.0f;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
+// The 16 levels times c in fp16, in the two forms that codes are decoded by.
+//   pair: a byte of codes is looked up in a table of 256 pairs in LDS (one dword: its low nibble's level, its
+//     high nibble's): 1 VALU and 1 LDS instruction for 2 elements.
+//   planes: byte permutes.  v_perm_b32 picks 4 bytes out of 8 by selectors 0..7; its selectors 8..15 give constants
+//     (the sign of byte 1, 3, 5 or 7 for 8..11, then 0, 0xFF, 0xFF, 0xFF).  So the low 8 entries of a byte plane
+//     looked up by the code and the high 8 by the code ^ 8 each give, for the codes that are not theirs, a constant
+//     of the code, which is xored into the tables beforehand: 2 permutes and a xor per plane of 4 codes, and 2 permutes
+//     to interleave the planes: 21 VALU for 8 elements.
 struct CodePlanes {
-  uint32_t lo[4], hi[4];   // as Planes: bytes of bf16(level * kLevelScale)
-  float inv;               // 1 / kLevelScale
+  uint32_t lo[4], hi[4];   // [0..1] entries 0..7, [2..3] entries 8..15 of the low and the high bytes
+  float inv;               // 1 / c
 };
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ f32x4 mfma16h(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+// two fp32 -> fp16, round to nearest even
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const f32x2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, a) * __builtin_bit_cast(f16x2, b));
+}
+__device__ __forceinline__ u32x4 decode_planes(const CodePlanes& p, uint32_t w) {
+  u32x4 o;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {   // elements 0..3 in the low nibbles, 4..7 in the high ones
+    const uint32_t a = (half ? w >> 4 : w) & 0x0F0F0F0Fu, b = a ^ 0x08080808u;
+    const uint32_t lo = __builtin_amdgcn_perm(p.lo[1], p.lo[0], a) ^ __builtin_amdgcn_perm(p.lo[3], p.lo[2], b);
+    const uint32_t hi = __builtin_amdgcn_perm(p.hi[1], p.hi[0], a) ^ __builtin_amdgcn_perm(p.hi[3], p.hi[2], b);
+    o[2 * half] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
+    o[2 * half + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+  }
+  return o;
+}
+// elements in the order 0, 4, 1, 5, 2, 6, 3, 7 (byte i holds i and i + 4)
+__device__ __forceinline__ u32x4 decode_pairs(const uint32_t* pair, uint32_t w) {
+  return u32x4{pair[w & 0xFFu], pair[(w >> 8) & 0xFFu], pair[(w >> 16) & 0xFFu], pair[w >> 24]};
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 <= e <= 127
+// exponent of a bf16 magnitude, kept where its power of two and the inverse are ordinary numbers
+__device__ __forceinline__ int exponent_of(uint32_t mag) { return min(max((int)(mag >> 7) - 127, -100), 126); }
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
@@ -59,6 +116,21 @@ __device__ __forceinline__ float group_sum(float v) {
   u = __float_as_uint(m);
   auto b = __builtin_amdgcn_permlane16_swap(u, u, false, false);
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = dpp_max<0xB1>(v);    // quad_perm [1, 0, 3, 2]
+  v = dpp_max<0x4E>(v);    // quad_perm [2, 3, 0, 1]
+  v = dpp_max<0x141>(v);   // row_half_mirror
+  v = dpp_max<0x140>(v);   // row_mirror
+  auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  v = max(a[0], a[1]);
+  auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return __builtin_amdgcn_readfirstlane(max(b[0], b[1]));
 }
 
 // Sequence b as a call sees it.
@@ -88,7 +160,8 @@ __device__ __forceinline__ int units_of(const AttnArgs& a, const Seq& s) {
     const int64_t w = (int64_t)a.window + tokens + kStep;
     if (w < span) span = w;
   }
-  const int u = (int)((span + kUnit - 1) / kUnit);
+  const int shift = kUnitShift + a.ushift;
+  const int u = (int)((span + (int64_t(1) << shift) - 1) >> shift);
   return u > 0 ? u : 1;
 }
 template <int TR>
@@ -96,28 +169,56 @@ __device__ __forceinline__ int tiles_of(const AttnArgs& a, const Seq& s) {
   return (int)(((int64_t)s.n * a.group + TR - 1) / TR);
 }
 
-// Prefix sums of the units of 256 sequences from c0 on: pre[i] = units before sequence c0 + i.
+// The same value, but what is computed from it is not moved to before this point: addresses of code outside a loop,
+// formed ahead of it, would be held in registers all through it (50 of them, here).
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// 256 sequences from c0 on: what the kernel needs of them, and the units before each.
+struct SeqTable {
+  int32_t pre[AT + 1];
+  int32_t row0[AT], n[AT], len[AT];
+  int32_t wave_tot[AW];
+};
 template <int TR>
-__device__ void scan_units(const AttnArgs& a, int c0, int64_t base, int64_t* pre, int64_t* wave_tot) {
-  const int t = threadIdx.x, i = c0 + t, lane = t & 63, w = t >> 6;
-  int64_t u = 0;
+__device__ void scan_units(const AttnArgs& a, int c0, int base, SeqTable& q) {
+  const int t = opaque(threadIdx.x), i = c0 + t, lane = t & 63, w = t >> 6;
+  int u = 0;
   if (i < a.b.batch) {
     const Seq s = seq_of(a.b, i);
-    u = (int64_t)tiles_of<TR>(a, s) * units_of<TR>(a, s) * a.c.heads;
+    u = tiles_of<TR>(a, s) * units_of<TR>(a, s) * a.c.heads;
+    q.row0[t] = (int)s.row0;
+    q.n[t] = s.n;
+    q.len[t] = s.len;
   }
-  int64_t inc = u;
+  int inc = u;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
-    const int64_t o = __shfl_up(inc, off, 64);
+    const int o = __shfl_up(inc, off, 64);
     if (lane >= off) inc += o;
   }
-  if (lane == 63) wave_tot[w] = inc;
+  if (lane == 63) q.wave_tot[w] = inc;
   __syncthreads();
-  for (int k = 0; k < w; ++k) inc += wave_tot[k];
-  pre[t + 1] = base + inc;
-  if (t == 0) pre[0] = base;
+#pragma unroll
+  for (int k = 0; k < AW - 1; ++k)
+    if (k < w) inc += q.wave_tot[k];
+  q.pre[t + 1] = base + inc;
+  if (t == 0) q.pre[0] = base;
   __syncthreads();
 }
+
+// Units 0 .. total - 1 in W <= total ranges as even as can be, the first total % W of them one longer.
+struct Ranges {
+  uint32_t len, more;
+  __device__ __forceinline__ Ranges(uint32_t total, uint32_t W) : len(total / W), more(total - total / W * W) {}
+  __device__ __forceinline__ uint32_t first(uint32_t w) const { return w * len + min(w, more); }
+  __device__ __forceinline__ uint32_t of(uint32_t unit) const {   // the range that holds a unit
+    const uint32_t border = more * (len + 1);
+    return unit < border ? unit / (len + 1) : more + (unit - border) / len;
+  }
+};
 
 // The tile of a segment, in registers that are the same in every lane.
 struct Tile {
@@ -145,6 +246,15 @@ __device__ __forceinline__ Tile tile_of(const AttnArgs& a, const Seq& s, int b, 
   return t;
 }
 
+// A step's four page entries (16 tokens each) as scalars.
+struct Pages {
+  int p[4];
+};
+__device__ __forceinline__ Pages pages_of(int pid) {
+  return Pages{{__builtin_amdgcn_readlane(pid, 0), __builtin_amdgcn_readlane(pid, 16), __builtin_amdgcn_readlane(pid, 32),
+                __builtin_amdgcn_readlane(pid, 48)}};
+}
+
 // Registers of one step's loads.
 template <int D, int NB>
 struct StepLoads {
@@ -156,47 +266,44 @@ struct StepLoads {
 };
 
 template <int D, int NB, int NR>
-__global__ __launch_bounds__(AT, 2) void k_kv_attn(AttnArgs a, CodePlanes cp) {
+__global__ __launch_bounds__(AT, kWaves<D>) void k_kv_attn(AttnArgs a, CodePlanes cp) {
   constexpr int TR = 16 * NR, B = D / NB, KK = D / 32, UN = D / 16;
   constexpr int RB = D / 2;                // bytes of a cache row
   constexpr int CH = RB / 16;              // 16-byte chunks of a row
-  constexpr int kVBytes = kStep * RB;      // a wave's value codes
-  constexpr int kScaleFloats = 2 * NB * kStep;
-  constexpr int kWaveBytes = kVBytes + kScaleFloats * 4;
+  constexpr int LB = RB + 16;              // a row in LDS: 16 rows' pieces of one column lie in different banks
+  constexpr int kVBytes = kStep * LB;      // a wave's value codes
+  constexpr int kWaveBytes = kVBytes + NB * kStep * 6;   // value codes, fp32 key scales, fp16 value scales
   constexpr int kMergeBytes = 2 * TR * (D + 4) * 4;
   constexpr int kShared = AW * kWaveBytes > kMergeBytes ? AW * kWaveBytes : kMergeBytes;
   __shared__ __attribute__((aligned(16))) unsigned char smem[kShared];
+  __shared__ uint32_t pair[256];
   __shared__ float ml[AW][2][TR];
-  __shared__ int64_t pre[AT + 1];
-  __shared__ int64_t wave_tot[AW];
+  __shared__ SeqTable seqs;
   __shared__ int found;
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   unsigned char* const vbuf = smem + wave * kWaveBytes;
   float* const kscale = reinterpret_cast<float*>(vbuf + kVBytes);
-  float* const vscale = kscale + NB * kStep;
-  Planes P;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    P.lo[i] = cp.lo[i];
-    P.hi[i] = cp.hi[i];
+  uint16_t* const vscale = reinterpret_cast<uint16_t*>(kscale + NB * kStep);
+  {
+    const u32x4 w = decode_planes(cp, threadIdx.x);   // elements 0 and 4: the low and the high nibble of byte 0
+    pair[threadIdx.x] = (w[0] & 0xFFFFu) | w[2] << 16;
   }
-  const float kmul = a.scale * kLog2e * cp.inv, vmul = cp.inv;
+  const float kmul = a.scale * kLog2e * cp.inv;
 
   // this workgroup's range of units
-  scan_units<TR>(a, 0, 0, pre, wave_tot);
+  scan_units<TR>(a, 0, 0, seqs);
   int c0 = 0;
-  int64_t total = pre[AT];
+  int total = seqs.pre[AT];
   for (int c = AT; c < a.b.batch; c += AT) {   // more than 256 sequences: the total first, then back to the front
     __syncthreads();
-    scan_units<TR>(a, c, total, pre, wave_tot);
-    total = pre[AT];
+    scan_units<TR>(a, c, total, seqs);
+    total = seqs.pre[AT];
     c0 = c;
   }
-  const int64_t W = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x, w = blockIdx.x;   // no empty ranges below W
-  const int64_t lo = w < W ? total * w / W : 0, hi = w < W ? total * (w + 1) / W : 0;
-  if (threadIdx.x == 0) a.meta[w * kMetaInts] = -1;
+  total = __builtin_amdgcn_readfirstlane(total);
+  int w = blockIdx.x;
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < a.b.batch; i += AT) {
       const int64_t s0 = a.b.start[i], s1 = a.b.start[i + 1];
@@ -204,42 +311,52 @@ __global__ __launch_bounds__(AT, 2) void k_kv_attn(AttnArgs a, CodePlanes cp) {
       const int len = a.b.length[i];
       if (len < 0 || len > a.b.max_len) raise_fault(a.b, kFaultLength);
     }
-  if (lo >= hi) return;
+  // workgroups are dealt out to the 8 XCDs in turn: neighbouring ranges, which can share a sequence's tokens, go to one
+  const int grid = gridDim.x;
+  if (total >= grid && (grid & 7) == 0) w = (w & 7) * (grid >> 3) + (w >> 3);
+  if (threadIdx.x == 0) a.meta[w * kMetaInts] = -1;   // (of the range: another workgroup's would come too late)
+  const int W = min(total, grid);
+  if (w >= W) return;
+  const Ranges ranges(total, W);
+  const int lo = ranges.first(w), hi = ranges.first(w + 1);
   if (c0 != 0) {
-    int64_t base = 0;
+    int base = 0;
     for (c0 = 0;; c0 += AT) {
       __syncthreads();
-      scan_units<TR>(a, c0, base, pre, wave_tot);
-      if (pre[AT] > lo) break;
-      base = pre[AT];
+      scan_units<TR>(a, c0, base, seqs);
+      if (seqs.pre[AT] > lo) break;
+      base = seqs.pre[AT];
     }
   }
 
-  for (int64_t cur = lo; cur < hi;) {
+  for (int cur = lo; cur < hi;) {
     // the sequence that holds unit `cur`
-    while (pre[AT] <= cur) {
-      const int64_t base = pre[AT];
+    while (seqs.pre[AT] <= cur) {
+      const int base = seqs.pre[AT];
       __syncthreads();
       c0 += AT;
-      scan_units<TR>(a, c0, base, pre, wave_tot);
+      scan_units<TR>(a, c0, base, seqs);
     }
-    if (pre[threadIdx.x] <= cur && cur < pre[threadIdx.x + 1]) found = threadIdx.x;
+    const int tx = opaque(threadIdx.x);
+    if (seqs.pre[tx] <= cur && cur < seqs.pre[tx + 1]) found = tx;
     __syncthreads();
     const int bi = __builtin_amdgcn_readfirstlane(found);
-    const Seq s = seq_of(a.b, c0 + bi);
+    Seq s;
+    s.row0 = __builtin_amdgcn_readfirstlane(seqs.row0[bi]);
+    s.n = __builtin_amdgcn_readfirstlane(seqs.n[bi]);
+    s.len = __builtin_amdgcn_readfirstlane(seqs.len[bi]);
     const int units = units_of<TR>(a, s), tiles = tiles_of<TR>(a, s);
-    const int64_t rem = cur - pre[bi];
-    const int64_t tile_id = rem / units;      // (head, tile) of the sequence
-    const int u0 = (int)(rem - tile_id * units);
-    const int u1 = (int)(hi - cur < units - u0 ? u0 + (hi - cur) : units);
-    const int h = (int)(tile_id / tiles), rt = (int)(tile_id - (int64_t)h * tiles);
+    const uint32_t rem = cur - __builtin_amdgcn_readfirstlane(seqs.pre[bi]);
+    const int tile_id = __builtin_amdgcn_readfirstlane(rem / (uint32_t)units);   // (head, tile) of the sequence
+    const int u0 = (int)rem - tile_id * units, u1 = min(u0 + hi - cur, units);
+    const int h = __builtin_amdgcn_readfirstlane((uint32_t)tile_id / (uint32_t)tiles), rt = tile_id - h * tiles;
     const Tile t = tile_of<TR>(a, s, c0 + bi, h, rt);
-    const int64_t item0 = cur - u0;           // the tile's first unit
     const bool whole = u0 == 0 && u1 == units;
 
     // rows of this lane: row r * 16 + l16 of the tile
     u32x4 qf[NR][KK];
     int32_t r_lo[NR], r_hi[NR];               // tokens it sees
+    float rs[NR];                             // logit (in log2) of one unit of its products
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const int rr = r * 16 + l16;
@@ -251,15 +368,37 @@ __global__ __launch_bounds__(AT, 2) void k_kv_attn(AttnArgs a, CodePlanes cp) {
       r_hi[r] = !ok ? 0 : a.causal ? p + 1 : len;
       r_lo[r] = a.window ? p + 1 - a.window : 0;
       const uint16_t* qp = a.q.data + (s.row0 + i) * a.q.rs + qh * a.q.hs;
+      uint32_t mag = 0;
 #pragma unroll
       for (int k = 0; k < KK; ++k) {
         qf[r][k] = *reinterpret_cast<const u32x4*>(qp + 32 * k + 8 * g);
         if (!ok) qf[r][k] = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) mag = max(mag, max(qf[r][k][x] & 0x7FFFu, (qf[r][k][x] >> 16) & 0x7FFFu));
+      }
+      mag = max(mag, (uint32_t)__shfl_xor((int)mag, 16, 64));
+      mag = max(mag, (uint32_t)__shfl_xor((int)mag, 32, 64));
+      const int e = exponent_of(mag);
+      const float f = pow2(-e);
+      rs[r] = kmul * pow2(e);
+      // in the order that pairs decode to: 0, 4, 1, 5, 2, 6, 3, 7
+#pragma unroll
+      for (int k = 0; k < KK; ++k) {
+        const u32x4 w = qf[r][k];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          qf[r][k][2 * x] = pack_f16x2(__uint_as_float(w[x] << 16) * f, __uint_as_float(w[x + 2] << 16) * f);
+          qf[r][k][2 * x + 1] =
+              pack_f16x2(__uint_as_float(w[x] & 0xFFFF0000u) * f, __uint_as_float(w[x + 2] & 0xFFFF0000u) * f);
+        }
       }
     }
 
     f32x4 O[NR][UN];
-    float m[NR], l[NR];
+    float m[NR], l[NR];                       // running maximum (in products' units) and this lane's part of the sum
+    int ve[NB];                               // O is in units of 2^ve of each block
+#pragma unroll
+    for (int b = 0; b < NB; ++b) ve[b] = -100;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       m[r] = neg_inf();
@@ -269,144 +408,217 @@ __global__ __launch_bounds__(AT, 2) void k_kv_attn(AttnArgs a, CodePlanes cp) {
     }
 
     const int steps = t.hi > t.base ? (t.hi - t.base + kStep - 1) / kStep : 0;
-    const int st_end = min(u1 * AW, steps);
+    const int st_end = min((u1 << a.ushift) * AW, steps);
 
-    // page of this lane group's 16 tokens of a step: -1 past the last token, -2 where the entry is wrong
+    // the table's entry for this lane group's 16 tokens of a step (its first entry past the last token): loaded two steps
+    // ahead, and looked at only when it is used, so that no wait for it waits for the loads behind it
+    const int32_t* const table = a.b.table + (int64_t)t.b * a.b.max_pages;
+    const int pshift = a.c.pshift;
     auto page_at = [&](int st) -> int {
       const int tok = t.base + st * kStep + 16 * g;
-      if (st >= st_end || tok >= t.hi) return -1;
-      const int pid = a.b.table[(int64_t)t.b * a.b.max_pages + (tok >> a.c.pshift)];
-      if (pid < 0 || pid >= a.c.pages) {
-        if (l16 == 0) raise_fault(a.b, kFaultPage);
-        return -2;
-      }
-      return pid;
+      return table[tok < t.hi ? tok >> pshift : 0];
     };
-    auto row_of = [&](int pid, int tok) -> int64_t {   // row of the cache's buffers (row 0 where there is none)
-      return pid < 0 ? 0 : (((int64_t)pid * a.c.heads + t.h) << a.c.pshift) + (tok & ((1 << a.c.pshift) - 1));
+    const uint32_t pages = (uint32_t)a.c.pages;
+    // this head's rows of page 0, and the row of a token from there (of page 0 where the entry is wrong: read, not used)
+    const int64_t head_row = (int64_t)t.h << a.c.pshift;
+    const uint8_t* const kc = a.c.kc + head_row * RB;
+    const uint8_t* const vc = a.c.vc + head_row * RB;
+    const uint16_t* const ksc = a.c.ks + head_row * NB;
+    const uint16_t* const vsc = a.c.vs + head_row * NB;
+    const uint32_t page_rows = (uint32_t)a.c.heads << a.c.pshift, slot_mask = (1u << a.c.pshift) - 1;
+    auto row_of = [&](int pid, int tok) -> uint64_t {
+      return (uint64_t)((uint32_t)pid < pages ? (uint32_t)pid : 0u) * page_rows + ((uint32_t)tok & slot_mask);
     };
-    auto load = [&](StepLoads<D, NB>& L, int st, int pid) {
-      const int tok0 = t.base + st * kStep;
-      // keys: row 4a + i of token tile tt is token 16a + 4tt + i
+    auto load_k = [&](StepLoads<D, NB>& L, int st, int pid, Pages pg) {
+      // row 4a + i of token tile tt is token 16a + 4tt + i: 16 tokens aligned to 16 lie in one page
       const int ka = l16 >> 2;
-      const int kp = __shfl(pid, 16 * ka, 64);
+      int pk = pg.p[0];
+      if (ka == 1) pk = pg.p[1];
+      if (ka == 2) pk = pg.p[2];
+      if (ka == 3) pk = pg.p[3];
+      const uint8_t* p = kc + row_of(pk, t.base + st * kStep + 16 * ka + (l16 & 3)) * RB;
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
-        const uint8_t* p = a.c.kc + row_of(kp, tok0 + 16 * ka + 4 * tt + (l16 & 3)) * RB;
         if constexpr (D == 64) {
-          const uint2 x = *reinterpret_cast<const uint2*>(p + 8 * g);
+          const uint2 x = *reinterpret_cast<const uint2*>(p + 4 * tt * RB + 8 * g);
           L.k[tt][0] = u32x4{x.x, x.y, 0, 0};
         } else {
 #pragma unroll
           for (int k = 0; k < StepLoads<D, NB>::KW; ++k)
-            L.k[tt][k] = *reinterpret_cast<const u32x4*>(p + 64 * k + 16 * g);
+            L.k[tt][k] = *reinterpret_cast<const u32x4*>(p + 4 * tt * RB + 64 * k + 16 * g);
         }
       }
-      // values: CH lanes per token
+    };
+    auto load_v = [&](StepLoads<D, NB>& L, int st, int pid, Pages pg) {
+      const int tok0 = t.base + st * kStep;
+      // CH lanes per token: a load takes 32 (D = 64), 16 or 8 (D = 256) tokens, so one or half of a page's 16, whose
+      // base is the same in all lanes, or two
+      const uint32_t own = 16 * lane;
 #pragma unroll
       for (int i = 0; i < StepLoads<D, NB>::VL; ++i) {
-        const int tk = i * (64 / CH) + lane / CH;
-        const int vp = __shfl(pid, tk & ~15, 64);
-        L.v[i] = *reinterpret_cast<const u32x4*>(a.c.vc + row_of(vp, tok0 + tk) * RB + 16 * (lane & (CH - 1)));
+        const uint8_t* p;
+        if constexpr (D == 64) {
+          const uint64_t r0 = row_of(pg.p[2 * i], tok0 + 32 * i), r1 = row_of(pg.p[2 * i + 1], tok0 + 32 * i + 16);
+          p = vc + (lane < 32 ? r0 : r1) * RB + (own & 511u);
+        } else {
+          constexpr int T = 64 / CH;
+          p = vc + row_of(pg.p[i * T / 16], tok0 + i * T) * RB + own;
+        }
+        L.v[i] = *reinterpret_cast<const u32x4*>(p);
       }
       // scales of token `lane`
-      const int64_t row = row_of(pid, tok0 + lane) * NB;
+      const uint64_t row = row_of(pid, tok0 + lane) * NB;
       if constexpr (NB == 1) {
-        L.ks[0] = a.c.ks[row];
-        L.vs[0] = a.c.vs[row];
+        L.ks[0] = ksc[row];
+        L.vs[0] = vsc[row];
       } else {
 #pragma unroll
         for (int k = 0; k < NB / 2; ++k) {
-          L.ks[k] = reinterpret_cast<const uint32_t*>(a.c.ks + row)[k];
-          L.vs[k] = reinterpret_cast<const uint32_t*>(a.c.vs + row)[k];
+          L.ks[k] = reinterpret_cast<const uint32_t*>(ksc + row)[k];
+          L.vs[k] = reinterpret_cast<const uint32_t*>(vsc + row)[k];
         }
-      }
-      // no token: scale 0; no page: NaN
-      const bool none = tok0 + lane >= t.hi;
-#pragma unroll
-      for (int k = 0; k < (NB + 1) / 2; ++k) {
-        if (pid == -2) L.ks[k] = L.vs[k] = kBf16NaN * 0x10001u;
-        if (none) L.ks[k] = L.vs[k] = 0;
       }
     };
 
-    int st = u0 * AW + wave;
+    int st = (u0 << a.ushift) * AW + wave;
     StepLoads<D, NB> L;
-    int pid = page_at(st);
-    int pid_next = page_at(st + AW);
-    if (st < st_end) load(L, st, pid);
+    int pid = page_at(st), pid_next = page_at(st + AW), pid_after;
+    if (st < st_end) {
+      const Pages pg = pages_of(pid);
+      load_v(L, st, pid, pg);
+      load_k(L, st, pid, pg);
+    }
+    // this lane's token row of the transposing reads: row n of 16 is token 8 (n / 8) + (n % 8) / 2 + 4 (n % 2), so that a
+    // dword of what comes back decodes in token order
+    unsigned char* const vplanes = vbuf + ((lane & ~7) + ((lane & 7) >> 1) + 4 * (lane & 1)) * LB;
     for (; st < st_end; st += AW) {
       const int tok0 = t.base + st * kStep;
+      pid_after = page_at(st + 2 * AW);
       // value codes and scales to LDS, this wave's own part of it (a wave's LDS accesses stay in order)
 #pragma unroll
       for (int i = 0; i < StepLoads<D, NB>::VL; ++i) {
         const int tk = i * (64 / CH) + lane / CH, c = lane & (CH - 1);
-        // chunks turned by the token, so that 16 tokens' pieces of one column lie in different banks
-        constexpr int SH = D == 64 ? 3 : D == 128 ? 2 : 1;
-        *reinterpret_cast<u32x4*>(vbuf + tk * RB + 16 * (c ^ ((tk >> SH) & (CH - 1)))) = L.v[i];
+        *reinterpret_cast<u32x4*>(vbuf + tk * LB + 16 * c) = L.v[i];
       }
+      const bool none = tok0 + lane >= t.hi;   // no token: scale 0; no page: NaN
+      const bool wrong = (uint32_t)pid >= pages && !none;
+      if (__any(wrong) && lane == 0) raise_fault(a.b, kFaultPage);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const uint32_t kw = b & 1 ? L.ks[b / 2] >> 16 : L.ks[b / 2] & 0xFFFFu;
-        const uint32_t vw = b & 1 ? L.vs[b / 2] >> 16 : L.vs[b / 2] & 0xFFFFu;
-        kscale[b * kStep + lane] = bf16_to_f32(kw) * kmul;
-        vscale[b * kStep + lane] = bf16_to_f32(vw) * vmul;
-      }
-      u32x4 kc[4][StepLoads<D, NB>::KW];
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-        for (int k = 0; k < StepLoads<D, NB>::KW; ++k) kc[tt][k] = L.k[tt][k];
-      // the next step's loads run under this step's work
-      if (st + AW < st_end) {
-        load(L, st + AW, pid_next);
-        pid_next = page_at(st + 2 * AW);
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-
-      // S^T: rows = tokens, columns = rows of q
-      f32x4 S[NR][4];
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          f32x4 acc[NR];
-#pragma unroll
-          for (int r = 0; r < NR; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = b * (B / 32); k < (b + 1) * (B / 32); ++k) {
-            const u32x4 kf = dequant8(P, kc[tt][k / 4][k % 4]);
-#pragma unroll
-            for (int r = 0; r < NR; ++r) acc[r] = mfma16(kf, qf[r][k], acc[r]);
-          }
-          const f32x4 sk = *reinterpret_cast<const f32x4*>(kscale + b * kStep + 16 * g + 4 * tt);
+        uint32_t kw = b & 1 ? L.ks[b / 2] >> 16 : L.ks[b / 2] & 0xFFFFu;
+        uint32_t vw = b & 1 ? L.vs[b / 2] >> 16 : L.vs[b / 2] & 0xFFFFu;
+        if (wrong) kw = vw = kBf16NaN;
+        if (none) kw = vw = 0;
+        kscale[b * kStep + lane] = bf16_to_f32(kw);
+        const uint32_t mag = vw & 0x7FFFu, held = (uint32_t)(ve[b] + 128) << 7;   // magnitudes below `held` fit
+        if (__any(mag >= held && mag < 0x7F80u)) {
+          const int e = exponent_of(wave_max(mag < 0x7F80u ? mag : 0u));
+          const float f = pow2(max(ve[b] - e, -126));
+          ve[b] = e;
 #pragma unroll
           for (int r = 0; r < NR; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              S[r][tt][i] = b == 0 ? acc[r][i] * sk[i] : __builtin_fmaf(acc[r][i], sk[i], S[r][tt][i]);
+            for (int u = b * (B / 16); u < (b + 1) * (B / 16); ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) O[r][u][i] *= f;
+        }
+        vscale[b * kStep + lane] = (uint16_t)(pack_f16x2(bf16_to_f32(vw) * pow2(-ve[b]), 0.0f) & 0xFFFFu);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+
+      // S^T: rows = tokens, columns = rows of q, in stages of two products (64 elements of a token tile).  The lookups
+      // of a stage are issued one stage ahead of its products (left to itself the compiler waits for each pair's own)
+      constexpr int ST = KK / 2, SB = B == 32 ? 2 : 1;   // stages of a token tile, blocks that a stage touches
+      f32x4 S[NR][4];
+      u32x4 kf[2][2];
+      f32x4 sk[2][SB];
+      auto fetch = [&](int i) {
+        const int tt = i / ST, h2 = i % ST;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int k = 2 * h2 + x;
+          kf[i & 1][x] = decode_pairs(pair, L.k[tt][k / 4][k % 4]);
+        }
+#pragma unroll
+        for (int x = 0; x < SB; ++x)
+          sk[i & 1][x] =
+              *reinterpret_cast<const f32x4*>(kscale + (2 * h2 + x) * 32 / B * kStep + 16 * g + 4 * tt);
+      };
+      fetch(0);
+      f32x4 acc[NR];
+#pragma unroll
+      for (int i = 0; i < 4 * ST; ++i) {
+        const int tt = i / ST, h2 = i % ST;
+        __builtin_amdgcn_sched_barrier(0);
+        if (i + 1 < 4 * ST) fetch(i + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int k = 2 * h2 + x;
+          const bool first = 32 * k % B == 0, last = 32 * (k + 1) % B == 0;   // of its block
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            if (first) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+            acc[r] = mfma16h(kf[i & 1][x], qf[r][k], acc[r]);
+            if (last) {
+              const f32x4 f = sk[i & 1][SB == 2 ? x : 0];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) S[r][tt][j] = k < B / 32 ? acc[r][j] * f[j] : __builtin_fmaf(acc[r][j], f[j], S[r][tt][j]);
+            }
+          }
+        }
+        // the scaled products are formed here: left alone, the compiler moves this into the branches below and holds
+        // the products of all blocks and all scales until then, 50 registers more
+        if (h2 == ST - 1) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r) asm volatile("" : "+v"(S[r][tt]));
         }
       }
+      pid = pid_next;
+      pid_next = pid_after;
+      // the next step's loads run under the rest of this one
+      if (st + AW < st_end) {
+        const Pages pg = pages_of(pid);
+        load_v(L, st + AW, pid, pg);
+        load_k(L, st + AW, pid, pg);
+      }
 
-      const bool edge = tok0 < t.lo_max || tok0 + kStep > t.hi_min;
-      uint32_t vis[NR];   // bit 4tt + i: the lane's row sees that token
+      // value codes, transposed, and scales: the first ones are read now and used after the softmax, the others two
+      // column tiles and one block ahead
+      typedef int v2i __attribute__((ext_vector_type(2)));
+      v2i vw[UN];
+      u32x4 sv[NB][2];
+      auto read_v = [&](int u) {
+        vw[u] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((__attribute__((address_space(3))) v2i*)(vplanes + 8 * u));
+      };
+      auto read_sv = [&](int b) {
 #pragma unroll
-      for (int r = 0; r < NR; ++r) vis[r] = 0xFFFFu;
+        for (int x = 0; x < 2; ++x) sv[b][x] = *reinterpret_cast<const u32x4*>(vscale + b * kStep + 16 * g + 8 * x);
+      };
+      read_sv(0);
+      read_v(0);
+      read_v(1);
+      __builtin_amdgcn_sched_barrier(0);
+
+      // tokens 16g + 4tt + i that the lane's row does not see (only in steps at an end of what some row sees)
+      const bool edge = tok0 < t.lo_max || tok0 + kStep > t.hi_min;
+      uint32_t vis[NR];   // bit 4tt + i: the lane's row sees that token (used at an edge only)
       if (edge) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          vis[r] = 0;
+          const int t0 = tok0 + 16 * g;
+          const int lo = min(max(r_lo[r] - t0, 0), 16), hi = min(max(r_hi[r] - t0, 0), 16);
+          vis[r] = (1u << hi) - (1u << min(lo, hi));
 #pragma unroll
           for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int tok = tok0 + 16 * g + 4 * tt + i;
-              const bool see = tok >= r_lo[r] && tok < r_hi[r];
-              if (!see) S[r][tt][i] = neg_inf();
-              vis[r] |= see ? 1u << (4 * tt + i) : 0u;
+              const uint32_t m = __builtin_amdgcn_sbfe((int)vis[r], 4 * tt + i, 1);
+              S[r][tt][i] = __uint_as_float((__float_as_uint(S[r][tt][i]) & m) | (0xFF800000u & ~m));
             }
         }
       }
+      uint32_t pp[NR][4][2];   // probabilities of tokens 16g + 4tt + 0, 1 and 2, 3 in fp16
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         float mx = S[r][0][0];
@@ -417,7 +629,7 @@ __global__ __launch_bounds__(AT, 2) void k_kv_attn(AttnArgs a, CodePlanes cp) {
         mx = fmaxf(group_max(mx), m[r]);
         const float mu = mx == neg_inf() ? 0.0f : mx;
         if (__any(mx > m[r])) {
-          const float alpha = __builtin_amdgcn_exp2f(m[r] - mu);
+          const float alpha = __builtin_amdgcn_exp2f((m[r] - mu) * rs[r]);
           l[r] *= alpha;
 #pragma unroll
           for (int u = 0; u < UN; ++u)
@@ -425,12 +637,16 @@ __global__ __launch_bounds__(AT, 2) void k_kv_attn(AttnArgs a, CodePlanes cp) {
             for (int i = 0; i < 4; ++i) O[r][u][i] *= alpha;
         }
         m[r] = mx;
+        const float off = kPBits - mu * rs[r];
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            S[r][tt][i] = __builtin_amdgcn_exp2f(S[r][tt][i] - mu);
-            l[r] += S[r][tt][i];
+          for (int i = 0; i < 2; ++i) {
+            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(S[r][tt][2 * i], rs[r], off));
+            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(S[r][tt][2 * i + 1], rs[r], off));
+            l[r] += p0;
+            l[r] += p1;
+            pp[r][tt][i] = pack_f16x2(p0, p1);
           }
       }
 
@@ -438,36 +654,35 @@ __global__ __launch_bounds__(AT, 2) void k_kv_attn(AttnArgs a, CodePlanes cp) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         u32x4 pf[NR][2];   // tokens 16g + 0..7 and + 8..15
-        f32x4 sv[4];
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) sv[tt] = *reinterpret_cast<const f32x4*>(vscale + b * kStep + 16 * g + 4 * tt);
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
-          for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              float x = S[r][tt][i] * sv[tt][i], y = S[r][tt][i + 1] * sv[tt][i + 1];
-              // a scale can be NaN: what the row does not see is left out, not multiplied by zero
-              if (!(vis[r] >> (4 * tt + i) & 1u)) x = 0.0f;
-              if (!(vis[r] >> (4 * tt + i + 1) & 1u)) y = 0.0f;
-              pf[r][tt / 2][2 * (tt & 1) + i / 2] = pack_bf16x2(x, y);
-            }
-#pragma unroll
-        for (int u = b * (B / 16); u < (b + 1) * (B / 16); ++u) {
-          // row of lane n of the 16: token 8 (n / 8) + (n % 8) / 2 + 4 (n % 2), so that the dword of 8 tokens
-          // decodes in token order
-          const int tk = 16 * g + (l16 & 8) + ((l16 & 7) >> 1) + 4 * (l16 & 1);
-          constexpr int SH = D == 64 ? 3 : D == 128 ? 2 : 1;
-          const int off = tk * RB + 16 * ((u >> 1) ^ ((tk >> SH) & (CH - 1))) + 8 * (u & 1);
-          typedef int v2i __attribute__((ext_vector_type(2)));
-          const v2i w2 =
-              __builtin_amdgcn_ds_read_tr4_b64_v2i32((__attribute__((address_space(3))) v2i*)(vbuf + off));
-          const u32x4 v0 = dequant8(P, (uint32_t)w2[0]), v1 = dequant8(P, (uint32_t)w2[1]);
+          for (int x = 0; x < 8; ++x)
+            pf[r][x / 4][x % 4] = mul_f16x2(pp[r][x / 2][x % 2], sv[b][x / 4][x % 4]);
+        if (edge) {
+          // a scale can be NaN: what the row does not see is left out, not multiplied by zero
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            O[r][u] = mfma16(v0, pf[r][0], O[r][u]);
-            O[r][u] = mfma16(v1, pf[r][1], O[r][u]);
+            uint32_t see = vis[r];
+            asm volatile("" : "+v"(see));   // formed anew for each block: the masks kept from one to the next are 24 registers
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const uint32_t m0 = __builtin_amdgcn_sbfe((int)see, 2 * x, 1), m1 = __builtin_amdgcn_sbfe((int)see, 2 * x + 1, 1);
+              pf[r][x / 4][x % 4] &= (m0 & 0xFFFFu) | (m1 & 0xFFFF0000u);
+            }
+          }
+        }
+#pragma unroll
+        for (int u = b * (B / 16); u < (b + 1) * (B / 16); ++u) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (u + 2 < UN) read_v(u + 2);
+          if (b + 1 < NB && u + 1 == (b + 1) * (B / 16)) read_sv(b + 1);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const u32x4 v = decode_planes(cp, (uint32_t)vw[u][x]);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) O[r][u] = mfma16h(v, pf[r][x], O[r][u]);
+            __builtin_amdgcn_sched_barrier(0);
           }
         }
       }
@@ -475,12 +690,14 @@ __global__ __launch_bounds__(AT, 2) void k_kv_attn(AttnArgs a, CodePlanes cp) {
     }
 
     // the four waves' sums, two by two
+    const int el = opaque(lane), e16 = el & 15, eg = el >> 4;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      l[r] = group_sum(l[r]);
-      if (g == 0) {
-        ml[wave][0][r * 16 + l16] = m[r];
-        ml[wave][1][r * 16 + l16] = l[r];
+      l[r] = group_sum(l[r]) * pow2(-(int)kPBits);
+      m[r] *= rs[r];
+      if (eg == 0) {
+        ml[wave][0][r * 16 + e16] = m[r];
+        ml[wave][1][r * 16 + e16] = l[r];
       }
     }
     __syncthreads();   // also: every wave is done with its value buffer
@@ -489,17 +706,19 @@ __global__ __launch_bounds__(AT, 2) void k_kv_attn(AttnArgs a, CodePlanes cp) {
     for (int r = 0; r < NR; ++r) {
       mt[r] = neg_inf();
 #pragma unroll
-      for (int k = 0; k < AW; ++k) mt[r] = fmaxf(mt[r], ml[k][0][r * 16 + l16]);
+      for (int k = 0; k < AW; ++k) mt[r] = fmaxf(mt[r], ml[k][0][r * 16 + e16]);
       const float mu = mt[r] == neg_inf() ? 0.0f : mt[r];
       lt[r] = 0.0f;
 #pragma unroll
       for (int k = 0; k < AW; ++k)
-        lt[r] += ml[k][1][r * 16 + l16] * __builtin_amdgcn_exp2f(ml[k][0][r * 16 + l16] - mu);
+        lt[r] += ml[k][1][r * 16 + e16] * __builtin_amdgcn_exp2f(ml[k][0][r * 16 + e16] - mu);
       const float f = __builtin_amdgcn_exp2f(m[r] - mu);
 #pragma unroll
-      for (int u = 0; u < UN; ++u)
+      for (int u = 0; u < UN; ++u) {
+        const float fv = f * (pow2(ve[u * 16 / B] - (int)kPBits) * cp.inv);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) O[r][u][i] *= f;
+        for (int i = 0; i < 4; ++i) O[r][u][i] *= fv;
+      }
     }
     float* const mg = reinterpret_cast<float*>(smem);
     constexpr int LDO = D + 4;
@@ -510,7 +729,7 @@ __global__ __launch_bounds__(AT, 2) void k_kv_attn(AttnArgs a, CodePlanes cp) {
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
-          for (int u = 0; u < UN; ++u) *reinterpret_cast<f32x4*>(d + (r * 16 + l16) * LDO + u * 16 + 4 * g) = O[r][u];
+          for (int u = 0; u < UN; ++u) *reinterpret_cast<f32x4*>(d + (r * 16 + e16) * LDO + u * 16 + 4 * eg) = O[r][u];
       }
       __syncthreads();
       if (wave < round) {
@@ -519,7 +738,7 @@ __global__ __launch_bounds__(AT, 2) void k_kv_attn(AttnArgs a, CodePlanes cp) {
         for (int r = 0; r < NR; ++r)
 #pragma unroll
           for (int u = 0; u < UN; ++u) {
-            const f32x4 x = *reinterpret_cast<const f32x4*>(d + (r * 16 + l16) * LDO + u * 16 + 4 * g);
+            const f32x4 x = *reinterpret_cast<const f32x4*>(d + (r * 16 + e16) * LDO + u * 16 + 4 * eg);
 #pragma unroll
             for (int i = 0; i < 4; ++i) O[r][u][i] += x[i];
           }
@@ -531,7 +750,7 @@ __global__ __launch_bounds__(AT, 2) void k_kv_attn(AttnArgs a, CodePlanes cp) {
       if (whole) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          const int rr = r * 16 + l16;
+          const int rr = r * 16 + e16;
           if (rr >= t.nval) continue;
           const int rho = t.rho0 + rr, i = rho / a.group, qh = t.h * a.group + (rho - i * a.group);
           float inv = lt[r] == 0.0f ? 0.0f : 1.0f / lt[r];
@@ -540,32 +759,32 @@ __global__ __launch_bounds__(AT, 2) void k_kv_attn(AttnArgs a, CodePlanes cp) {
 #pragma unroll
           for (int u = 0; u < UN; ++u) {
             // rows 4g + i of the tile: elements d, d + 4, d + 1, d + 5
-            uint32_t* d = reinterpret_cast<uint32_t*>(op + 16 * u + 8 * (g >> 1) + 2 * (g & 1));
+            uint32_t* d = reinterpret_cast<uint32_t*>(op + 16 * u + 8 * (eg >> 1) + 2 * (eg & 1));
             d[0] = pack_bf16x2(O[r][u][0] * inv, O[r][u][2] * inv);
             d[2] = pack_bf16x2(O[r][u][1] * inv, O[r][u][3] * inv);
           }
-          if (a.lse && g == 0)
+          if (a.lse && eg == 0)
             a.lse[(s.row0 + i) * a.q.n + qh] =
                 s.len < 0 ? __builtin_nanf("") : lt[r] == 0.0f ? neg_inf() : (mt[r] + __builtin_amdgcn_logf(lt[r])) * kLn2;
         }
       } else {
         // slot 0: the range's first tile, begun in an earlier range; slot 1: its last, ending in a later one
-        float* d = a.part + (2 * w + (u0 == 0 ? 1 : 0)) * (int64_t)(TR * (D + 2));
+        float* d = a.part + (2 * (int64_t)w + (u0 == 0 ? 1 : 0)) * (TR * (D + 2));
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          const int rr = r * 16 + l16;
+          const int rr = r * 16 + e16;
 #pragma unroll
           for (int u = 0; u < UN; ++u)
-            *reinterpret_cast<f32x4*>(d + rr * D + u * 16 + 4 * g) = O[r][u];
-          if (g == 0) {
+            *reinterpret_cast<f32x4*>(d + rr * D + u * 16 + 4 * eg) = O[r][u];
+          if (eg == 0) {
             d[TR * D + rr] = mt[r];
             d[TR * D + TR + rr] = lt[r];
           }
         }
-        if (u0 != 0 && u1 == units && lane == 0) {
+        if (u0 != 0 && u1 == units && el == 0) {
           // this range ends the tile: the join of its partial sums is noted here
           int32_t* mt_ = a.meta + w * kMetaInts;
-          mt_[0] = (int32_t)(((item0 + 1) * W - 1) / total);   // the workgroup whose range holds its first unit
+          mt_[0] = (int32_t)ranges.of(cur - u0);   // the range that holds its first unit
           mt_[1] = (int32_t)s.row0;
           mt_[2] = t.rho0;
           mt_[3] = t.nval;
@@ -578,52 +797,92 @@ __global__ __launch_bounds__(AT, 2) void k_kv_attn(AttnArgs a, CodePlanes cp) {
   }
 }
 
-// Adds the partial sums of a tile that was cut: workgroup (w, y) the tile that ends in range w, if any,
-// rows y, y + gridDim.y, ...  The parts lie in slot 1 of the first range and slot 0 of the others.
+// Adds the partial sums of a tile that was cut: workgroup (w, y) the tile that ends in range w, if any, wave v the row
+// 4y + v.  The parts lie in slot 1 of the first range and slot 0 of the others; they are read eight at a time, so that
+// the loads of eight ranges are in flight together.
 template <int D, int TR>
-__global__ __launch_bounds__(D) void k_kv_attn_join(AttnArgs a) {
-  const int64_t w = blockIdx.x;
-  const int32_t* mt = a.meta + w * kMetaInts;
-  const int64_t w0 = mt[0];
-  if (w0 < 0) return;
-  const int d = threadIdx.x;
+__global__ __launch_bounds__(256) void k_kv_attn_join(AttnArgs a) {
+  constexpr int C = D / 64;   // columns of a lane
   constexpr int64_t P = TR * (D + 2);
-  for (int rr = blockIdx.y; rr < mt[3]; rr += gridDim.y) {
-    float m = neg_inf();
-    for (int64_t k = w0; k <= w; ++k) m = fmaxf(m, a.part[(2 * k + (k == w0)) * P + TR * D + rr]);
-    const float mu = m == neg_inf() ? 0.0f : m;
-    float l = 0.0f, o = 0.0f;
-    for (int64_t k = w0; k <= w; ++k) {
-      const float* p = a.part + (2 * k + (k == w0)) * P;
-      const float f = __builtin_amdgcn_exp2f(p[TR * D + rr] - mu);
-      l = __builtin_fmaf(p[TR * D + TR + rr], f, l);
-      o = __builtin_fmaf(p[rr * D + d], f, o);
+  typedef float vec __attribute__((ext_vector_type(C)));
+  const int w = blockIdx.x, lane = threadIdx.x & 63;
+  const int32_t* mt = a.meta + w * kMetaInts;
+  const int w0 = mt[0], rr = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (w0 < 0 || rr >= mt[3]) return;
+  float m = neg_inf(), l = 0.0f;
+  vec o = 0.0f;
+  for (int k0 = w0; k0 <= w; k0 += 8) {
+    float pm[8], pl[8];
+    vec po[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = min(k0 + i, w);
+      const float* p = a.part + (2 * (int64_t)k + (k == w0)) * P;
+      pm[i] = p[TR * D + rr];
+      pl[i] = p[TR * D + TR + rr];
+      po[i] = *reinterpret_cast<const vec*>(p + rr * D + lane * C);
     }
-    const int rho = mt[2] + rr, i = rho / a.group, qh = mt[4] * a.group + (rho - i * a.group);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    // position d of a partial row: row d % 16 of column tile d / 16
-    const int e = (d & ~15) + (d & 8) + ((d & 7) >> 1) + 4 * (d & 1);
-    a.o.data[(mt[1] + i) * a.o.rs + qh * a.o.hs + e] = (uint16_t)(pack_bf16x2(o * inv, 0.0f) & 0xFFFFu);
-    if (a.lse && d == 0)
-      a.lse[(mt[1] + i) * (int64_t)a.q.n + qh] = l == 0.0f ? neg_inf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    float mx = m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (k0 + i > w) pm[i] = neg_inf(), pl[i] = 0.0f, po[i] = 0.0f;
+      mx = fmaxf(mx, pm[i]);
+    }
+    const float mu = mx == neg_inf() ? 0.0f : mx;
+    const float f0 = __builtin_amdgcn_exp2f(m - mu);
+    m = mx;
+    l *= f0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] *= f0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float f = __builtin_amdgcn_exp2f(pm[i] - mu);
+      l = __builtin_fmaf(pl[i], f, l);
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] = __builtin_fmaf(po[i][c], f, o[c]);
+    }
   }
+  const int rho = mt[2] + rr, i = rho / a.group, qh = mt[4] * a.group + (rho - i * a.group);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t* out = a.o.data + (mt[1] + i) * a.o.rs + qh * a.o.hs;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    // position d of a partial row: row d % 16 of column tile d / 16
+    const int d = lane * C + c, e = (d & ~15) + (d & 8) + ((d & 7) >> 1) + 4 * (d & 1);
+    out[e] = (uint16_t)(pack_bf16x2(o[c] * inv, 0.0f) & 0xFFFFu);
+  }
+  if (a.lse && lane == 0)
+    a.lse[(mt[1] + i) * (int64_t)a.q.n + qh] = l == 0.0f ? neg_inf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-uint16_t bf16_host(float f) {
-  uint32_t b;
-  __builtin_memcpy(&b, &f, 4);
-  return (uint16_t)((b + 0x7FFFu + ((b >> 16) & 1u)) >> 16);
+// Byte tables of v_perm_b32 lookups by the code and by the code ^ 8 whose xor is table[code] (see CodePlanes).
+void xor_tables(const uint8_t (&table)[16], uint32_t (&out)[4]) {
+  uint8_t t[16];
+  for (int i = 0; i < 16; ++i) t[i] = table[i];
+  // low entry c (0..7) is xored with what the high table's lookup gives for selector c + 8, high entry c with what the
+  // low table's gives; the signs that selectors 8..11 copy are those of entries finished before
+  auto sign = [&](int i) { return (uint8_t)(t[i] & 0x80 ? 0xFF : 0); };
+  for (int c = 5; c < 8; ++c) t[c] ^= 0xFF, t[8 + c] ^= 0xFF;   // selectors 13..15; 12 gives 0
+  t[3] ^= sign(8 + 7), t[8 + 3] ^= sign(7);                     // selector 11: byte 7
+  t[1] ^= sign(8 + 3), t[8 + 1] ^= sign(3);                     // selector 9: byte 3
+  t[2] ^= sign(8 + 5), t[8 + 2] ^= sign(5);                     // selector 10: byte 5
+  t[0] ^= sign(8 + 1), t[8 + 0] ^= sign(1);                     // selector 8: byte 1
+  for (int i = 0; i < 4; ++i)
+    out[i] = t[4 * i] | (uint32_t)t[4 * i + 1] << 8 | (uint32_t)t[4 * i + 2] << 16 | (uint32_t)t[4 * i + 3] << 24;
 }
 
 CodePlanes planes_host(int cb) {
   CodePlanes p{};
-  const float c = cb == QLORA_CODEBOOK_FP4 ? 6.0f : cb == QLORA_CODEBOOK_INT4 ? 7.0f : 1.43675f;
+  const float c = cb == QLORA_CODEBOOK_FP4 ? 6.0f : cb == QLORA_CODEBOOK_INT4 ? 7.0f : 1.0f;
   const float* lv = codebook_levels_host(cb);
+  uint8_t lo[16], hi[16];
   for (int i = 0; i < 16; ++i) {
-    const uint16_t h = bf16_host(lv[i] * c);
-    p.lo[i / 4] |= (uint32_t)(h & 0xFF) << (8 * (i % 4));
-    p.hi[i / 4] |= (uint32_t)(h >> 8) << (8 * (i % 4));
+    const uint16_t h = __builtin_bit_cast(uint16_t, (_Float16)(lv[i] * c));
+    lo[i] = (uint8_t)(h & 0xFF);
+    hi[i] = (uint8_t)(h >> 8);
   }
+  xor_tables(lo, p.lo);
+  xor_tables(hi, p.hi);
   p.inv = 1.0f / c;
   return p;
 }
@@ -635,16 +894,21 @@ AttnPlan attn_plan(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t batc
   const int64_t group = q_heads / kv_heads;
   p.tile = 16;
   const int64_t tiles = ((rows * group + p.tile - 1) / p.tile + batch) * kv_heads;
-  const int64_t units = (max_len + kUnit - 1) / kUnit + 1;
-  p.wgs = 768;
-  if (tiles < p.wgs && tiles * units < p.wgs) p.wgs = tiles * units;
+  // units so large that their number stays below 2^30
+  p.ushift = 0;
+  while (tiles * ((max_len >> (kUnitShift + p.ushift)) + 1) >= int64_t(1) << 30 && p.ushift < 22) ++p.ushift;
+  const int64_t units = (max_len >> (kUnitShift + p.ushift)) + 1;
+  p.wgs = resident_wgs(D);
+  if (tiles * units < p.wgs) p.wgs = tiles * units;
   p.part_floats = (size_t)p.wgs * 2 * p.tile * (D + 2);
   p.meta_ints = (size_t)p.wgs * kMetaInts;
   return p;
 }
 
 template <int D, int NB>
-static hipError_t launch_attn(const AttnArgs& a, const AttnPlan& pl, hipStream_t s) {
+static hipError_t launch_attn(const AttnArgs& a0, const AttnPlan& pl, hipStream_t s) {
+  AttnArgs a = a0;
+  a.ushift = pl.ushift;
   {
     ProfScope ps("k_kv_attn", s);
     hipLaunchKernelGGL((k_kv_attn<D, NB, 1>), dim3((unsigned)pl.wgs), dim3(AT), 0, s, a, planes_host(a.c.cb));
@@ -652,7 +916,7 @@ static hipError_t launch_attn(const AttnArgs& a, const AttnPlan& pl, hipStream_t
     if (e != hipSuccess) return e;
   }
   ProfScope ps("k_kv_attn_join", s);
-  hipLaunchKernelGGL((k_kv_attn_join<D, 16>), dim3((unsigned)pl.wgs, 4), dim3(D), 0, s, a);
+  hipLaunchKernelGGL((k_kv_attn_join<D, 16>), dim3((unsigned)pl.wgs, 4), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

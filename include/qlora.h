@@ -307,7 +307,8 @@ qlora_status qlora_qk_norm_rope_bwd(const qlora_heads* dq_out, const qlora_heads
  * An element stands for level[code] * scale.  A block that holds an infinity or a NaN is stored with
  * a NaN scale; one whose absmax is below 2^-126 as zeros.
  * Requires: head_dim 64, 128 or 256; block_size 32, 64 or 128 (0 = 64), at most head_dim; page_size a
- * power of two from 16 to 2^20; pages >= 1; heads 1..1024; buffers 16-byte aligned.                    */
+ * power of two from 16 to 2^20; 1 <= pages < 2^31; heads 1..1024; heads * page_size * head_dim < 2^32;
+ * buffers 16-byte aligned.                                                                             */
 typedef struct {
   int64_t pages;
   int32_t page_size;

@@ -1,13 +1,15 @@
 """GPU parity of the 4-bit cache (written, read back: bit for bit) and of the attention over it.
 
-Attention's tolerance, from the roundings on its path.  The kernel holds level * c rounded to bf16 (c per
-codebook, chosen so that this is at most 1.75e-3 off for NF4 and exact for FP4 and Int4; TAB below) and rounds
-p * scale_v to bf16 (half a step: 2^-8).  A logit is then off by at most TAB * scale * sum |q k| plus fp32
-errors (2^-16 of that sum is ample), so p / sum p by twice that (relatively), and with E = that error
-  |o - want| <= (2 E + 2^-8 + TAB) (1 + small) sum p|v| + 2^-8 |want|.
-Errors of different elements are independent, so over a whole output they come to far less: relative
-Frobenius error at most 6e-3 (2^-8 / sqrt 3 = 2.3e-3 for p and for the output each, 0.85e-3 for values and for logits
-of unit spread: 3.4e-3 in all), asserted for the cases of ordinary data."""
+Attention's tolerance, from the roundings on its path (fp16: half a step is 2^-11 of a normal value, 2^-25 below
+2^-14).  Levels are held in fp16 times a constant that makes FP4's and Int4's exact: TAB below.  A logit is then off by
+at most TAB * scale * sum |q k| plus fp32 errors and what a row's elements below 2^-17 of its largest lose (2^-16 of
+that sum is ample), so p / sum p by twice that (relatively).  p is rounded to fp16 and multiplied with a power-of-two
+share of the value's scale, rounded again: 2 * 2^-11, or, where small, at most 3 * 2^-25 of the largest such product's
+unit, which is 2^-13 of the largest scale: 3 * 2^-38 * max|v| for each of n tokens.  With E = the logit's error
+  |o - want| <= (2 E + 2^-10 + TAB) (1 + small) sum p|v| + 3 n 2^-38 max|v| + 2^-8 |want|.
+Errors of different elements are independent, so over a whole output they come to far less: relative Frobenius
+error at most 3e-3 (2^-8 / sqrt 3 = 2.3e-3 is the most that the output's own rounding to bf16 can come to for any
+distribution of its significands, 0.3e-3 each for p, values and logits of unit spread), asserted for ordinary data."""
 import math
 
 import numpy as np
@@ -21,7 +23,8 @@ from oracle import kv
 
 pytestmark = pytest.mark.gpu
 
-TAB = {"nf4": 1.75e-3, "fp4": 2.0 ** -22, "int4": 2.0 ** -22}
+TAB = {"nf4": 2.0 ** -11, "fp4": 2.0 ** -22, "int4": 2.0 ** -22}
+P16 = 2.0 ** -10
 FAULT_START, FAULT_LENGTH, FAULT_PAGE = 1, 2, 4
 
 
@@ -193,17 +196,21 @@ def check_attention(h, heads, group, dim, block, book, seed=0, causal=True, wind
             mag = np.einsum("nhd,lhd->nhl", np.abs(qf), np.abs(np.repeat(ks[b], group, 1))).max(-1)
             err[r] = (TAB[book] + 2.0 ** -16) * scale * mag
     e = err[..., None]
-    tol = (np.expm1(2 * e) + 2.0 ** -8 + TAB[book]) * 1.02 * bound + 2.0 ** -8 * np.abs(want) * 1.02
+    tol = (np.expm1(2 * e) + P16 + TAB[book]) * 1.02 * bound + 2.0 ** -8 * np.abs(want) * 1.02
+    for b, n in enumerate(h.lens):
+        if n:
+            tol[h.start[b]:h.start[b + 1]] += 3 * n * 2.0 ** -38 * np.abs(vs[b]).max()
     d = np.abs(got - want)
     assert np.all(np.isfinite(got))
     assert np.all(d <= tol), (d.max(), (d / np.maximum(tol, 1e-30)).max())
     empty = np.isneginf(wl)
     assert np.array_equal(empty, np.isneginf(gl)) and np.all(got[empty] == 0)
+    gl, wl = np.where(empty, 0, gl), np.where(empty, 0, wl)
     assert np.all(np.abs(gl - wl)[~empty] <= err[~empty] + 2.0 ** -20 * (1 + np.abs(wl[~empty])))
     if fro and np.linalg.norm(want) > 0:
         rel = np.linalg.norm(d) / np.linalg.norm(want)
         log(f"  rel fro {rel:.2e}")
-        assert rel <= 6e-3, rel
+        assert rel <= 3e-3, rel
     return cache
 
 
@@ -434,7 +441,7 @@ def test_decoding_steps_eager_and_captured():
             want, _, bound = kv.attention(kv.f64(host_u16(q[b:b + 1])), *vals, lens[b], dim ** -0.5)
             d = np.abs(host(o[b:b + 1].float()).astype(np.float64) - want)
             mag = np.abs(kv.f64(host_u16(q[b]))).sum(-1).max() * np.abs(vals[0]).max() * dim ** -0.5
-            assert np.all(d <= (np.expm1(2 * TAB["nf4"] * mag) + 2.0 ** -8 + TAB["nf4"]) * 1.02 * bound + 2.0 ** -8 * np.abs(want))
+            assert np.all(d <= (np.expm1(2 * TAB["nf4"] * mag) + P16 + TAB["nf4"]) * 1.02 * bound + 2.0 ** -8 * np.abs(want))
 
     # the same from a captured step
     cache2 = fresh()
