@@ -93,17 +93,25 @@ struct AttnArgs {
   float scale;
   int32_t causal, window;
   int32_t ushift;                 // log2 of the unit of work in steps of every wave
+  int32_t few;                    // rows per cache head up to which a sequence is the first kernel's
   float* part;                    // partial sums of ranges that end inside an item
   int32_t* meta;                  // [workgroups][kMetaInts]
 };
 // Sizes of a launch, from what the host knows.
 struct AttnPlan {
   int tile;                       // query rows per tile (row = token and query head of one cache head)
-  int ushift;
-  int64_t wgs;                    // workgroups of the ranges
-  size_t part_floats, meta_ints;
+  int ushift, few;                // as in AttnArgs; few = INT32_MAX: the first kernel alone, 0: the second alone
+  int64_t wgs;                    // workgroups of the first kernel's ranges
+  int64_t many_items;             // tiles x cache heads of the second kernel at most
+  int splits;                     // parts that the tokens of each are cut into
+  size_t part_floats, meta_ints;  // workspace, and where the second kernel's share of it begins
+  size_t many_part, many_meta;
 };
 AttnPlan attn_plan(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t batch, int64_t max_len, int D);
 hipError_t launch_kv_attn(const AttnArgs& a, const AttnPlan& pl, int D, int block, hipStream_t s);
+// sequences with many rows (kv_attn_many.hip)
+struct CodePlanes;
+CodePlanes code_planes(int codebook);
+hipError_t launch_kv_attn_many(const AttnArgs& a, const AttnPlan& pl, int D, int block, hipStream_t s);
 
 }  // namespace qlora

@@ -27,8 +27,7 @@
 // brought to about 1 by a power of two first: a row of q by its own largest element (all 8 bits of elements down to
 // 2^-17 of it stay), the scaled probabilities of a step by the largest scale so far of that
 // block of elements (a running exponent, like the running maximum, that all rows share).
-#include "kernels.h"
-#include "kv.h"
+#include "kv_attn.h"
 
 namespace qlora {
 
@@ -38,7 +37,6 @@ constexpr int AT = 256, AW = AT / 64;
 constexpr int kStep = 64;              // tokens per wave step
 constexpr int kUnitShift = 8;          // log2 of the tokens per unit of work: one step of every wave
 static_assert(kStep * AW == 1 << kUnitShift, "a unit is one step of every wave");
-constexpr int kMetaInts = 8;
 // Waves per SIMD, and the workgroups of a launch: as many as are resident then.  The registers of a step's loads,
 // operands and sums decide: D = 64 fits three without spilling (16 sequences of 16 k tokens, 8 cache heads: 45 us, 48
 // with two waves), 128 and 256 two (82 and 153 us; 84 and 348 with three and the spills, 98 and 184 with one).
@@ -50,56 +48,6 @@ int64_t resident_wgs(int D) { return kCUs * (D == 64 ? kWaves<64> : kWaves<128>)
 // Probabilities are held times 2^13 (with a scale, up to twice its power of two, below fp16's 65504), so that ones
 // down to 2^-27 of the largest keep all their bits and ones below 2^-38 of it are lost.
 constexpr float kPBits = 13.0f;
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-
-// The 16 levels times c in fp16, in the two forms that codes are decoded by.
-//   pair: a byte of codes is looked up in a table of 256 pairs in LDS (one dword: its low nibble's level, its
-//     high nibble's): 1 VALU and 1 LDS instruction for 2 elements.
-//   planes: byte permutes.  v_perm_b32 picks 4 bytes out of 8 by selectors 0..7; its selectors 8..15 give constants
-//     (the sign of byte 1, 3, 5 or 7 for 8..11, then 0, 0xFF, 0xFF, 0xFF).  So the low 8 entries of a byte plane
-//     looked up by the code and the high 8 by the code ^ 8 each give, for the codes that are not theirs, a constant
-//     of the code, which is xored into the tables beforehand: 2 permutes and a xor per plane of 4 codes, and 2 permutes
-//     to interleave the planes: 21 VALU for 8 elements.
-struct CodePlanes {
-  uint32_t lo[4], hi[4];   // [0..1] entries 0..7, [2..3] entries 8..15 of the low and the high bytes
-  float inv;               // 1 / c
-};
-
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ f32x4 mfma16h(u32x4 a, u32x4 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-// two fp32 -> fp16, round to nearest even
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const f32x2 v = {lo, hi};
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, a) * __builtin_bit_cast(f16x2, b));
-}
-__device__ __forceinline__ u32x4 decode_planes(const CodePlanes& p, uint32_t w) {
-  u32x4 o;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {   // elements 0..3 in the low nibbles, 4..7 in the high ones
-    const uint32_t a = (half ? w >> 4 : w) & 0x0F0F0F0Fu, b = a ^ 0x08080808u;
-    const uint32_t lo = __builtin_amdgcn_perm(p.lo[1], p.lo[0], a) ^ __builtin_amdgcn_perm(p.lo[3], p.lo[2], b);
-    const uint32_t hi = __builtin_amdgcn_perm(p.hi[1], p.hi[0], a) ^ __builtin_amdgcn_perm(p.hi[3], p.hi[2], b);
-    o[2 * half] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
-    o[2 * half + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
-  }
-  return o;
-}
-// elements in the order 0, 4, 1, 5, 2, 6, 3, 7 (byte i holds i and i + 4)
-__device__ __forceinline__ u32x4 decode_pairs(const uint32_t* pair, uint32_t w) {
-  return u32x4{pair[w & 0xFFu], pair[(w >> 8) & 0xFFu], pair[(w >> 16) & 0xFFu], pair[w >> 24]};
-}
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 <= e <= 127
-// exponent of a bf16 magnitude, kept where its power of two and the inverse are ordinary numbers
-__device__ __forceinline__ int exponent_of(uint32_t mag) { return min(max((int)(mag >> 7) - 127, -100), 126); }
-
-__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
-
 // maximum over the four lane groups (lanes l % 16 + 16 g)
 __device__ __forceinline__ float group_max(float v) {
   uint32_t u = __float_as_uint(v);
@@ -118,39 +66,6 @@ __device__ __forceinline__ float group_sum(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
-}
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  v = dpp_max<0xB1>(v);    // quad_perm [1, 0, 3, 2]
-  v = dpp_max<0x4E>(v);    // quad_perm [2, 3, 0, 1]
-  v = dpp_max<0x141>(v);   // row_half_mirror
-  v = dpp_max<0x140>(v);   // row_mirror
-  auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  v = max(a[0], a[1]);
-  auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  return __builtin_amdgcn_readfirstlane(max(b[0], b[1]));
-}
-
-// Sequence b as a call sees it.
-struct Seq {
-  int64_t row0;   // first row
-  int32_t n;      // rows (tokens of this call); 0 if its start entries are wrong
-  int32_t len;    // tokens in the cache; -1 if the entry is wrong
-};
-
-__device__ __forceinline__ Seq seq_of(const BatchView& b, int i) {
-  Seq s;
-  const int64_t s0 = b.start[i], s1 = b.start[i + 1];
-  const int len = b.length[i];
-  const bool ok = s0 >= 0 && s1 >= s0 && s1 <= b.rows;
-  s.row0 = ok ? s0 : 0;
-  s.n = ok ? (int)(s1 - s0) : 0;
-  s.len = (len < 0 || len > b.max_len) ? -1 : len;
-  return s;
-}
-
 // Units of every tile of a sequence: enough for the tile that sees the most tokens.
 template <int TR>
 __device__ __forceinline__ int units_of(const AttnArgs& a, const Seq& s) {
@@ -166,47 +81,8 @@ __device__ __forceinline__ int units_of(const AttnArgs& a, const Seq& s) {
 }
 template <int TR>
 __device__ __forceinline__ int tiles_of(const AttnArgs& a, const Seq& s) {
-  return (int)(((int64_t)s.n * a.group + TR - 1) / TR);
-}
-
-// The same value, but what is computed from it is not moved to before this point: addresses of code outside a loop,
-// formed ahead of it, would be held in registers all through it (50 of them, here).
-__device__ __forceinline__ int opaque(int v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
-
-// 256 sequences from c0 on: what the kernel needs of them, and the units before each.
-struct SeqTable {
-  int32_t pre[AT + 1];
-  int32_t row0[AT], n[AT], len[AT];
-  int32_t wave_tot[AW];
-};
-template <int TR>
-__device__ void scan_units(const AttnArgs& a, int c0, int base, SeqTable& q) {
-  const int t = opaque(threadIdx.x), i = c0 + t, lane = t & 63, w = t >> 6;
-  int u = 0;
-  if (i < a.b.batch) {
-    const Seq s = seq_of(a.b, i);
-    u = tiles_of<TR>(a, s) * units_of<TR>(a, s) * a.c.heads;
-    q.row0[t] = (int)s.row0;
-    q.n[t] = s.n;
-    q.len[t] = s.len;
-  }
-  int inc = u;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int o = __shfl_up(inc, off, 64);
-    if (lane >= off) inc += o;
-  }
-  if (lane == 63) q.wave_tot[w] = inc;
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < AW - 1; ++k)
-    if (k < w) inc += q.wave_tot[k];
-  q.pre[t + 1] = base + inc;
-  if (t == 0) q.pre[0] = base;
-  __syncthreads();
+  const int64_t rows = (int64_t)s.n * a.group;
+  return rows > a.few ? 0 : (int)((rows + TR - 1) / TR);   // many rows: the other kernel's
 }
 
 // Units 0 .. total - 1 in W <= total ranges as even as can be, the first total % W of them one longer.
@@ -219,32 +95,6 @@ struct Ranges {
     return unit < border ? unit / (len + 1) : more + (unit - border) / len;
   }
 };
-
-// The tile of a segment, in registers that are the same in every lane.
-struct Tile {
-  Seq s;
-  int32_t b, h, rho0, nval;      // sequence, cache head, first row of the tile and rows it has
-  int32_t base, hi, hi_min, lo_max;   // tokens base .. hi - 1 are seen by some row, lo_max .. hi_min - 1 by all
-};
-
-template <int TR>
-__device__ __forceinline__ Tile tile_of(const AttnArgs& a, const Seq& s, int b, int h, int rt) {
-  Tile t;
-  t.s = s;
-  t.b = b;
-  t.h = h;
-  t.rho0 = rt * TR;
-  const int left = (int)((int64_t)s.n * a.group - t.rho0);
-  t.nval = left < TR ? left : TR;
-  const int len = s.len < 0 ? 0 : s.len;
-  const int p0 = len - s.n + t.rho0 / a.group, p1 = len - s.n + (t.rho0 + t.nval - 1) / a.group;
-  t.hi = a.causal ? max(p1 + 1, 0) : len;
-  t.hi_min = a.causal ? p0 + 1 : len;
-  const int lo = a.window ? max(p0 + 1 - a.window, 0) : 0;
-  t.lo_max = a.window ? max(p1 + 1 - a.window, 0) : 0;
-  t.base = lo & ~(kStep - 1);
-  return t;
-}
 
 // A step's four page entries (16 tokens each) as scalars.
 struct Pages {
@@ -278,7 +128,7 @@ __global__ __launch_bounds__(AT, kWaves<D>) void k_kv_attn(AttnArgs a, CodePlane
   __shared__ __attribute__((aligned(16))) unsigned char smem[kShared];
   __shared__ uint32_t pair[256];
   __shared__ float ml[AW][2][TR];
-  __shared__ SeqTable seqs;
+  __shared__ SeqTable<AT> seqs;
   __shared__ int found;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -293,24 +143,19 @@ __global__ __launch_bounds__(AT, kWaves<D>) void k_kv_attn(AttnArgs a, CodePlane
   const float kmul = a.scale * kLog2e * cp.inv;
 
   // this workgroup's range of units
-  scan_units<TR>(a, 0, 0, seqs);
+  auto count = [&](const Seq& s) -> int { return tiles_of<TR>(a, s) * units_of<TR>(a, s) * a.c.heads; };
+  scan_seqs(a.b, 0, 0, seqs, count);
   int c0 = 0;
   int total = seqs.pre[AT];
   for (int c = AT; c < a.b.batch; c += AT) {   // more than 256 sequences: the total first, then back to the front
     __syncthreads();
-    scan_units<TR>(a, c, total, seqs);
+    scan_seqs(a.b, c, total, seqs, count);
     total = seqs.pre[AT];
     c0 = c;
   }
   total = __builtin_amdgcn_readfirstlane(total);
   int w = blockIdx.x;
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.b.batch; i += AT) {
-      const int64_t s0 = a.b.start[i], s1 = a.b.start[i + 1];
-      if (s0 < 0 || s1 < s0 || s1 > a.b.rows) raise_fault(a.b, kFaultStart);
-      const int len = a.b.length[i];
-      if (len < 0 || len > a.b.max_len) raise_fault(a.b, kFaultLength);
-    }
+  if (blockIdx.x == 0) check_batch_entries<AT>(a.b);
   // workgroups are dealt out to the 8 XCDs in turn: neighbouring ranges, which can share a sequence's tokens, go to one
   const int grid = gridDim.x;
   if (total >= grid && (grid & 7) == 0) w = (w & 7) * (grid >> 3) + (w >> 3);
@@ -323,7 +168,7 @@ __global__ __launch_bounds__(AT, kWaves<D>) void k_kv_attn(AttnArgs a, CodePlane
     int base = 0;
     for (c0 = 0;; c0 += AT) {
       __syncthreads();
-      scan_units<TR>(a, c0, base, seqs);
+      scan_seqs(a.b, c0, base, seqs, count);
       if (seqs.pre[AT] > lo) break;
       base = seqs.pre[AT];
     }
@@ -335,16 +180,13 @@ __global__ __launch_bounds__(AT, kWaves<D>) void k_kv_attn(AttnArgs a, CodePlane
       const int base = seqs.pre[AT];
       __syncthreads();
       c0 += AT;
-      scan_units<TR>(a, c0, base, seqs);
+      scan_seqs(a.b, c0, base, seqs, count);
     }
     const int tx = opaque(threadIdx.x);
     if (seqs.pre[tx] <= cur && cur < seqs.pre[tx + 1]) found = tx;
     __syncthreads();
     const int bi = __builtin_amdgcn_readfirstlane(found);
-    Seq s;
-    s.row0 = __builtin_amdgcn_readfirstlane(seqs.row0[bi]);
-    s.n = __builtin_amdgcn_readfirstlane(seqs.n[bi]);
-    s.len = __builtin_amdgcn_readfirstlane(seqs.len[bi]);
+    const Seq s = seqs.seq(bi);
     const int units = units_of<TR>(a, s), tiles = tiles_of<TR>(a, s);
     const uint32_t rem = cur - __builtin_amdgcn_readfirstlane(seqs.pre[bi]);
     const int tile_id = __builtin_amdgcn_readfirstlane(rem / (uint32_t)units);   // (head, tile) of the sequence
@@ -797,62 +639,19 @@ __global__ __launch_bounds__(AT, kWaves<D>) void k_kv_attn(AttnArgs a, CodePlane
   }
 }
 
-// Adds the partial sums of a tile that was cut: workgroup (w, y) the tile that ends in range w, if any, wave v the row
-// 4y + v.  The parts lie in slot 1 of the first range and slot 0 of the others; they are read eight at a time, so that
-// the loads of eight ranges are in flight together.
+// Adds the partial sums of a tile that was cut: workgroup (w, y) the tile that ends in range w, if any, wave v row
+// 4y + v.  The parts lie in slot 1 of the first range and slot 0 of the others.
 template <int D, int TR>
 __global__ __launch_bounds__(256) void k_kv_attn_join(AttnArgs a) {
-  constexpr int C = D / 64;   // columns of a lane
   constexpr int64_t P = TR * (D + 2);
-  typedef float vec __attribute__((ext_vector_type(C)));
-  const int w = blockIdx.x, lane = threadIdx.x & 63;
+  const int w = blockIdx.x;
   const int32_t* mt = a.meta + w * kMetaInts;
   const int w0 = mt[0], rr = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (w0 < 0 || rr >= mt[3]) return;
-  float m = neg_inf(), l = 0.0f;
-  vec o = 0.0f;
-  for (int k0 = w0; k0 <= w; k0 += 8) {
-    float pm[8], pl[8];
-    vec po[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int k = min(k0 + i, w);
-      const float* p = a.part + (2 * (int64_t)k + (k == w0)) * P;
-      pm[i] = p[TR * D + rr];
-      pl[i] = p[TR * D + TR + rr];
-      po[i] = *reinterpret_cast<const vec*>(p + rr * D + lane * C);
-    }
-    float mx = m;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (k0 + i > w) pm[i] = neg_inf(), pl[i] = 0.0f, po[i] = 0.0f;
-      mx = fmaxf(mx, pm[i]);
-    }
-    const float mu = mx == neg_inf() ? 0.0f : mx;
-    const float f0 = __builtin_amdgcn_exp2f(m - mu);
-    m = mx;
-    l *= f0;
-#pragma unroll
-    for (int c = 0; c < C; ++c) o[c] *= f0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float f = __builtin_amdgcn_exp2f(pm[i] - mu);
-      l = __builtin_fmaf(pl[i], f, l);
-#pragma unroll
-      for (int c = 0; c < C; ++c) o[c] = __builtin_fmaf(po[i][c], f, o[c]);
-    }
-  }
-  const int rho = mt[2] + rr, i = rho / a.group, qh = mt[4] * a.group + (rho - i * a.group);
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t* out = a.o.data + (mt[1] + i) * a.o.rs + qh * a.o.hs;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    // position d of a partial row: row d % 16 of column tile d / 16
-    const int d = lane * C + c, e = (d & ~15) + (d & 8) + ((d & 7) >> 1) + 4 * (d & 1);
-    out[e] = (uint16_t)(pack_bf16x2(o[c] * inv, 0.0f) & 0xFFFFu);
-  }
-  if (a.lse && lane == 0)
-    a.lse[(mt[1] + i) * (int64_t)a.q.n + qh] = l == 0.0f ? neg_inf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+  join_row<D>(
+      a, w - w0 + 1, TR, rr, mt, [&](int k) { return a.part + (2 * (int64_t)(w0 + k) + (k == 0)) * P; },
+      // position d of a partial row: row d % 16 of column tile d / 16
+      [](int d) { return (d & ~15) + (d & 8) + ((d & 7) >> 1) + 4 * (d & 1); });
 }
 
 // Byte tables of v_perm_b32 lookups by the code and by the code ^ 8 whose xor is table[code] (see CodePlanes).
@@ -871,7 +670,9 @@ void xor_tables(const uint8_t (&table)[16], uint32_t (&out)[4]) {
     out[i] = t[4 * i] | (uint32_t)t[4 * i + 1] << 8 | (uint32_t)t[4 * i + 2] << 16 | (uint32_t)t[4 * i + 3] << 24;
 }
 
-CodePlanes planes_host(int cb) {
+}  // namespace
+
+CodePlanes code_planes(int cb) {
   CodePlanes p{};
   const float c = cb == QLORA_CODEBOOK_FP4 ? 6.0f : cb == QLORA_CODEBOOK_INT4 ? 7.0f : 1.0f;
   const float* lv = codebook_levels_host(cb);
@@ -887,21 +688,42 @@ CodePlanes planes_host(int cb) {
   return p;
 }
 
-}  // namespace
+// Sequences with at most kFew rows per cache head go to the kernel of this file, those with more to the one for many rows.
+// The host knows the rows and the sequences of a call, not which has how many: where the mean is low it leaves all of
+// them to the first kernel (which is right for any), with one sequence all to one, otherwise it launches both.
+constexpr int kFew = 32;
 
 AttnPlan attn_plan(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t batch, int64_t max_len, int D) {
-  AttnPlan p;
-  const int64_t group = q_heads / kv_heads;
+  AttnPlan p{};
+  const int64_t rows_h = rows * (q_heads / kv_heads), nseq = batch > 1 ? batch : 1;
+  if (rows_h <= kFew * nseq) p.few = INT32_MAX;
+  else p.few = nseq == 1 ? 0 : kFew;
   p.tile = 16;
-  const int64_t tiles = ((rows * group + p.tile - 1) / p.tile + batch) * kv_heads;
-  // units so large that their number stays below 2^30
-  p.ushift = 0;
-  while (tiles * ((max_len >> (kUnitShift + p.ushift)) + 1) >= int64_t(1) << 30 && p.ushift < 22) ++p.ushift;
-  const int64_t units = (max_len >> (kUnitShift + p.ushift)) + 1;
-  p.wgs = resident_wgs(D);
-  if (tiles * units < p.wgs) p.wgs = tiles * units;
-  p.part_floats = (size_t)p.wgs * 2 * p.tile * (D + 2);
-  p.meta_ints = (size_t)p.wgs * kMetaInts;
+  if (p.few > 0) {
+    const int64_t tiles = ((rows_h + p.tile - 1) / p.tile + nseq) * kv_heads;
+    // units so large that their number stays below 2^30
+    while (tiles * ((max_len >> (kUnitShift + p.ushift)) + 1) >= int64_t(1) << 30 && p.ushift < 22) ++p.ushift;
+    const int64_t units = (max_len >> (kUnitShift + p.ushift)) + 1;
+    p.wgs = resident_wgs(D);
+    if (tiles * units < p.wgs) p.wgs = tiles * units;
+    p.part_floats = (size_t)p.wgs * 2 * p.tile * (D + 2);
+    p.meta_ints = (size_t)p.wgs * kMetaInts;
+  }
+  p.splits = 1;
+  if (p.few != INT32_MAX) {
+    const int tr = many_threads(D) / 2;
+    const int64_t most = rows_h / (p.few + 1) + 1;   // sequences that can have more than `few` rows
+    p.many_items = (rows_h / tr + (most < nseq ? most : nseq)) * kv_heads;
+    // fewer tiles than CUs: the tokens of a tile in parts of at least 512
+    const int64_t parts = (max_len + 511) / 512;
+    if (p.many_items <= kCUs / 2) p.splits = (int)(parts < kCUs / p.many_items ? parts : kCUs / p.many_items);
+    if (p.splits > 1) {
+      p.many_part = p.part_floats;
+      p.many_meta = p.meta_ints;
+      p.part_floats += (size_t)p.many_items * p.splits * tr * (D + 2);
+      p.meta_ints += (size_t)p.many_items * kMetaInts;
+    }
+  }
   return p;
 }
 
@@ -909,9 +731,10 @@ template <int D, int NB>
 static hipError_t launch_attn(const AttnArgs& a0, const AttnPlan& pl, hipStream_t s) {
   AttnArgs a = a0;
   a.ushift = pl.ushift;
+  a.few = pl.few;
   {
     ProfScope ps("k_kv_attn", s);
-    hipLaunchKernelGGL((k_kv_attn<D, NB, 1>), dim3((unsigned)pl.wgs), dim3(AT), 0, s, a, planes_host(a.c.cb));
+    hipLaunchKernelGGL((k_kv_attn<D, NB, 1>), dim3((unsigned)pl.wgs), dim3(AT), 0, s, a, code_planes(a.c.cb));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -920,12 +743,24 @@ static hipError_t launch_attn(const AttnArgs& a0, const AttnPlan& pl, hipStream_
   return hipGetLastError();
 }
 
-hipError_t launch_kv_attn(const AttnArgs& a, const AttnPlan& pl, int D, int block, hipStream_t s) {
+static hipError_t launch_few(const AttnArgs& a, const AttnPlan& pl, int D, int block, hipStream_t s) {
   const int nb = D / block;
   if (D == 64) return nb == 1 ? launch_attn<64, 1>(a, pl, s) : launch_attn<64, 2>(a, pl, s);
   if (D == 128)
     return nb == 1 ? launch_attn<128, 1>(a, pl, s) : nb == 2 ? launch_attn<128, 2>(a, pl, s) : launch_attn<128, 4>(a, pl, s);
   return nb == 2 ? launch_attn<256, 2>(a, pl, s) : nb == 4 ? launch_attn<256, 4>(a, pl, s) : launch_attn<256, 8>(a, pl, s);
+}
+
+hipError_t launch_kv_attn(const AttnArgs& a, const AttnPlan& pl, int D, int block, hipStream_t s) {
+  if (pl.few != INT32_MAX) {
+    AttnArgs m = a;
+    m.few = pl.few;
+    m.part = a.part + pl.many_part;
+    m.meta = a.meta + pl.many_meta;
+    const hipError_t e = launch_kv_attn_many(m, pl, D, block, s);
+    if (e != hipSuccess || pl.few == 0) return e;
+  }
+  return launch_few(a, pl, D, block, s);
 }
 
 }  // namespace qlora
