@@ -159,7 +159,7 @@ AttnWs attn_layout(void* base, const AttnPlan& p) {
   AttnWs w;
   w.part = c.take<float>(p.part_floats);
   w.meta = c.take<int32_t>(p.meta_ints);
-  w.bytes = round_up(c.off, 256);
+  w.bytes = std::max<size_t>(round_up(c.off, 256), 256);   // never 0, which the query gives for sizes that are refused
   return w;
 }
 

@@ -312,6 +312,8 @@ def test_kv_attn_validation(lib):
     need = lib.qlora_kv_attn_workspace(C.byref(c), C.byref(b), 3, 8)
     assert need > 0 and need % 256 == 0
     assert lib.qlora_kv_attn_workspace(C.byref(c), C.byref(b), 0, 8) > 0
+    # sizes that need no scratch at all ask for some, so that 0 always means that they are refused
+    assert lib.qlora_kv_attn_workspace(C.byref(_cache(heads=8)), C.byref(_batch(batch=1, max_pages=512)), 8192, 32) > 0
     # the query reads sizes alone
     assert lib.qlora_kv_attn_workspace(C.byref(_cache(kc=0, vs=0)), C.byref(_batch(start=0, table=0)), 3, 8) == need
     for bad in ((c, b, -1, 8), (c, b, 3, 6), (c, b, 3, 0), (_cache(dim=80), b, 3, 8), (c, _batch(max_pages=0), 3, 8),
