@@ -9,11 +9,15 @@
 // product's operand as it stands (its token order is the accumulator's; the values are read to match, transposed by
 // ds_read_b64_tr_b16).  The maximum is moved only when one grows by more than 2^6, so that the sums are rarely rescaled.
 //
-// Per wave and 64 tokens (D = 128): 32 MFMA of 32 cycles, 32 exponentials of 16 cycles, about 250 other VALU instructions of 4
-// cycles, 100 of them its share of the decoding: bound by the VALU, the matrix cores next.
+// Per wave and 64 tokens (D = 128) the matrix cores take 1024 cycles and the other instructions, about 400 VALU and 90
+// scalar ones, 1800 of issue for the SIMD's two waves: bound by the issue of VALU instructions, the matrix cores next.
+// Measured: 16384 rows of one sequence, 32 query on 8 cache heads of 128, causal, 2.46 to 2.54 ms = 865 to 890 TFLOP/s
+// (a square library product of 8192 reaches 1190); 4 x 4096 rows 0.78 ms, 705; heads of 64 0.50 ms, 546 (twice the
+// exponentials and decoding per product); heads of 256 454 (4 waves to a CU: 512 registers each).  A workgroup's start,
+// its first tile and its end cost 12 to 15 us, which is what short sequences pay: 1024 rows 46 us.
 //
-// One workgroup per tile, those that see the most tokens first; with fewer tiles than CUs the tokens of a tile are cut into
-// `splits` parts, whose sums k_kv_attn_many_join adds.
+// One workgroup per tile; with up to 128 tiles (half the CUs) the tokens of a tile are cut into `splits` parts, whose sums
+// k_kv_attn_many_join adds.
 #include "kv_attn.h"
 
 namespace qlora {
@@ -51,12 +55,14 @@ struct ManyLoads {
   static constexpr int ITEMS = 2 * kTile * CH / T > 0 ? 2 * kTile * CH / T : 1;
   static constexpr int KN = D == 64 ? 2 : 4;               // 32-element runs that a key chunk touches
   static constexpr int NKS = KN * NB * 32 / D > 0 ? KN * NB * 32 / D : 1;   // and blocks
+  uint32_t page[ITEMS];                                    // the table's entries
   u32x4 c[ITEMS];
   uint32_t s[ITEMS][(NKS + 1) / 2];                        // bf16 scales (a value chunk has one)
 };
 
 template <int D, int NB>
-__global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_attn_many(AttnArgs a, CodePlanes cp, int splits) {
+__global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_attn_many(AttnArgs a, CodePlanes cp0,
+                                                                                        int splits) {
   using Loads = ManyLoads<D, NB>;
   constexpr int T = Loads::T, MW = T / 64, TR = 32 * MW, B = D / NB, CH = Loads::CH, ITEMS = Loads::ITEMS;
   constexpr int NKS = Loads::NKS, KN = Loads::KN, KK = D / 16, DT = D / 32, RB = D / 2;
@@ -64,10 +70,15 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
   constexpr int VS = 2 * D + 64;          // of a value row: 4 rows' pieces of 64 bytes do
   __shared__ __attribute__((aligned(16))) unsigned char kt[2][kTile * KS];
   __shared__ __attribute__((aligned(16))) unsigned char vt[2][kTile * VS];
-  __shared__ uint32_t pub[2][2][MW];      // per wave: the largest finite scale of its key and of its value chunks
+  __shared__ uint32_t pub[2][16];         // per wave the largest finite scale of its key chunks, from 8 on of its value chunks
   __shared__ uint32_t poison[2][2 * NB];  // tokens whose values are NaN, per block
   __shared__ SeqTable<T> seqs;
   __shared__ int found;
+
+  // the tables in vector registers: a byte permute takes one scalar operand at most, and would have the other copied each time
+  CodePlanes cp = cp0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(cp.lo[i]), "+v"(cp.hi[i]));
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, h32 = lane >> 5;
@@ -96,7 +107,7 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
   __syncthreads();
   const int bi = __builtin_amdgcn_readfirstlane(found);
   const Seq s = seqs.seq(bi);
-  // the last tiles see the most tokens: they start first
+  // the last tiles of a sequence see the most tokens: they start first
   const int rt = tiles(s) - 1 - (tile_at - __builtin_amdgcn_readfirstlane(seqs.pre[bi]));
   const Tile t = tile_of<TR>(a, s, c0 + bi, h, rt);
 
@@ -110,57 +121,55 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
   float rs;                               // logit (in log2) of one unit of its products, but for the keys' exponent
   {
     const uint16_t* qp = a.q.data + (s.row0 + ri) * a.q.rs + qh * a.q.hs + 8 * h32;
-    uint32_t mag = 0;
 #pragma unroll
-    for (int k = 0; k < KK; ++k) {
-      qf[k] = *reinterpret_cast<const u32x4*>(qp + 16 * k);
-      if (!ok) qf[k] = u32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int x = 0; x < 4; ++x) mag = max(mag, max(qf[k][x] & 0x7FFFu, (qf[k][x] >> 16) & 0x7FFFu));
-    }
-    mag = max(mag, (uint32_t)__shfl_xor((int)mag, 32, 64));
-    const int e = exponent_of(mag);
-    const float f = pow2(-e);
-    rs = a.scale * kLog2e * cp.inv * pow2(e);
-#pragma unroll
-    for (int k = 0; k < KK; ++k)
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        qf[k][x] = pack_f16x2(__uint_as_float(qf[k][x] << 16) * f, __uint_as_float(qf[k][x] & 0xFFFF0000u) * f);
+    for (int k = 0; k < KK; ++k) qf[k] = *reinterpret_cast<const u32x4*>(qp + 16 * k);
   }
 
   // this part's steps
   const int all = t.hi > t.base ? (t.hi - t.base + kTile - 1) / kTile : 0;
   const int per = (all + splits - 1) / splits, st0 = min(part * per, all), st1 = min(st0 + per, all);
 
-  const int64_t head_row = (int64_t)h << a.c.pshift;
+  const int pshift = a.c.pshift;
+  const uint32_t pages = (uint32_t)a.c.pages;
+  const int64_t head_row = (int64_t)h << pshift;
+  const uint8_t *const kc = a.c.kc + head_row * RB, *const vc = a.c.vc + head_row * RB;
+  const uint16_t *const ksc = a.c.ks + head_row * NB, *const vsc = a.c.vs + head_row * NB;
   const uint32_t page_rows = (uint32_t)a.c.heads << a.c.pshift, slot_mask = (1u << a.c.pshift) - 1;
   const int32_t* const table = a.b.table + (int64_t)t.b * a.b.max_pages;
 
   // Chunk `i` of this thread: of the keys for the first half of all chunks, then of the values.  (64 chunks of one kind
   // to a wave, so the kind is a scalar.)
   auto is_key = [&](int i) { return wave * 64 + i * T < kTile * CH; };
-  auto has = [&](int i) { return wave * 64 + i * T < 2 * kTile * CH; };
+  auto has = [&](int i) { return 2 * kTile * CH % T == 0 || wave * 64 + i * T < 2 * kTile * CH; };
   auto chunk_of = [&](int i, int& tok, int& c) {
     const int n = ((int)threadIdx.x + i * T) & (kTile * CH - 1);
     tok = n / CH;
     c = n % CH;
   };
-  auto load = [&](Loads& L, int st) {
+  // The table's entries of a tile are loaded a tile ahead of its codes, and neither they nor the scales are looked at
+  // before the step in which they are used: a wait for one load would be one for all.
+  auto load_pages = [&](uint32_t (&pg)[ITEMS], int st) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      if (!has(i)) continue;
+      int tk, c;
+      chunk_of(i, tk, c);
+      const int tok = t.base + st * kTile + tk;
+      pg[i] = table[tok < t.hi ? tok >> pshift : 0];
+    }
+  };
+  auto load = [&](Loads& L, const uint32_t (&pg)[ITEMS], int st) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       if (!has(i)) continue;
       const bool key = is_key(i);
       int tk, c;
       chunk_of(i, tk, c);
-      const int tok = t.base + st * kTile + tk;
-      const bool in = tok < t.hi;
-      const uint32_t pid = table[in ? tok >> a.c.pshift : 0];
-      const bool page = pid < (uint32_t)a.c.pages;
-      if (in && !page && c == 0 && key) raise_fault(a.b, kFaultPage);
-      const uint64_t row = (uint64_t)(page ? pid : 0u) * page_rows + ((uint32_t)tok & slot_mask) + head_row;
-      L.c[i] = *reinterpret_cast<const u32x4*>((key ? a.c.kc : a.c.vc) + row * RB + 16 * c);
-      const uint16_t* sp = (key ? a.c.ks : a.c.vs) + row * NB;
+      L.page[i] = pg[i];
+      const uint32_t tok = t.base + st * kTile + tk;
+      const uint64_t row = (uint64_t)(pg[i] < pages ? pg[i] : 0u) * page_rows + (tok & slot_mask);
+      L.c[i] = *reinterpret_cast<const u32x4*>((key ? kc : vc) + row * RB + 16 * c);
+      const uint16_t* sp = (key ? ksc : vsc) + row * NB;
       if (key) {
         sp += D == 256 ? (c / 4) * NKS : 0;   // the scales of its section
         if constexpr (NKS == 1) {
@@ -172,17 +181,33 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
       } else {
         L.s[i][0] = sp[32 * c / B];
       }
-      // no token: scale 0; no page: NaN
-#pragma unroll
-      for (int x = 0; x < (NKS + 1) / 2; ++x) {
-        if (!page) L.s[i][x] = kBf16NaN * 0x10001u;
-        if (!in) L.s[i][x] = 0;
-      }
     }
   };
   auto finite = [](uint32_t h) { return (h & 0x7FFFu) < 0x7F80u ? h & 0x7FFFu : 0u; };
-  // largest finite scales of a loaded tile, and (bit 31) whether a value's is not finite
-  auto publish = [&](const Loads& L, int par) {
+  // Tile st, loaded: scales of tokens past the end become 0, of tokens without a page NaN; then its largest finite scales
+  // and (bit 31) whether a value's is not finite, for all waves.
+  auto publish = [&](Loads& L, int st) {
+    const int par = st & 1;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      if (!has(i)) continue;
+      int tk, c;
+      chunk_of(i, tk, c);
+      if (NKS > 1 && !is_key(i)) {   // a value chunk has one scale: in every place
+#pragma unroll
+        for (int x = 0; x < (NKS + 1) / 2; ++x) L.s[i][x] = (L.s[i][0] & 0xFFFFu) * 0x10001u;
+      }
+      const bool last = t.base + (st + 1) * kTile > t.hi, in = !last || t.base + st * kTile + tk < t.hi;
+      const bool wrong = in && L.page[i] >= pages;
+      if (last || __any(wrong)) {
+        if (__any(wrong) && lane == 0) raise_fault(a.b, kFaultPage);
+#pragma unroll
+        for (int x = 0; x < (NKS + 1) / 2; ++x) {
+          if (wrong) L.s[i][x] = kBf16NaN * 0x10001u;
+          if (!in) L.s[i][x] = 0;
+        }
+      }
+    }
     uint32_t mk = 0, mv = 0;
     bool bad = false;
 #pragma unroll
@@ -199,11 +224,19 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
         bad |= (L.s[i][0] & 0x7FFFu) >= 0x7F80u;
       }
     }
-    mk = wave_max(mk);
-    mv = wave_max(mv) | (__any(bad) ? 0x80000000u : 0u);
+    if constexpr (ITEMS == 1) {   // a wave's chunks are of one kind
+      const bool key = is_key(0);
+      const uint32_t m = wave_max(key ? mk : mv);
+      mk = key ? m : 0u;
+      mv = key ? 0u : m;
+    } else {
+      mk = wave_max(mk);
+      mv = wave_max(mv);
+    }
+    if (__any(bad)) mv |= 0x80000000u;
     if (lane == 0) {
-      pub[par][0][wave] = mk;
-      pub[par][1][wave] = mv;
+      pub[par][wave] = mk;
+      pub[par][8 + wave] = mv;
     }
   };
   struct TileExp {
@@ -212,65 +245,68 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
   };
   int v_most = -100;   // (the same in all waves)
   auto exps = [&](int par) {
-    uint32_t mk = 0, mv = 0, bad = 0;
-#pragma unroll
-    for (int w = 0; w < MW; ++w) {
-      mk = max(mk, pub[par][0][w]);
-      mv = max(mv, pub[par][1][w] & 0x7FFFFFFFu);
-      bad |= pub[par][1][w];
-    }
+    // lanes 0 .. 7 (of every 16) take the waves' keys, 8 .. 15 their values
+    const uint32_t w = (lane & 7) < MW ? pub[par][lane & 15] : 0u;
     TileExp e;
-    e.k = __builtin_amdgcn_readfirstlane(exponent_of(mk));
+    e.bad = __any(w >> 31);
+    uint32_t m = w & 0x7FFFFFFFu;
+    m = dpp_max<0xB1>(m);    // quad_perm [1, 0, 3, 2]
+    m = dpp_max<0x4E>(m);    // quad_perm [2, 3, 0, 1]
+    m = dpp_max<0x141>(m);   // row_half_mirror
+    e.k = exponent_of(__builtin_amdgcn_readlane(m, 0));
     // not below 2^-60 of the largest so far: the probabilities that make up for it stay in range
-    e.v = max((int)__builtin_amdgcn_readfirstlane(exponent_of(mv)), v_most - 60);
+    e.v = max(exponent_of(__builtin_amdgcn_readlane(m, 8)), v_most - 60);
     v_most = max(v_most, e.v);
-    e.bad = __builtin_amdgcn_readfirstlane(bad >> 31) != 0;
     return e;
   };
-  auto decode = [&](const Loads& L, int par, const TileExp& e) {
-    if (e.bad) {   // (the same in all waves)
-      if (threadIdx.x < 2 * NB) poison[par][threadIdx.x] = 0;
-      __syncthreads();
+  // The tokens of a tile whose values are NaN, for the rows that see them: in the tile they are zeros (0 * NaN would reach
+  // rows that do not).  All waves take this branch or none does.
+  auto note_poison = [&](const Loads& L, int par) {
+    if (threadIdx.x < 2 * NB) poison[par][threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      if (!has(i) || is_key(i)) continue;
+      int tk, c;
+      chunk_of(i, tk, c);
+      if ((L.s[i][0] & 0x7FFFu) >= 0x7F80u) atomicOr(&poison[par][2 * (32 * c / B) + (tk >> 5)], 1u << (tk & 31));
     }
+    __syncthreads();
+  };
+  // Quarter x of this thread's decoding (8 elements of each chunk), and what it needs of the scales.
+  auto scales = [&](const Loads& L, const TileExp& e, uint32_t (&sc)[ITEMS][NKS]) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      if (!has(i)) continue;
+      const bool key = is_key(i);
+      const float f = pow2(key ? -e.k : -e.v);
+#pragma unroll
+      for (int x = 0; x < NKS; ++x) {
+        const uint32_t w = x & 1 ? L.s[i][x / 2] & 0xFFFF0000u : L.s[i][x / 2] << 16;
+        float v = __uint_as_float(w) * f;
+        if (!key && (w & 0x7F800000u) == 0x7F800000u) v = 0.0f;
+        sc[i][x] = pack_f16x2(v, v);
+      }
+    }
+  };
+  auto decode = [&](const Loads& L, int par, const uint32_t (&sc)[ITEMS][NKS], int x) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       if (!has(i)) continue;
       const bool key = is_key(i);
       int tk, c;
       chunk_of(i, tk, c);
-      uint32_t sc[NKS];
-      const float f = pow2(key ? -e.k : -e.v);
+      u32x4 v = decode_planes(cp, L.c[i][x]);
+      // dword 4c + x of the row: of a key row run k, group g of its section
+      const int k = D == 64 ? x & 1 : x;
+      const uint32_t sx = sc[i][NKS == 1 ? 0 : NKS == KN ? k : k / 2];
 #pragma unroll
-      for (int x = 0; x < NKS; ++x) {
-        uint32_t w = L.s[i][x / 2];
-        w = x & 1 ? w >> 16 : w & 0xFFFFu;
-        if (!key && (w & 0x7FFFu) >= 0x7F80u) {
-          // zeros in the tile (0 * NaN would reach rows that do not see it), noted for the rows that do
-          w = 0;
-          if (x == 0) atomicOr(&poison[par][2 * (32 * c / B) + (tk >> 5)], 1u << (tk & 31));
-        }
-        const float v = bf16_to_f32(w) * f;
-        sc[x] = pack_f16x2(v, v);
-      }
-      if (!key) {
-#pragma unroll
-        for (int x = 1; x < NKS; ++x) sc[x] = sc[0];
-      }
+      for (int y = 0; y < 4; ++y) v[y] = mul_f16x2(v[y], sx);
+      const int own = key ? (D == 64 ? 2 * c : (c & ~3) * 4 + (c & 3)) : 4 * c;
+      const int at = key ? (D == 64 ? 4 * (x & 1) + (x >> 1) : 4 * x) : x;
       unsigned char* const row = key ? kt[par] + tk * KS : vt[par] + tk * VS;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        u32x4 v = decode_planes(cp, L.c[i][x]);
-        // dword 4c + x of the row: of a key row run k, group g of its section
-        const int k = D == 64 ? x & 1 : x;
-        const uint32_t sx = sc[NKS == 1 ? 0 : NKS == KN ? k : k / 2];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) v[y] = mul_f16x2(v[y], sx);
-        int at = 4 * c + x;
-        if (key) at = D == 64 ? 4 * (x & 1) + 2 * c + (x >> 1) : (c & ~3) * 4 + 4 * x + (c & 3);
-        *reinterpret_cast<u32x4*>(row + 16 * at) = v;
-      }
+      *reinterpret_cast<u32x4*>(row + 16 * own + 16 * at) = v;
     }
-    if (e.bad) __syncthreads();
   };
 
   f32x16 O[DT];
@@ -282,38 +318,78 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
   int ve = -100;                      // O is in units of 2^ve
   uint32_t nan_blocks = 0;            // blocks in which this row has seen a NaN
 
-  Loads L;
+  // the first two tiles' loads are in flight while the rows are brought to fp16
+  Loads L, L0;
+  uint32_t pg[ITEMS], pg0[ITEMS], pg1[ITEMS];
   TileExp cur{0, 0, false}, nxt{0, 0, false};
   if (st0 < st1) {
-    load(L, st0);
-    publish(L, st0 & 1);
+    load_pages(pg0, st0);
+    load_pages(pg1, st0 + 1);
+    load_pages(pg, st0 + 2);
+    load(L0, pg0, st0);
+    load(L, pg1, st0 + 1);
+  }
+  {
+    uint32_t mag = 0;
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      if (!ok) qf[k] = u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mag = max(mag, max(qf[k][x] & 0x7FFFu, (qf[k][x] >> 16) & 0x7FFFu));
+    }
+    mag = max(mag, (uint32_t)__shfl_xor((int)mag, 32, 64));
+    const int e = exponent_of(mag);
+    const float f = pow2(-e);
+    rs = a.scale * kLog2e * cp.inv * pow2(e);
+#pragma unroll
+    for (int k = 0; k < KK; ++k)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        qf[k][x] = pack_f16x2(__uint_as_float(qf[k][x] << 16) * f, __uint_as_float(qf[k][x] & 0xFFFF0000u) * f);
+  }
+  if (st0 < st1) {
+    publish(L0, st0);
     __syncthreads();
     cur = exps(st0 & 1);
-    decode(L, st0 & 1, cur);
-    if (st0 + 1 < st1) {
-      load(L, st0 + 1);
-      publish(L, (st0 + 1) & 1);
-    }
+    if (cur.bad) note_poison(L0, st0 & 1);
+    uint32_t sc[ITEMS][NKS];
+    scales(L0, cur, sc);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) decode(L0, st0 & 1, sc, x);
+    publish(L, st0 + 1);
   }
   for (int st = st0; st < st1; ++st) {
     const int par = st & 1, tok0 = t.base + st * kTile;
     __syncthreads();   // tile st is in LDS, tile st - 1 done with, tile st + 1's exponents published
-    if (st + 1 < st1) {
-      nxt = exps(par ^ 1);
-      decode(L, par ^ 1, nxt);
-      if (st + 2 < st1) load(L, st + 2);
-    }
+    nxt = exps(par ^ 1);   // (past the last tile: of an earlier one, and what is decoded is not used)
+    if (nxt.bad) note_poison(L, par ^ 1);
+    uint32_t sc[ITEMS][NKS];
+    scales(L, nxt, sc);
 
-    // S^T: 64 tokens x 32 rows
+    // S^T: 64 tokens x 32 rows; a key operand is read four products ahead of its own, and the next tile is decoded
+    // between the products
     f32x16 S[2];
 #pragma unroll
-    for (int tt = 0; tt < 2; ++tt) {
+    for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) S[tt][i] = 0.0f;
-      const unsigned char* kp = kt[par] + (tt * 32 + l32) * KS + 16 * h32;
+    // a wave in its products goes before the SIMD's other one, which then finds the matrix core free for its own (1% here)
+    __builtin_amdgcn_s_setprio(1);
+    const unsigned char* const kp = kt[par] + l32 * KS + 16 * h32;
+    constexpr int QK = 2 * KK, RING = 4;
+    u32x4 kf[RING];
+    auto read_k = [&](int n) { return *reinterpret_cast<const u32x4*>(kp + (n / KK) * 32 * KS + 32 * (n % KK)); };
 #pragma unroll
-      for (int k = 0; k < KK; ++k) S[tt] = mfma32h(*reinterpret_cast<const u32x4*>(kp + 32 * k), qf[k], S[tt]);
+    for (int n = 0; n < RING; ++n) kf[n] = read_k(n);
+#pragma unroll
+    for (int n = 0; n < QK; ++n) {
+      S[n / KK] = mfma32h(kf[n % RING], qf[n % KK], S[n / KK]);
+      if (n + RING < QK) kf[n % RING] = read_k(n + RING);
+      if (n % (QK / 4) == QK / 8) decode(L, par ^ 1, sc, n / (QK / 4));
     }
+    __builtin_amdgcn_s_setprio(0);
+    load(L, pg, st + 2);
+    load_pages(pg, st + 3);
     // register i of tile tt is token 32 tt + 8 (i / 4) + 4 h32 + i % 4
     const bool edge = tok0 < t.lo_max || tok0 + kTile > t.hi_min;
     if (edge) {
@@ -364,6 +440,7 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
     l = __builtin_fmaf(ls, back, l);
 
     // O^T += V^T P^T: 16 tokens at a time, slot (h32, j) of them token 4 h32 + j, or 8 + 4 h32 + j - 4 from j = 4 on
+    __builtin_amdgcn_s_setprio(1);
     const int G = lane >> 4, j = lane & 15;
     const unsigned char* vp = vt[par] + (4 * (G >> 1) + (j >> 2)) * VS + 2 * (16 * (G & 1) + 4 * (j & 3));
 #pragma unroll
@@ -379,13 +456,14 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
         O[d] = mfma32h(u32x4{w0.x, w0.y, w1.x, w1.y}, pf, O[d]);
       }
     }
+    __builtin_amdgcn_s_setprio(0);
     if (cur.bad) {   // rare: which blocks hold a NaN that this row sees
       for (int b = 0; b < NB; ++b)
         for (int n = 0; n < kTile; ++n)
           if ((poison[par][2 * b + (n >> 5)] >> (n & 31) & 1u) && tok0 + n < r_hi && tok0 + n >= r_lo) nan_blocks |= 1u << b;
     }
     cur = nxt;
-    if (st + 2 < st1) publish(L, par);
+    if (st + 1 < st1) publish(L, st + 2);
   }
 
   l = pair_sum(l) * pow2(-(int)kManyBits);
