@@ -84,11 +84,18 @@ __global__ __launch_bounds__(KT) void k_kv_write(Heads k, Heads v, KvView c, Bat
   const Slot<D> s = find_slot<D>(b, c, t0, r, cnt);
   if (!s.ok) return;
   const int nb = LR >> bl;   // blocks per row (1 << bl lanes each)
-  for (int item = blockIdx.y; item < 2 * c.heads; item += gridDim.y) {
+  auto load = [&](int item) {
     const bool key = item < c.heads;
     const int h = key ? item : item - c.heads;
     const Heads& x = key ? k : v;
-    const uint4 w = *reinterpret_cast<const uint4*>(x.data + (t0 + r) * x.rs + h * x.hs + e * 8);
+    return *reinterpret_cast<const uint4*>(x.data + (t0 + r) * x.rs + h * x.hs + e * 8);
+  };
+  uint4 next = load(blockIdx.y);
+  for (int item = blockIdx.y; item < 2 * c.heads; item += gridDim.y) {
+    const bool key = item < c.heads;
+    const int h = key ? item : item - c.heads;
+    const uint4 w = next;
+    if (item + (int)gridDim.y < 2 * c.heads) next = load(item + gridDim.y);   // the next head's row, a head ahead
     uint32_t u[8] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16, w.z & 0xFFFFu, w.z >> 16, w.w & 0xFFFFu, w.w >> 16};
     // largest magnitude: on bf16 bit patterns the magnitude order is the integer order
     uint32_t m = 0;

@@ -81,11 +81,17 @@ __device__ __forceinline__ void rotate(float (&v)[16], const Rot& r, float sign)
   }
 }
 
-// sum over the L lanes of a head
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+// sum over the L lanes of a head: lanes 1 and 2 away, then the other half of 8 and of 16 (mirrored)
 template <int L>
 __device__ __forceinline__ float head_sum(float v) {
-#pragma unroll
-  for (int off = 1; off < L; off <<= 1) v += __shfl_xor(v, off, 64);
+  v = dpp_add<0xB1>(v);
+  v = dpp_add<0x4E>(v);
+  if (L >= 8) v = dpp_add<0x141>(v);
+  if (L >= 16) v = dpp_add<0x140>(v);
   return v;
 }
 
@@ -135,9 +141,9 @@ __global__ __launch_bounds__(QT) void k_qk_norm_rope(QkArgs a) {
 // columns over all heads and rows it meets, the workgroup adds its lanes and waves in a fixed order
 // and writes one partial of both; k_qk_weight_grad adds the partials.
 template <int L, bool INTER>
-__global__ __launch_bounds__(QT) void k_qk_norm_rope_bwd(QkArgs a) {
+__global__ __launch_bounds__(QT, 4) void k_qk_norm_rope_bwd(QkArgs a) {
   constexpr int HP = 64 / L, D = 16 * L;
-  __shared__ float sum[QW][2][D];
+  __shared__ __attribute__((aligned(16))) float sum[QW][2][D];
   const int lane = threadIdx.x & 63, sub = lane & (L - 1), hl = lane / L, wave = threadIdx.x >> 6;
   int c0, c1;
   chunks_of(sub, a.rot, c0, c1);
@@ -185,15 +191,26 @@ __global__ __launch_bounds__(QT) void k_qk_norm_rope_bwd(QkArgs a) {
     }
   }
   if (!a.part) return;
+  // The wave's heads, halving the values with each exchange: lanes 32 .. 63 go on with the keys' weight, then odd rows of
+  // 16 lanes with the second chunk.  (Through LDS, 32 values over 64 / L heads each, it was 4 us of a call that takes 10.)
+  float v[16];
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
+  for (int i = 0; i < 16; ++i) {
+    auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(dw[0][i]), __float_as_uint(dw[1][i]), false, false);
+    v[i] = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+  }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float s = dw[t][i];
-#pragma unroll
-      for (int off = L; off < 64; off <<= 1) s += __shfl_xor(s, off, 64);
-      if (hl == 0) sum[wave][t][(i < 8 ? c0 : c1) * 8 + (i & 7)] = s;
-    }
+  for (int i = 0; i < 8; ++i) {
+    auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 8]), false, false);
+    v[i] = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    if (L <= 8) v[i] = dpp_add<0x128>(v[i]);   // row_ror 8
+    if (L <= 4) v[i] = dpp_add<0x124>(v[i]);   // row_ror 4
+  }
+  if ((lane & 15) < L) {
+    float* const p = &sum[wave][lane >> 5][(lane & 16 ? c1 : c0) * 8];
+    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * D; i += QT) {
     float s = 0.0f;
@@ -203,21 +220,34 @@ __global__ __launch_bounds__(QT) void k_qk_norm_rope_bwd(QkArgs a) {
   }
 }
 
-// dw[t][d] = sum over n partials [n][2][D]: 16 columns per workgroup, 16 threads per column.
-__global__ __launch_bounds__(QT) void k_qk_weight_grad(const float* __restrict__ part, int n, int D, float* dwq,
+// dw[t][d] = sum over n partials [n][2][D]: 16 columns per workgroup, 64 threads per column with up to 16 loads each in
+// flight (1024 partials are one round trip to memory).
+constexpr int WT = 1024, WR = WT / 16, WL = 16;
+__global__ __launch_bounds__(WT) void k_qk_weight_grad(const float* __restrict__ part, int n, int D, float* dwq,
                                                        float* dwk) {
-  __shared__ float sum[16][17];
-  const int col = blockIdx.x * 16 + (threadIdx.x & 15), r = threadIdx.x >> 4;
+  __shared__ float sum[WR][17];
+  const int c = threadIdx.x & 15, r = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
   float s = 0.0f;
-  for (int i = r; i < n; i += 16) s += part[(int64_t)i * 2 * D + col];
-  sum[r][threadIdx.x & 15] = s;
-  __syncthreads();
-  if (r == 0) {
-    s = 0.0f;
-    for (int i = 0; i < 16; ++i) s += sum[i][threadIdx.x];
-    float* out = col < D ? dwq : dwk;
-    if (out) out[col < D ? col : col - D] = s;
+  for (int i0 = r; i0 < n; i0 += WR * WL) {
+    float v[WL];
+#pragma unroll
+    for (int j = 0; j < WL; ++j) {
+      const int i = i0 + j * WR;
+      v[j] = i < n ? part[(int64_t)i * 2 * D + col] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < WL; ++j) s += v[j];
   }
+  sum[r][c] = s;
+  __syncthreads();
+  // wave w: column w
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  s = sum[lane][w];
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) s += __shfl_xor(s, off, 64);
+  const int out_col = blockIdx.x * 16 + w;
+  float* out = out_col < D ? dwq : dwk;
+  if (out && lane == 0) out[out_col < D ? out_col : out_col - D] = s;
 }
 
 int head_groups(int32_t q_heads, int32_t k_heads, int D) {
@@ -273,7 +303,7 @@ hipError_t launch_qk_bwd(const QkArgs& a0, int D, bool inter, float* dwq, float*
   }
   if (!a.part) return hipSuccess;
   ProfScope ps("k_qk_weight_grad", s);
-  hipLaunchKernelGGL(k_qk_weight_grad, dim3((unsigned)(2 * D / 16)), dim3(QT), 0, s, a.part, grid, D, dwq, dwk);
+  hipLaunchKernelGGL(k_qk_weight_grad, dim3((unsigned)(2 * D / 16)), dim3(WT), 0, s, a.part, grid, D, dwq, dwk);
   return hipGetLastError();
 }
 
