@@ -95,15 +95,16 @@ struct AttnArgs {
   int32_t ushift;                 // log2 of the unit of work in steps of every wave
   int32_t few;                    // rows per cache head up to which a sequence is the first kernel's
   float* part;                    // partial sums of ranges that end inside an item
-  int32_t* meta;                  // [workgroups][kMetaInts]
+  int32_t* meta;                  // [workgroups][kMetaInts] (second kernel: [1 + tiles])
 };
 // Sizes of a launch, from what the host knows.
 struct AttnPlan {
   int tile;                       // query rows per tile (row = token and query head of one cache head)
   int ushift, few;                // as in AttnArgs; few = INT32_MAX: the first kernel alone, 0: the second alone
   int64_t wgs;                    // workgroups of the first kernel's ranges
-  int64_t many_items;             // tiles x cache heads of the second kernel at most
-  int splits;                     // parts that the tokens of each are cut into
+  int64_t many_wgs;               // workgroups of the second kernel, its tiles x cache heads at most
+  int64_t many_split;             // how many of these it may cut into parts: 0 (no join), or up to kSplitWgs / 2
+  bool sparse;                    // its tiles are mostly less than half full
   size_t part_floats, meta_ints;  // workspace, and where the second kernel's share of it begins
   size_t many_part, many_meta;
 };

@@ -225,6 +225,10 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, int n, int rows, int
     a.lse[(mt[1] + i) * (int64_t)a.q.n + qh] = l == 0.0f ? neg_inf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
+// The kernel for many rows cuts the tokens of its tiles into parts of at least kSplitTokens where kSplitWgs workgroups have
+// two or more for each.
+constexpr int kSplitTokens = 256, kSplitWgs = 256;
+
 // Threads of a workgroup of the kernel for many rows: 32 rows of a tile to a wave, 8 waves where the registers allow two
 // waves per SIMD, 4 otherwise.
 constexpr int many_threads(int D) { return D == 256 ? 256 : 512; }

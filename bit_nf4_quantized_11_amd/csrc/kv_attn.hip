@@ -40,10 +40,8 @@ static_assert(kStep * AW == 1 << kUnitShift, "a unit is one step of every wave")
 // Waves per SIMD, and the workgroups of a launch: as many as are resident then.  The registers of a step's loads,
 // operands and sums decide: D = 64 fits three without spilling (16 sequences of 16 k tokens, 8 cache heads: 45 us, 48
 // with two waves), 128 and 256 two (82 and 153 us; 84 and 348 with three and the spills, 98 and 184 with one).
-template <int D>
-constexpr int kWaves = D == 64 ? 3 : 2;
+constexpr int waves_of(int D, int NR) { return D == 64 && NR == 1 ? 3 : 2; }
 constexpr int64_t kCUs = 256;
-int64_t resident_wgs(int D) { return kCUs * (D == 64 ? kWaves<64> : kWaves<128>); }
 
 // Probabilities are held times 2^13 (with a scale, up to twice its power of two, below fp16's 65504), so that ones
 // down to 2^-27 of the largest keep all their bits and ones below 2^-38 of it are lost.
@@ -116,7 +114,7 @@ struct StepLoads {
 };
 
 template <int D, int NB, int NR>
-__global__ __launch_bounds__(AT, kWaves<D>) void k_kv_attn(AttnArgs a, CodePlanes cp) {
+__global__ __launch_bounds__(AT, waves_of(D, NR)) void k_kv_attn(AttnArgs a, CodePlanes cp) {
   constexpr int TR = 16 * NR, B = D / NB, KK = D / 32, UN = D / 16;
   constexpr int RB = D / 2;                // bytes of a cache row
   constexpr int CH = RB / 16;              // 16-byte chunks of a row
@@ -691,64 +689,79 @@ CodePlanes code_planes(int cb) {
 // Sequences with at most kFew rows per cache head go to the kernel of this file, those with more to the one for many rows.
 // The host knows the rows and the sequences of a call, not which has how many: where the mean is low it leaves all of
 // them to the first kernel (which is right for any), with one sequence all to one, otherwise it launches both.
-constexpr int kFew = 32;
+// 16 sequences of 4096 tokens, 8 cache heads, this kernel and the other one: D = 128, 40 rows 56 and 76 us, 64 rows 58 and 78,
+// 96 rows 105 and 83; D = 64, 64 rows 39 and 72, 96 rows 56 and 75; D = 256, 64 rows 72 and 93, 96 rows 106 and 96.
+constexpr int kFew = 64;
 
 AttnPlan attn_plan(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t batch, int64_t max_len, int D) {
   AttnPlan p{};
   const int64_t rows_h = rows * (q_heads / kv_heads), nseq = batch > 1 ? batch : 1;
   if (rows_h <= kFew * nseq) p.few = INT32_MAX;
   else p.few = nseq == 1 ? 0 : kFew;
-  p.tile = 16;
+  // Tiles of 32 rows decode a token once for twice the rows, but make half the units: they are taken where sequences have more
+  // than 16 rows and every workgroup still has two units.  16 sequences of 4096, 8 cache heads of 128, 32 and 64
+  // rows of each: 39 and 58 us (43 and 70 with tiles of 16); one sequence 21 and 25 us (17 and 23).  D = 256 has no
+  // registers for it.
+  const int64_t units32 = nseq * kv_heads * ((max_len >> kUnitShift) + 1);
+  const int nr = D < 256 && rows_h > 16 * nseq && units32 >= 2 * kCUs * waves_of(D, 2) ? 2 : 1;
+  p.tile = 16 * nr;
   if (p.few > 0) {
     const int64_t tiles = ((rows_h + p.tile - 1) / p.tile + nseq) * kv_heads;
     // units so large that their number stays below 2^30
     while (tiles * ((max_len >> (kUnitShift + p.ushift)) + 1) >= int64_t(1) << 30 && p.ushift < 22) ++p.ushift;
     const int64_t units = (max_len >> (kUnitShift + p.ushift)) + 1;
-    p.wgs = resident_wgs(D);
+    p.wgs = kCUs * waves_of(D, nr);
     if (tiles * units < p.wgs) p.wgs = tiles * units;
     p.part_floats = (size_t)p.wgs * 2 * p.tile * (D + 2);
     p.meta_ints = (size_t)p.wgs * kMetaInts;
   }
-  p.splits = 1;
   if (p.few != INT32_MAX) {
     const int tr = many_threads(D) / 2;
-    const int64_t most = rows_h / (p.few + 1) + 1;   // sequences that can have more than `few` rows
-    p.many_items = (rows_h / tr + (most < nseq ? most : nseq)) * kv_heads;
-    // fewer tiles than CUs: the tokens of a tile in parts of at least 512
-    const int64_t parts = (max_len + 511) / 512;
-    if (p.many_items <= kCUs / 2) p.splits = (int)(parts < kCUs / p.many_items ? parts : kCUs / p.many_items);
-    if (p.splits > 1) {
+    const int64_t most = rows_h / ((int64_t)p.few + 1) + 1;   // sequences that can have more than `few` rows
+    p.many_wgs = (rows_h / tr + (most < nseq ? most : nseq)) * kv_heads;
+    p.sparse = p.many_wgs * tr >= 2 * rows_h * kv_heads;
+    const int64_t least = (rows_h - p.few * nseq) / tr * kv_heads;   // tiles that there are, if all rows are a sequence's
+    if (max_len >= 2 * kSplitTokens && least <= kSplitWgs / 2) {
+      p.many_split = p.many_wgs < kSplitWgs / 2 ? p.many_wgs : kSplitWgs / 2;
+      if (p.many_wgs < kSplitWgs) p.many_wgs = kSplitWgs;
       p.many_part = p.part_floats;
       p.many_meta = p.meta_ints;
-      p.part_floats += (size_t)p.many_items * p.splits * tr * (D + 2);
-      p.meta_ints += (size_t)p.many_items * kMetaInts;
+      p.part_floats += (size_t)kSplitWgs * tr * (D + 2);
+      p.meta_ints += (size_t)(1 + p.many_split) * kMetaInts;
     }
   }
   return p;
 }
 
-template <int D, int NB>
+template <int D, int NB, int NR>
 static hipError_t launch_attn(const AttnArgs& a0, const AttnPlan& pl, hipStream_t s) {
   AttnArgs a = a0;
   a.ushift = pl.ushift;
   a.few = pl.few;
   {
     ProfScope ps("k_kv_attn", s);
-    hipLaunchKernelGGL((k_kv_attn<D, NB, 1>), dim3((unsigned)pl.wgs), dim3(AT), 0, s, a, code_planes(a.c.cb));
+    hipLaunchKernelGGL((k_kv_attn<D, NB, NR>), dim3((unsigned)pl.wgs), dim3(AT), 0, s, a, code_planes(a.c.cb));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   ProfScope ps("k_kv_attn_join", s);
-  hipLaunchKernelGGL((k_kv_attn_join<D, 16>), dim3((unsigned)pl.wgs, 4), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((k_kv_attn_join<D, 16 * NR>), dim3((unsigned)pl.wgs, 4 * NR), dim3(256), 0, s, a);
   return hipGetLastError();
+}
+template <int D, int NB>
+static hipError_t launch_tile(const AttnArgs& a, const AttnPlan& pl, hipStream_t s) {
+  if constexpr (D < 256) {
+    if (pl.tile == 32) return launch_attn<D, NB, 2>(a, pl, s);
+  }
+  return launch_attn<D, NB, 1>(a, pl, s);
 }
 
 static hipError_t launch_few(const AttnArgs& a, const AttnPlan& pl, int D, int block, hipStream_t s) {
   const int nb = D / block;
-  if (D == 64) return nb == 1 ? launch_attn<64, 1>(a, pl, s) : launch_attn<64, 2>(a, pl, s);
+  if (D == 64) return nb == 1 ? launch_tile<64, 1>(a, pl, s) : launch_tile<64, 2>(a, pl, s);
   if (D == 128)
-    return nb == 1 ? launch_attn<128, 1>(a, pl, s) : nb == 2 ? launch_attn<128, 2>(a, pl, s) : launch_attn<128, 4>(a, pl, s);
-  return nb == 2 ? launch_attn<256, 2>(a, pl, s) : nb == 4 ? launch_attn<256, 4>(a, pl, s) : launch_attn<256, 8>(a, pl, s);
+    return nb == 1 ? launch_tile<128, 1>(a, pl, s) : nb == 2 ? launch_tile<128, 2>(a, pl, s) : launch_tile<128, 4>(a, pl, s);
+  return nb == 2 ? launch_tile<256, 2>(a, pl, s) : nb == 4 ? launch_tile<256, 4>(a, pl, s) : launch_tile<256, 8>(a, pl, s);
 }
 
 hipError_t launch_kv_attn(const AttnArgs& a, const AttnPlan& pl, int D, int block, hipStream_t s) {

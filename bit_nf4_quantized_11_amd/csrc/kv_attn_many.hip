@@ -60,9 +60,9 @@ struct ManyLoads {
   uint32_t s[ITEMS][(NKS + 1) / 2];                        // bf16 scales (a value chunk has one)
 };
 
-template <int D, int NB>
+template <int D, int NB, bool SKIP>
 __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_attn_many(AttnArgs a, CodePlanes cp0,
-                                                                                        int splits) {
+                                                                                        bool split) {
   using Loads = ManyLoads<D, NB>;
   constexpr int T = Loads::T, MW = T / 64, TR = 32 * MW, B = D / NB, CH = Loads::CH, ITEMS = Loads::ITEMS;
   constexpr int NKS = Loads::NKS, KN = Loads::KN, KK = D / 16, DT = D / 32, RB = D / 2;
@@ -83,26 +83,47 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, h32 = lane >> 5;
 
-  // this workgroup's tile: item = ((tile of the call) * heads + head) * splits + part
-  const int item = blockIdx.x / splits, part = blockIdx.x - item * splits;
-  const int tile_at = item / a.c.heads, h = item - tile_at * a.c.heads;
-  int c0 = 0;
+  // All tiles of the call and the longest cache among them: from these, in how many parts each tile is cut.
   auto tiles = [&](const Seq& s) -> int {
     const int64_t rows = (int64_t)s.n * a.group;
     return rows > a.few ? (int)((rows + TR - 1) / TR) : 0;
   };
+  if (threadIdx.x == 0) found = 0;
   if (blockIdx.x == 0) check_batch_entries<T>(a.b);
-  scan_seqs(a.b, 0, 0, seqs, tiles);
-  while (seqs.pre[T] <= tile_at) {
-    const int base = seqs.pre[T];
-    if (c0 + T >= a.b.batch) {
-      if (splits > 1 && part == 0 && threadIdx.x == 0) a.meta[item * kMetaInts + 3] = 0;   // no such tile
-      return;
-    }
+  int c0 = 0, total = 0;
+  for (;;) {
+    scan_seqs(a.b, c0, total, seqs, tiles);
+    total = __builtin_amdgcn_readfirstlane(seqs.pre[T]);
+    if (split && c0 + threadIdx.x < a.b.batch && tiles(Seq{0, seqs.n[threadIdx.x], 0})) atomicMax(&found, seqs.len[threadIdx.x]);
     __syncthreads();
+    if (c0 + T >= a.b.batch) break;
     c0 += T;
-    scan_seqs(a.b, c0, base, seqs, tiles);
   }
+  int splits = 1;
+  if (split) {
+    const int most = __builtin_amdgcn_readfirstlane(found) / kSplitTokens;
+    if (total <= kSplitWgs / a.c.heads) splits = max(min(most, kSplitWgs / max(total * a.c.heads, 1)), 1);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      a.meta[0] = total;
+      a.meta[1] = splits;
+    }
+  }
+  // this workgroup's tile: item = ((tile of the call) * heads + head) * splits + part
+  const int item = blockIdx.x / splits, part = blockIdx.x - item * splits;
+  const int tile_at = item / a.c.heads, h = item - tile_at * a.c.heads;
+  if (tile_at >= total) return;
+  if (a.b.batch > T) {
+    c0 = 0;
+    int base = 0;
+    for (;;) {
+      __syncthreads();
+      scan_seqs(a.b, c0, base, seqs, tiles);
+      base = seqs.pre[T];
+      if (base > tile_at) break;
+      c0 += T;
+    }
+  }
+  __syncthreads();
   if (seqs.pre[threadIdx.x] <= tile_at && tile_at < seqs.pre[threadIdx.x + 1]) found = threadIdx.x;
   __syncthreads();
   const int bi = __builtin_amdgcn_readfirstlane(found);
@@ -117,6 +138,8 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
   const int rho = t.rho0 + (ok ? rr : 0), ri = rho / a.group, qh = h * a.group + (rho - ri * a.group);
   const int len = s.len < 0 ? 0 : s.len, pos = len - s.n + ri;
   const int r_hi = !ok ? 0 : a.causal ? pos + 1 : len, r_lo = a.window ? pos + 1 - a.window : 0;
+  // tokens that some row of this wave sees
+  const int w_hi = (int)wave_max((uint32_t)max(r_hi, 0)), w_lo = __builtin_amdgcn_readfirstlane(r_lo);
   u32x4 qf[KK];
   float rs;                               // logit (in log2) of one unit of its products, but for the keys' exponent
   {
@@ -366,6 +389,16 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
     uint32_t sc[ITEMS][NKS];
     scales(L, nxt, sc);
 
+    if (SKIP && (tok0 >= w_hi || tok0 + kTile <= w_lo)) {   // nothing that this wave's rows see
+#pragma unroll
+      for (int x = 0; x < 4; ++x) decode(L, par ^ 1, sc, x);
+      load(L, pg, st + 2);
+      load_pages(pg, st + 3);
+      cur = nxt;
+      if (st + 1 < st1) publish(L, st + 2);
+      continue;
+    }
+
     // S^T: 64 tokens x 32 rows; a key operand is read four products ahead of its own, and the next tile is decoded
     // between the products
     f32x16 S[2];
@@ -468,8 +501,8 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
 
   l = pair_sum(l) * pow2(-(int)kManyBits);
   const float ofs = pow2(ve - (int)kManyBits) * cp.inv;
+  if (!ok) return;
   if (splits == 1) {
-    if (!ok) return;
     float inv = l == 0.0f ? 0.0f : ofs / l;
     if (s.len < 0) inv = __builtin_nanf("");
     uint16_t* op = a.o.data + (s.row0 + ri) * a.o.rs + qh * a.o.hs + 4 * h32;
@@ -502,8 +535,8 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
     dst[TR * D + rr] = m;
     dst[TR * D + TR + rr] = s.len < 0 ? __builtin_nanf("") : l;
   }
-  if (part == 0 && threadIdx.x == 0) {
-    int32_t* mt = a.meta + item * kMetaInts;
+  if (part == 0 && threadIdx.x == 0) {   // (its row is always there)
+    int32_t* mt = a.meta + (1 + item) * kMetaInts;
     mt[1] = (int32_t)s.row0;
     mt[2] = t.rho0;
     mt[3] = t.nval;
@@ -513,9 +546,11 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
 
 // Adds the parts of a tile: workgroup (item, y), wave v row 4y + v.
 template <int D>
-__global__ __launch_bounds__(256) void k_kv_attn_many_join(AttnArgs a, int splits) {
+__global__ __launch_bounds__(256) void k_kv_attn_many_join(AttnArgs a) {
   constexpr int TR = many_threads(D) / 2;
-  const int32_t* mt = a.meta + blockIdx.x * kMetaInts;
+  const int splits = a.meta[1];
+  if (splits == 1 || (int)blockIdx.x / a.c.heads >= a.meta[0]) return;
+  const int32_t* mt = a.meta + (1 + blockIdx.x) * kMetaInts;
   const int rr = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (rr >= mt[3]) return;
   constexpr int64_t P = TR * (D + 2);
@@ -529,14 +564,16 @@ template <int D, int NB>
 static hipError_t launch_many(const AttnArgs& a, const AttnPlan& pl, hipStream_t s) {
   {
     ProfScope ps("k_kv_attn_many", s);
-    hipLaunchKernelGGL((k_kv_attn_many<D, NB>), dim3((unsigned)(pl.many_items * pl.splits)), dim3(many_threads(D)), 0, s, a,
-                       code_planes(a.c.cb), pl.splits);
+    const dim3 g((unsigned)pl.many_wgs), t(many_threads(D));
+    const CodePlanes cp = code_planes(a.c.cb);
+    // (for D = 256 the second loop body spills registers: 16 sequences of 40 rows 305 us, 289 without it)
+    if (D < 256 && pl.sparse) hipLaunchKernelGGL((k_kv_attn_many<D, NB, D < 256>), g, t, 0, s, a, cp, pl.many_split > 0);
+    else hipLaunchKernelGGL((k_kv_attn_many<D, NB, false>), g, t, 0, s, a, cp, pl.many_split > 0);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || pl.splits == 1) return e;
+    if (e != hipSuccess || !pl.many_split) return e;
   }
   ProfScope ps("k_kv_attn_many_join", s);
-  hipLaunchKernelGGL((k_kv_attn_many_join<D>), dim3((unsigned)pl.many_items, many_threads(D) / 8), dim3(256), 0, s, a,
-                     pl.splits);
+  hipLaunchKernelGGL((k_kv_attn_many_join<D>), dim3((unsigned)pl.many_split, many_threads(D) / 8), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
