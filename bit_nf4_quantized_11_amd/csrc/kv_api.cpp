@@ -14,6 +14,7 @@ using namespace qlora;
 
 namespace {
 
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int64_t kMaxRows = int64_t(1) << 26;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 constexpr int32_t kMaxHeads = 1024;
@@ -82,7 +83,8 @@ KvView cache_view(const qlora_kv_cache* c) {
 qlora_status check_batch_sizes(const qlora_kv_batch* b, const qlora_kv_cache* c) {
   if (!b) return QLORA_ERR_NULL;
   if (b->batch < 0 || b->batch > 65536 || b->max_pages < 1) return QLORA_ERR_SHAPE;
-  if ((int64_t)b->max_pages * c->page_size >= (int64_t(1) << 31)) return QLORA_ERR_SHAPE;
+  // token indexes a few tiles past the last one, and sums of a position and a window, stay within 32 bits
+  if ((int64_t)b->max_pages * c->page_size > kMaxTokens) return QLORA_ERR_SHAPE;
   return QLORA_OK;
 }
 
@@ -327,7 +329,8 @@ qlora_status qlora_kv_attn(const qlora_heads* q, int64_t rows, const qlora_kv_ca
   a.group = q->heads / cache->heads;
   a.scale = scale;
   a.causal = causal;
-  a.window = window;
+  // (a window that no cache of this batch outgrows is none)
+  a.window = window < (int64_t)batch->max_pages * cache->page_size ? window : 0;
   a.part = w.part;
   a.meta = w.meta;
   QL_HIP(launch_kv_attn(a, p, cache->head_dim, cache_block(cache), stream));

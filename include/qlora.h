@@ -337,7 +337,7 @@ qlora_status qlora_kv_sizes(const qlora_kv_cache* cache, size_t* codes_bytes, si
  *   - a length outside 0 .. max_pages * page_size: nothing is written, rows read and attend NaN (bit 1);
  *   - a page outside 0 .. pages - 1: not written, reads NaN, every row that sees it attends NaN (bit 2);
  * and the bit is OR-ed into *fault if that is not NULL (the caller clears it).
- * Requires: batch 0..65536, max_pages >= 1, max_pages * page_size < 2^31, 4-byte aligned arrays.      */
+ * Requires: batch 0..65536, max_pages >= 1, max_pages * page_size <= 2^30, 4-byte aligned arrays.     */
 typedef struct {
   int32_t batch;
   int32_t max_pages;

@@ -296,6 +296,7 @@ def test_kv_validation(lib):
         assert call(fn, c=_cache(pages=0)) == 2 and call(fn, c=_cache(heads=0)) == 2 and call(fn, c=_cache(pages=1 << 31)) == 2
         assert call(fn, b=_batch(batch=-1)) == 2 and call(fn, b=_batch(batch=65537)) == 2
         assert call(fn, b=_batch(max_pages=0)) == 2 and call(fn, b=_batch(max_pages=1 << 27)) == 2
+        assert call(fn, rows=0, b=_batch(max_pages=1 << 26)) == 0 and call(fn, b=_batch(max_pages=(1 << 26) + 1)) == 2
         for c in (_cache(dim=32), _cache(dim=96), _cache(block=16), _cache(block=256), _cache(dim=64, block=128), _cache(cb=3),
                   _cache(cb=-1), _cache(page=8), _cache(page=48), _cache(page=1 << 21), _cache(page=0)):
             assert call(fn, c=c) == 4
