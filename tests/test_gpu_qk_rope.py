@@ -185,3 +185,68 @@ def test_no_rows_and_non_finite_heads():
     q, _ = Q.qlora_qk_norm_rope(x, None, pos, freq, w)
     good = torch.isfinite(q.float()).all(-1)
     assert good.sum() == 5 and not good[0, 1]
+
+
+def test_captured_forward_and_backward():
+    """Both in one captured graph with the workspace passed in, replayed with other inputs, positions and eager calls
+    between (which use the same workspace): the eager bits every time."""
+    require_gpu()
+    rows, hq, hk, dim = 300, 6, 2, 64
+    t = [dev_bf16(bits(i, (rows, h, dim))) for i, h in enumerate((hq, hk, hq, hk))]
+    new = [[dev_bf16(bits(10 * j + i, x.shape)) for i, x in enumerate(t)] for j in (1, 2, 3)]
+    pos = torch.arange(rows, device="cuda")
+    freq = torch.tensor(10000.0 ** (-np.arange(32) / 32), dtype=torch.float32, device="cuda")
+    w = [dev_bf16(bits(40 + i, (dim,))) for i in range(2)]
+    ws = torch.empty(Q.qlora_qk_norm_rope_bwd_workspace(rows, hq, hk, dim), dtype=torch.uint8, device="cuda")
+
+    def run():
+        return (*Q.qlora_qk_norm_rope(t[0], t[1], pos, freq, *w),
+                *Q.qlora_qk_norm_rope_bwd(t[2], t[3], t[0], t[1], pos, freq, *w, workspace=ws))
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = run()
+    for values in new:
+        for x, y in zip(t, values):
+            x.copy_(y)
+        pos.add_(77)
+        eager = [x.clone() for x in run()]
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, eager))
+
+
+def test_binding_refusals():
+    """What the binding refuses before any launch."""
+    require_gpu()
+    x = torch.zeros(5, 3, 64, dtype=torch.bfloat16, device="cuda")
+    pos, freq = torch.arange(5, device="cuda"), torch.ones(16, device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    for bad in (x.float(), x.cpu(), x[0], x[..., ::2], torch.zeros(5, 3, 96, dtype=torch.bfloat16, device="cuda")):
+        with pytest.raises(Q.QLoRAError):
+            Q.qlora_qk_norm_rope(bad, None, pos, freq)
+        with pytest.raises(Q.QLoRAError):
+            Q.qlora_qk_norm_rope(x, None, pos, freq, q_out=bad)
+        with pytest.raises(Q.QLoRAError):
+            Q.qlora_qk_norm_rope_bwd(x, None, bad, None, pos, freq, w)
+    for args in ((None, freq), (pos.int(), freq), (pos[:4], freq), (pos.cpu(), freq), (pos, freq.double()),
+                 (pos, freq.cpu()), (pos, torch.ones(12, device="cuda")), (pos, torch.ones(40, device="cuda"))):
+        with pytest.raises(Q.QLoRAError):
+            Q.qlora_qk_norm_rope(x, x, *args)
+    for bad in (w.float(), w[:32], w.cpu()):
+        with pytest.raises(Q.QLoRAError):
+            Q.qlora_qk_norm_rope(x, None, pos, freq, bad)
+    for kw in ({"k_weight": w}, {"k_out": x.clone()}, {"eps": -1.0}, {"eps": float("nan")}):
+        with pytest.raises(Q.QLoRAError):
+            Q.qlora_qk_norm_rope(x, None, pos, freq, **kw)
+    with pytest.raises(Q.QLoRAError):
+        Q.qlora_qk_norm_rope(x, x[:4], pos, freq)
+    for kw in ({"q_weight": w}, {"k_weight": w}, {"dk": x.clone()}, {"dq_weight": torch.zeros(64, device="cuda")},
+               {"q_weight": w, "dq_weight": torch.zeros(32, device="cuda")},
+               {"q_weight": w, "workspace": torch.empty(64, dtype=torch.uint8, device="cuda")}):
+        q = x if "dq_weight" in kw or "workspace" in kw else None
+        with pytest.raises(Q.QLoRAError):
+            Q.qlora_qk_norm_rope_bwd(x, None, q, None, pos, freq, **kw)
