@@ -305,7 +305,15 @@ def _heads(t: torch.Tensor, name: str, device=None, shape=None) -> _lib.qlora_he
         raise QLoRAError(f"{name} must be on {device}")
     if shape is not None and t.shape != shape:
         raise QLoRAError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    return _lib.qlora_heads(t.data_ptr(), strides[0], strides[1], t.shape[1], 0)
+    return _lib.qlora_heads(t.data_ptr(), strides[0], strides[1], t.size(1), 0)
+
+
+def _out(given, name: str, device, shape):
+    """An output and its view: the caller's, checked, or a new contiguous one."""
+    if given is not None:
+        return given, _heads(given, name, device, shape)
+    t = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    return t, _lib.qlora_heads(t.data_ptr(), shape[1] * shape[2], shape[2], shape[1], 0)
 
 
 def _ref(x):
@@ -444,10 +452,8 @@ def qlora_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch
         raise QLoRAError("k_out needs k")
 
     def run(stream):
-        qo = q.new_empty(q.shape) if q_out is None else q_out
-        ko = k_out if k is None or k_out is not None else k.new_empty(k.shape)
-        oq = _heads(qo, "q_out", dev, q.shape)
-        ok = None if k is None else _heads(ko, "k_out", dev, k.shape)
+        qo, oq = _out(q_out, "q_out", dev, q.shape)
+        ko, ok = (None, None) if k is None else _out(k_out, "k_out", dev, k.shape)
         _check(lib().qlora_qk_norm_rope(_ref(hq), _ref(hk), rows, dim, _ptr(q_weight), _ptr(k_weight), eps,
                                         _ptr(positions), _ptr(inv_freq), rot, interleaved, _ref(oq), _ref(ok), stream),
                "qlora_qk_norm_rope")
@@ -483,8 +489,8 @@ def qlora_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q:
         raise QLoRAError("a weight's gradient needs the weight")
 
     def run(stream):
-        oq = dq_out.new_empty(dq_out.shape) if dq is None else dq
-        ok = dk if dk_out is None or dk is not None else dk_out.new_empty(dk_out.shape)
+        oq, hq = _out(dq, "dq", dev, dq_out.shape)
+        ok, hk = (None, None) if dk_out is None else _out(dk, "dk", dev, dk_out.shape)
         gwq, gwk = dq_weight, dk_weight
         if q_weight is not None:
             gwq = torch.empty(dim, dtype=torch.float32, device=dev) if gwq is None else \
@@ -492,8 +498,6 @@ def qlora_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q:
         if k_weight is not None:
             gwk = torch.empty(dim, dtype=torch.float32, device=dev) if gwk is None else \
                 _need(gwk, torch.float32, dev, "dk_weight", (dim,))
-        hq = _heads(oq, "dq", dev, dq_out.shape)
-        hk = None if dk_out is None else _heads(ok, "dk", dev, dk_out.shape)
         ws = None
         if q_weight is not None or k_weight is not None:
             ws = _bytes(workspace, dev, lambda: qlora_qk_norm_rope_bwd_workspace(
@@ -525,9 +529,8 @@ def qlora_kv_read(cache: KVCache, batch: KVBatch, rows: int, k: torch.Tensor | N
     shape = (rows, cache.heads, cache.head_dim)
 
     def run(stream):
-        ko = cache.k_scale.new_empty(shape) if k is None else k
-        vo = cache.k_scale.new_empty(shape) if v is None else v
-        hk, hv = _heads(ko, "k", dev, shape), _heads(vo, "v", dev, shape)
+        ko, hk = _out(k, "k", dev, shape)
+        vo, hv = _out(v, "v", dev, shape)
         _check(lib().qlora_kv_read(_ref(cache.desc()), _ref(batch.desc()), rows, _ref(hk), _ref(hv), stream),
                "qlora_kv_read")
         return ko, vo
@@ -550,8 +553,7 @@ def qlora_kv_attn(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float 
     rows, heads = q.shape[0], q.shape[1]
 
     def run(stream):
-        o = q.new_empty(q.shape) if out is None else out
-        ho = _heads(o, "out", dev, q.shape)
+        o, ho = _out(out, "out", dev, q.shape)
         sums = None
         if lse is True:
             sums = torch.empty((rows, heads), dtype=torch.float32, device=dev)
