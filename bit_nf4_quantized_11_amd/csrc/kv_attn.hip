@@ -12,21 +12,27 @@
 //
 // A wave takes 64 tokens at a time, on its own (no barrier until the end of a tile):
 //   S^T = K Q^T (16x16x32 MFMA, K as the row operand): a lane holds the codes of one token's 32
-//     elements in one 16-byte load (the key rows' dword order), decodes them to bf16 by byte
-//     permutes of a constant table, and the block's scale is applied to the accumulators, 4 tokens per lane,
+//     elements in one 16-byte load (the key rows' dword order), decodes them to fp16 by lookups of
+//     pairs of codes in LDS, and the block's scale is applied to the accumulators, 4 tokens per lane,
 //     instead of to 32 elements;
 //   P^T falls out of that in the layout that the next product's column operand has: which token is which
 //     row of the S^T tiles is chosen so that lane group g holds tokens 16g .. 16g + 15;
 //   O^T = V^T P^T: the value codes go through LDS as they are and come back transposed by nibbles
 //     (ds_read_b64_tr_b4: a lane gets 16 tokens of one element), so 4 bits per element cross LDS instead
-//     of 16; the scale of a value depends on the token, the reduction index here, so it is multiplied
-//     into P, once per block.
+//     of 16, and are decoded by byte permutes (the keys' lookups leave LDS no time for theirs); the scale of a
+//     value depends on the token, the reduction index here, so it is multiplied into P, once per block.
 // The products are in fp16, not bf16: its 11 bits bring the level tables (times 6 for FP4 and 7 for Int4, which
 // makes them exact) and the probabilities 8 times closer, and the output's error down to little more than
 // its own rounding to bf16 (with bf16 operands it was twice that).  What fp16 lacks is range, so every operand is
 // brought to about 1 by a power of two first: a row of q by its own largest element (all 8 bits of elements down to
 // 2^-17 of it stay), the scaled probabilities of a step by the largest scale so far of that
 // block of elements (a running exponent, like the running maximum, that all rows share).
+//
+// Measured: 16 sequences of up to 32768 tokens (311 k in all, 338 MB), 64 query on 8 cache heads of 128: 87 us of this
+// kernel = 3.9 TB/s and 2 of the join, where a large copy reaches 4.8: the steps are bound by HBM (a step's 18.9 MB in
+// 4 us when all 2048 waves are in theirs), VALU issue close behind; the start of a range (lengths, then table, then codes: three
+// round trips) and the end of each tile (four waves' sums) cost about 6 us of a call.  Sixteen sequences of 4096: 22 us
+// of 15 at copy rate; one of 777 tokens 6 us, all of it that chain.
 #include "kv_attn.h"
 
 namespace qlora {

@@ -9,15 +9,20 @@
 // product's operand as it stands (its token order is the accumulator's; the values are read to match, transposed by
 // ds_read_b64_tr_b16).  The maximum is moved only when one grows by more than 2^6, so that the sums are rarely rescaled.
 //
-// Per wave and 64 tokens (D = 128) the matrix cores take 1024 cycles and the other instructions, about 400 VALU and 90
-// scalar ones, 1800 of issue for the SIMD's two waves: bound by the issue of VALU instructions, the matrix cores next.
-// Measured: 16384 rows of one sequence, 32 query on 8 cache heads of 128, causal, 2.46 to 2.54 ms = 865 to 890 TFLOP/s
-// (a square library product of 8192 reaches 1190); 4 x 4096 rows 0.78 ms, 705; heads of 64 0.50 ms, 546 (twice the
-// exponentials and decoding per product); heads of 256 454 (4 waves to a CU: 512 registers each).  A workgroup's start,
-// its first tile and its end cost 12 to 15 us, which is what short sequences pay: 1024 rows 46 us.
+// Per 64 tokens and SIMD (D = 128, two waves) the matrix cores take 2048 cycles, about 400 VALU instructions of each
+// wave 3700 with the exponentials' 16 each, LDS 2250: of 5800 in all.  Bound by the issue of VALU instructions, which
+// the matrix products of the other wave overlap in part.
+// Measured: 16384 rows of one sequence, 32 query on 8 cache heads of 128, causal, 2.49 to 2.6 ms = 850 to 884 TFLOP/s
+// (a square library product of 8192 reaches 1190); 4 x 4096 rows 0.78 ms, 705; heads of 64 0.51 ms, 543 (twice the
+// exponentials and decoding per product); heads of 256 447 (4 waves to a CU with 512 registers each: nothing overlaps a wave's
+// waits).  A workgroup's start, its first tile and its end cost 12 to 15 us, which is what short sequences pay: 1024 rows 46 us.
 //
-// One workgroup per tile; with up to 128 tiles (half the CUs) the tokens of a tile are cut into `splits` parts, whose sums
-// k_kv_attn_many_join adds.
+// One workgroup per tile of a sequence.  Each finds all tiles of the call from the device's lengths; where there are no more
+// than half as many as CUs, the tokens of every tile are cut into parts for all of them, whose sums k_kv_attn_many_join adds (2
+// sequences of 8192, 512 rows of each, 197 us; 290 with the tiles whole).
+// SKIP: waves pass over tokens that none of their rows sees, for tiles that are mostly empty: a wave without rows then decodes
+// only (64 sequences of 4096, 12 rows each of 4 query heads per cache head, 246 us; 319 without).  Full tiles do better without
+// the second loop body: 16384 rows 2.59 ms, 2.67 with it.
 #include "kv_attn.h"
 
 namespace qlora {
@@ -566,7 +571,7 @@ static hipError_t launch_many(const AttnArgs& a, const AttnPlan& pl, hipStream_t
     ProfScope ps("k_kv_attn_many", s);
     const dim3 g((unsigned)pl.many_wgs), t(many_threads(D));
     const CodePlanes cp = code_planes(a.c.cb);
-    // (for D = 256 the second loop body spills registers: 16 sequences of 40 rows 305 us, 289 without it)
+    // (for D = 256 the second loop body spills registers: 16 sequences of 40 rows 305 us with it, 289 without)
     if (D < 256 && pl.sparse) hipLaunchKernelGGL((k_kv_attn_many<D, NB, D < 256>), g, t, 0, s, a, cp, pl.many_split > 0);
     else hipLaunchKernelGGL((k_kv_attn_many<D, NB, false>), g, t, 0, s, a, cp, pl.many_split > 0);
     const hipError_t e = hipGetLastError();

@@ -9,6 +9,11 @@
 // elements (16 bytes, one dword of codes); a workgroup takes as many consecutive rows as its lanes
 // hold of one head, so that the code dwords of rows that are neighbours in a page land side by side,
 // and grid.y spreads the heads.
+//
+// Measured: 8192 rows of 32 heads of 128 in blocks of 32 (172 MB each way): written in 43 to 45 us = 3.9 TB/s (50 us where each
+// head's row is loaded only when the last one is stored; the encoding, two fifths of the time by its instructions, hides behind
+// the loads), read back in 37 us = 4.6 TB/s; 25385 rows of 16 heads read (266 MB) in 60 us = 4.4 TB/s; 64 rows of 8 heads
+// 4 us each, the chain of loads.
 #include "kernels.h"
 #include "kv.h"
 

@@ -12,6 +12,10 @@
 // and used for all of them.  The angle is reduced in float64, in revolutions (the unit of the sine
 // instruction): pos * freq is exact to 2^-53 however far the position, the fraction is then
 // exact in fp32 to 2^-25 revolutions, where an fp32 product at position 10^6 is off by 0.06 radians.
+//
+// Measured: 4096 rows of 32 + 32 heads of 128 with norms 26 us = 5.1 TB/s (a copy of 2 GiB: 4.8; part of the data is still in the
+// 256 MB cache here), their backward at 2048 rows of 64 + 64 heads 38.6 us = 5.2 TB/s; 16 rows of 64 + 64 heads 3.7 us, which
+// is one launch and two dependent loads.
 #include "kernels.h"
 #include "kv.h"
 

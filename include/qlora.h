@@ -332,6 +332,7 @@ qlora_status qlora_kv_sizes(const qlora_kv_cache* cache, size_t* codes_bytes, si
  * length[b] - n + i.  Position p lives in page table[b * max_pages + p / page_size], slot p % page_size.
  * Rows that belong to no sequence (before start[0], from start[batch] on) are left alone.  A row with a
  * negative position (length[b] < n) has no token: it is not written, reads zeros, attends nothing.
+ * start is meant to ascend (rows that entries out of order name twice are computed twice).
  * The kernels check every entry and read and write nothing out of range; where one is wrong,
  *   - a sequence whose start entries are out of order or past `rows`: its rows are left alone (bit 0);
  *   - a length outside 0 .. max_pages * page_size: nothing is written, rows read and attend NaN (bit 1);
@@ -365,12 +366,19 @@ qlora_status qlora_kv_read(const qlora_kv_cache* cache, const qlora_kv_batch* ba
  * window > 0 (causal only) j > position - window.  Query head h reads cache head h / (q_heads / heads).
  * A row that sees nothing gives zeros and lse = -infinity.  What a row does not see does not reach it,
  * NaN included.  lse (or NULL): fp32 [rows][q_heads], the natural logarithm of sum_j p_j.
- * bf16 products with fp32 accumulation; maximum, sum and output held in fp32; the levels (times a
- * constant per codebook) and the probabilities (times the value scales) are rounded to bf16 for the
- * matrix instructions.  Deterministic.
+ * fp16 products with fp32 accumulation; maximum, sum and output held in fp32.  Rounded to fp16 for the
+ * matrix instructions, each brought to about 1 by a power of two first: a row of q (by its largest
+ * element), the levels (FP4's and Int4's exactly), the probabilities, and the scales, or levels times
+ * scales.  What fp16's range then loses: an element of k or v below 2^-14 of the largest scale of its
+ * 64 tokens (or, for v, of those so far) is off by up to 2^-25 of that scale; and a probability below
+ * 2^-21 of the largest one is off by up to 2^-31 of it (times the largest value scale, in the output).
+ * Value scales below 2^-100 are held in units of 2^-100.
+ * The same call gives the same bits (no sum depends on the order in which workgroups run).
  * Requires: q_heads a multiple of cache.heads, at most 1024; scale finite and > 0; window >= 0, 0 if not
- * causal; o like q; ws of qlora_kv_attn_workspace bytes (which reads the sizes of `cache` and `batch`
- * only, not their arrays).                                                                             */
+ * causal; o like q, not overlapping it; (rows * q_heads / cache.heads) < 2^30; ws of
+ * qlora_kv_attn_workspace bytes, 16-byte aligned (the query reads the sizes of `cache` and `batch` only,
+ * not their arrays, and gives 0 for sizes that the call refuses).  Calls that may run at the same time
+ * need a workspace each.                                                                               */
 size_t qlora_kv_attn_workspace(const qlora_kv_cache* cache, const qlora_kv_batch* batch, int64_t rows,
                                int32_t q_heads);
 qlora_status qlora_kv_attn(const qlora_heads* q, int64_t rows, const qlora_kv_cache* cache,
