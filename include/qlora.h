@@ -331,7 +331,8 @@ qlora_status qlora_kv_sizes(const qlora_kv_cache* cache, size_t* codes_bytes, si
  * the last tokens of sequence b: with n = start[b + 1] - start[b], row start[b] + i is its position
  * length[b] - n + i.  Position p lives in page table[b * max_pages + p / page_size], slot p % page_size.
  * Rows that belong to no sequence (before start[0], from start[batch] on) are left alone.  A row with a
- * negative position (length[b] < n) has no token: it is not written, reads zeros, attends nothing.
+ * negative position (length[b] < n) has no token: it is not written, reads zeros, and sees nothing where
+ * attention is causal.
  * start is meant to ascend (rows that entries out of order name twice are computed twice).
  * The kernels check every entry and read and write nothing out of range; where one is wrong,
  *   - a sequence whose start entries are out of order or past `rows`: its rows are left alone (bit 0);
