@@ -89,7 +89,9 @@ struct AttnArgs {
   float* lse;                     // [rows][q.n] or NULL
   KvView c;
   BatchView b;
-  int32_t group;                  // query heads per cache head
+  int32_t group;                  // query heads per cache head, and n / group = n group_mul >> group_shift
+  uint32_t group_mul;
+  int32_t group_shift;
   float scale;
   int32_t causal, window;
   int32_t ushift;                 // log2 of the unit of work in steps of every wave

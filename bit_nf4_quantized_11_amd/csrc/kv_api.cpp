@@ -327,6 +327,12 @@ qlora_status qlora_kv_attn(const qlora_heads* q, int64_t rows, const qlora_kv_ca
   a.c = cache_view(cache);
   a.b = batch_view(batch, cache, rows);
   a.group = q->heads / cache->heads;
+  // 2^s >= group > 2^(s - 1), so the multiplier, 2^(31 + s) / group rounded up, is at most 2^32 - 1 past group 1 and off by
+  // less than 1, which an n below 2^31 takes less than 2^31 <= 2^(31 + s) / group of the way to the next quotient
+  int s = 0;
+  while (1 << s < a.group) ++s;
+  a.group_shift = 31 + s;
+  a.group_mul = (uint32_t)(((uint64_t(1) << a.group_shift) + a.group - 1) / a.group);
   a.scale = scale;
   a.causal = causal;
   // (a window that no cache of this batch outgrows is none)

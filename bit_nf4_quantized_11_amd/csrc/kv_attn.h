@@ -158,6 +158,11 @@ struct Tile {
   int32_t base, hi, hi_min, lo_max;   // tokens base .. hi - 1 are seen by some row, lo_max .. hi_min - 1 by all
 };
 
+// n / a.group for 0 <= n < 2^31 (a product and a shift: a division is 30 dependent instructions)
+__device__ __forceinline__ int div_group(const AttnArgs& a, int n) {
+  return (int)((uint64_t)(uint32_t)n * a.group_mul >> a.group_shift);
+}
+
 template <int TR>
 __device__ __forceinline__ Tile tile_of(const AttnArgs& a, const Seq& s, int b, int h, int rt) {
   Tile t;
@@ -168,7 +173,7 @@ __device__ __forceinline__ Tile tile_of(const AttnArgs& a, const Seq& s, int b, 
   const int left = (int)((int64_t)s.n * a.group - t.rho0);
   t.nval = left < TR ? left : TR;
   const int len = s.len < 0 ? 0 : s.len;
-  const int p0 = len - s.n + t.rho0 / a.group, p1 = len - s.n + (t.rho0 + t.nval - 1) / a.group;
+  const int p0 = len - s.n + div_group(a, t.rho0), p1 = len - s.n + div_group(a, t.rho0 + t.nval - 1);
   t.hi = a.causal ? max(p1 + 1, 0) : len;
   t.hi_min = a.causal ? p0 + 1 : len;
   const int lo = a.window ? max(p0 + 1 - a.window, 0) : 0;
@@ -216,7 +221,7 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, int n, int rows, int
       for (int c = 0; c < C; ++c) o[c] = __builtin_fmaf(po[i][c], f, o[c]);
     }
   }
-  const int rho = mt[2] + rr, i = rho / a.group, qh = mt[4] * a.group + (rho - i * a.group);
+  const int rho = mt[2] + rr, i = div_group(a, rho), qh = mt[4] * a.group + (rho - i * a.group);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint16_t* out = a.o.data + (mt[1] + i) * a.o.rs + qh * a.o.hs;
 #pragma unroll

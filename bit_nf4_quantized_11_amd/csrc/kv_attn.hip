@@ -126,12 +126,13 @@ __global__ __launch_bounds__(AT, waves_of(D, NR)) void k_kv_attn(AttnArgs a, Cod
   constexpr int CH = RB / 16;              // 16-byte chunks of a row
   constexpr int LB = RB + 16;              // a row in LDS: 16 rows' pieces of one column lie in different banks
   constexpr int kVBytes = kStep * LB;      // a wave's value codes
-  constexpr int kWaveBytes = kVBytes + NB * kStep * 6;   // value codes, fp32 key scales, fp16 value scales
-  constexpr int kMergeBytes = 2 * TR * (D + 4) * 4;
-  constexpr int kShared = AW * kWaveBytes > kMergeBytes ? AW * kWaveBytes : kMergeBytes;
-  __shared__ __attribute__((aligned(16))) unsigned char smem[kShared];
+  constexpr int kStepBytes = kVBytes + NB * kStep * 6;   // value codes, fp32 key scales, fp16 value scales
+  constexpr int LDO = D + 4;               // floats of a row of sums
+  constexpr int kWaveBytes = kStepBytes > TR * LDO * 4 ? kStepBytes : TR * LDO * 4;
+  __shared__ __attribute__((aligned(16))) unsigned char smem[AW * kWaveBytes];
   __shared__ uint32_t pair[256];
-  __shared__ float ml[AW][2][TR];
+  __shared__ float ml[AW][2][TR];          // maxima (log2) and sums of each wave's rows
+  __shared__ int vexp[AW][NB];             // units of its output sums
   __shared__ SeqTable<AT> seqs;
   __shared__ int found;
 
@@ -193,9 +194,10 @@ __global__ __launch_bounds__(AT, waves_of(D, NR)) void k_kv_attn(AttnArgs a, Cod
     const Seq s = seqs.seq(bi);
     const int units = units_of<TR>(a, s), tiles = tiles_of<TR>(a, s);
     const uint32_t rem = cur - __builtin_amdgcn_readfirstlane(seqs.pre[bi]);
-    const int tile_id = __builtin_amdgcn_readfirstlane(rem / (uint32_t)units);   // (head, tile) of the sequence
+    // (head, tile) of the sequence; most sequences of a decoding step have one tile, short ones one unit
+    const int tile_id = units == 1 ? (int)rem : __builtin_amdgcn_readfirstlane(rem / (uint32_t)units);
     const int u0 = (int)rem - tile_id * units, u1 = min(u0 + hi - cur, units);
-    const int h = __builtin_amdgcn_readfirstlane((uint32_t)tile_id / (uint32_t)tiles), rt = tile_id - h * tiles;
+    const int h = tiles == 1 ? tile_id : __builtin_amdgcn_readfirstlane((uint32_t)tile_id / (uint32_t)tiles), rt = tile_id - h * tiles;
     const Tile t = tile_of<TR>(a, s, c0 + bi, h, rt);
     const bool whole = u0 == 0 && u1 == units;
 
@@ -208,7 +210,7 @@ __global__ __launch_bounds__(AT, waves_of(D, NR)) void k_kv_attn(AttnArgs a, Cod
       const int rr = r * 16 + l16;
       const bool ok = rr < t.nval;
       const int rho = t.rho0 + (ok ? rr : 0);
-      const int i = rho / a.group, qh = t.h * a.group + (rho - i * a.group);
+      const int i = div_group(a, rho), qh = t.h * a.group + (rho - i * a.group);
       const int len = s.len < 0 ? 0 : s.len;
       const int p = len - s.n + i;
       r_hi[r] = !ok ? 0 : a.causal ? p + 1 : len;
@@ -535,108 +537,79 @@ __global__ __launch_bounds__(AT, waves_of(D, NR)) void k_kv_attn(AttnArgs a, Cod
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 
-    // the four waves' sums, two by two
-    const int el = opaque(lane), e16 = el & 15, eg = el >> 4;
+    // The four waves' sums: each leaves its own in LDS, then all threads add them up, a thread 8 neighbouring columns
+    // of a row.  (Added two by two, and written by one wave, this took 4200 cycles of the 15000 of a tile with one step.)
+    {
+      const int el = opaque(lane), e16 = el & 15, eg = el >> 4;
+      float* const mg = reinterpret_cast<float*>(vbuf);
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      l[r] = group_sum(l[r]) * pow2(-(int)kPBits);
-      m[r] *= rs[r];
-      if (eg == 0) {
-        ml[wave][0][r * 16 + e16] = m[r];
-        ml[wave][1][r * 16 + e16] = l[r];
-      }
-    }
-    __syncthreads();   // also: every wave is done with its value buffer
-    float mt[NR], lt[NR];
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      mt[r] = neg_inf();
-#pragma unroll
-      for (int k = 0; k < AW; ++k) mt[r] = fmaxf(mt[r], ml[k][0][r * 16 + e16]);
-      const float mu = mt[r] == neg_inf() ? 0.0f : mt[r];
-      lt[r] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < AW; ++k)
-        lt[r] += ml[k][1][r * 16 + e16] * __builtin_amdgcn_exp2f(ml[k][0][r * 16 + e16] - mu);
-      const float f = __builtin_amdgcn_exp2f(m[r] - mu);
-#pragma unroll
-      for (int u = 0; u < UN; ++u) {
-        const float fv = f * (pow2(ve[u * 16 / B] - (int)kPBits) * cp.inv);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) O[r][u][i] *= fv;
-      }
-    }
-    float* const mg = reinterpret_cast<float*>(smem);
-    constexpr int LDO = D + 4;
-#pragma unroll
-    for (int round = 2; round >= 1; round >>= 1) {
-      if (wave >= round && wave < 2 * round) {
-        float* d = mg + (wave - round) * TR * LDO;
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int u = 0; u < UN; ++u) *reinterpret_cast<f32x4*>(d + (r * 16 + e16) * LDO + u * 16 + 4 * eg) = O[r][u];
-      }
-      __syncthreads();
-      if (wave < round) {
-        const float* d = mg + wave * TR * LDO;
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int u = 0; u < UN; ++u) {
-            const f32x4 x = *reinterpret_cast<const f32x4*>(d + (r * 16 + e16) * LDO + u * 16 + 4 * eg);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) O[r][u][i] += x[i];
-          }
-      }
-      __syncthreads();
-    }
-
-    if (wave == 0) {
-      if (whole) {
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const int rr = r * 16 + e16;
-          if (rr >= t.nval) continue;
-          const int rho = t.rho0 + rr, i = rho / a.group, qh = t.h * a.group + (rho - i * a.group);
-          float inv = lt[r] == 0.0f ? 0.0f : 1.0f / lt[r];
-          if (s.len < 0) inv = __builtin_nanf("");
-          uint16_t* op = a.o.data + (s.row0 + i) * a.o.rs + qh * a.o.hs;
-#pragma unroll
-          for (int u = 0; u < UN; ++u) {
-            // rows 4g + i of the tile: elements d, d + 4, d + 1, d + 5
-            uint32_t* d = reinterpret_cast<uint32_t*>(op + 16 * u + 8 * (eg >> 1) + 2 * (eg & 1));
-            d[0] = pack_bf16x2(O[r][u][0] * inv, O[r][u][2] * inv);
-            d[2] = pack_bf16x2(O[r][u][1] * inv, O[r][u][3] * inv);
-          }
-          if (a.lse && eg == 0)
-            a.lse[(s.row0 + i) * a.q.n + qh] =
-                s.len < 0 ? __builtin_nanf("") : lt[r] == 0.0f ? neg_inf() : (mt[r] + __builtin_amdgcn_logf(lt[r])) * kLn2;
+      for (int r = 0; r < NR; ++r) {
+        l[r] = group_sum(l[r]);
+        if (eg == 0) {
+          ml[wave][0][r * 16 + e16] = m[r] * rs[r];
+          ml[wave][1][r * 16 + e16] = l[r];
         }
+#pragma unroll
+        for (int u = 0; u < UN; ++u) *reinterpret_cast<f32x4*>(mg + (r * 16 + e16) * LDO + u * 16 + 4 * eg) = O[r][u];
+      }
+      if (el == 0)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) vexp[wave][b] = ve[b];
+    }
+    __syncthreads();
+    constexpr int CT = D / 8;   // threads of a row
+#pragma unroll
+    for (int i = 0; i < (TR * CT + AT - 1) / AT; ++i) {
+      const int item = opaque(threadIdx.x) + i * AT, rr = item / CT, c = item % CT;
+      if (rr >= t.nval) continue;
+      float mk[AW], mt = neg_inf(), lt = 0.0f;
+#pragma unroll
+      for (int k = 0; k < AW; ++k) mt = fmaxf(mt, mk[k] = ml[k][0][rr]);
+      const float mu = mt == neg_inf() ? 0.0f : mt;
+      f32x4 o[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int k = 0; k < AW; ++k) {
+        const float f = __builtin_amdgcn_exp2f(mk[k] - mu) * pow2(-(int)kPBits);
+        const float fo = f * pow2(vexp[k][8 * c / B]) * cp.inv;
+        lt = __builtin_fmaf(ml[k][1][rr], f, lt);
+        const f32x4* const p = reinterpret_cast<const f32x4*>(smem + k * kWaveBytes) + (rr * LDO + 8 * c) / 4;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const f32x4 w = p[x];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[x][j] = __builtin_fmaf(w[j], fo, o[x][j]);
+        }
+      }
+      if (whole) {
+        const int rho = t.rho0 + rr, row = div_group(a, rho), qh = t.h * a.group + (rho - row * a.group);
+        float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
+        if (s.len < 0) inv = __builtin_nanf("");
+        // the columns hold elements 0, 4, 1, 5, 2, 6, 3, 7 of their eight
+        *reinterpret_cast<uint4*>(a.o.data + (s.row0 + row) * a.o.rs + qh * a.o.hs + 8 * c) =
+            make_uint4(pack_bf16x2(o[0][0] * inv, o[0][2] * inv), pack_bf16x2(o[1][0] * inv, o[1][2] * inv),
+                       pack_bf16x2(o[0][1] * inv, o[0][3] * inv), pack_bf16x2(o[1][1] * inv, o[1][3] * inv));
+        if (a.lse && c == 0)
+          a.lse[(s.row0 + row) * a.q.n + qh] =
+              s.len < 0 ? __builtin_nanf("") : lt == 0.0f ? neg_inf() : (mt + __builtin_amdgcn_logf(lt)) * kLn2;
       } else {
         // slot 0: the range's first tile, begun in an earlier range; slot 1: its last, ending in a later one
         float* d = a.part + (2 * (int64_t)w + (u0 == 0 ? 1 : 0)) * (TR * (D + 2));
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const int rr = r * 16 + e16;
-#pragma unroll
-          for (int u = 0; u < UN; ++u)
-            *reinterpret_cast<f32x4*>(d + rr * D + u * 16 + 4 * eg) = O[r][u];
-          if (eg == 0) {
-            d[TR * D + rr] = mt[r];
-            d[TR * D + TR + rr] = lt[r];
-          }
-        }
-        if (u0 != 0 && u1 == units && el == 0) {
-          // this range ends the tile: the join of its partial sums is noted here
-          int32_t* mt_ = a.meta + w * kMetaInts;
-          mt_[0] = (int32_t)ranges.of(cur - u0);   // the range that holds its first unit
-          mt_[1] = (int32_t)s.row0;
-          mt_[2] = t.rho0;
-          mt_[3] = t.nval;
-          mt_[4] = t.h;
+        for (int x = 0; x < 2; ++x) *reinterpret_cast<f32x4*>(d + rr * D + 8 * c + 4 * x) = o[x];
+        if (c == 0) {
+          d[TR * D + rr] = mt;
+          d[TR * D + TR + rr] = lt;
         }
       }
+    }
+    if (!whole && u0 != 0 && u1 == units && threadIdx.x == 0) {
+      // this range ends the tile: the join of its partial sums is noted here
+      int32_t* mt_ = a.meta + w * kMetaInts;
+      mt_[0] = (int32_t)ranges.of(cur - u0);   // the range that holds its first unit
+      mt_[1] = (int32_t)s.row0;
+      mt_[2] = t.rho0;
+      mt_[3] = t.nval;
+      mt_[4] = t.h;
     }
     cur += u1 - u0;
     __syncthreads();

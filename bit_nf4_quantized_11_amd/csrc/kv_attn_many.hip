@@ -140,7 +140,7 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
   // rows of q: row 32 wave + l32 of the tile
   const int rr = wave * 32 + l32;
   const bool ok = rr < t.nval;
-  const int rho = t.rho0 + (ok ? rr : 0), ri = rho / a.group, qh = h * a.group + (rho - ri * a.group);
+  const int rho = t.rho0 + (ok ? rr : 0), ri = div_group(a, rho), qh = h * a.group + (rho - ri * a.group);
   const int len = s.len < 0 ? 0 : s.len, pos = len - s.n + ri;
   const int r_hi = !ok ? 0 : a.causal ? pos + 1 : len, r_lo = a.window ? pos + 1 - a.window : 0;
   // tokens that some row of this wave sees
