@@ -179,21 +179,28 @@ __global__ __launch_bounds__(AT, waves_of(D, NR)) void k_kv_attn(AttnArgs a, Cod
     }
   }
 
+  int seq_first = 0, seq_end = 0, bi = 0, units = 1, tiles = 1;   // the sequence at hand: its units, as numbered here
+  Seq s{};
   for (int cur = lo; cur < hi;) {
-    // the sequence that holds unit `cur`
-    while (seqs.pre[AT] <= cur) {
-      const int base = seqs.pre[AT];
+    if (cur >= seq_end) {
+      // the sequence that holds unit `cur`
+      while (seqs.pre[AT] <= cur) {
+        const int base = seqs.pre[AT];
+        __syncthreads();
+        c0 += AT;
+        scan_seqs(a.b, c0, base, seqs, count);
+      }
+      const int tx = opaque(threadIdx.x);
+      if (seqs.pre[tx] <= cur && cur < seqs.pre[tx + 1]) found = tx;
       __syncthreads();
-      c0 += AT;
-      scan_seqs(a.b, c0, base, seqs, count);
+      bi = __builtin_amdgcn_readfirstlane(found);
+      s = seqs.seq(bi);
+      units = units_of<TR>(a, s);
+      tiles = tiles_of<TR>(a, s);
+      seq_first = __builtin_amdgcn_readfirstlane(seqs.pre[bi]);
+      seq_end = __builtin_amdgcn_readfirstlane(seqs.pre[bi + 1]);
     }
-    const int tx = opaque(threadIdx.x);
-    if (seqs.pre[tx] <= cur && cur < seqs.pre[tx + 1]) found = tx;
-    __syncthreads();
-    const int bi = __builtin_amdgcn_readfirstlane(found);
-    const Seq s = seqs.seq(bi);
-    const int units = units_of<TR>(a, s), tiles = tiles_of<TR>(a, s);
-    const uint32_t rem = cur - __builtin_amdgcn_readfirstlane(seqs.pre[bi]);
+    const uint32_t rem = cur - seq_first;
     // (head, tile) of the sequence; most sequences of a decoding step have one tile, short ones one unit
     const int tile_id = units == 1 ? (int)rem : __builtin_amdgcn_readfirstlane(rem / (uint32_t)units);
     const int u0 = (int)rem - tile_id * units, u1 = min(u0 + hi - cur, units);
