@@ -28,11 +28,12 @@
 // 2^-17 of it stay), the scaled probabilities of a step by the largest scale so far of that
 // block of elements (a running exponent, like the running maximum, that all rows share).
 //
-// Measured: 16 sequences of up to 32768 tokens (311 k in all, 338 MB), 64 query on 8 cache heads of 128: 87 us of this
-// kernel = 3.9 TB/s and 2 of the join, where a large copy reaches 4.8: the steps are bound by HBM (a step's 18.9 MB in
-// 4 us when all 2048 waves are in theirs), VALU issue close behind; the start of a range (lengths, then table, then codes: three
-// round trips) and the end of each tile (four waves' sums) cost about 6 us of a call.  Sixteen sequences of 4096: 22 us
-// of 15 at copy rate; one of 777 tokens 6 us, all of it that chain.
+// Measured: 16 sequences of up to 32768 tokens (311 k in all, 338 MB), 64 query on 8 cache heads of 128: 84 us of this
+// kernel = 4.0 TB/s and 2 of the join, where a large copy reaches 4.8: the steps are bound by HBM (a step's 18.9 MB in
+// 4 us when all 2048 waves are in theirs), VALU issue close behind.  A tile of a single step takes about 10500 cycles of one
+// workgroup: 1200 to find it, 2400 for table, queries and codes, 6000 for the step, 1000 for the waves' sums; two workgroups
+// to a CU overlap half of that: 1000 sequences of one token 86 us, 512 of 128 tokens 53 (17 at copy rate), 16 of
+// 4096 21 (15), one of 777 tokens 6.
 #include "kv_attn.h"
 
 namespace qlora {
@@ -672,22 +673,24 @@ CodePlanes code_planes(int cb) {
   return p;
 }
 
-// Sequences with at most kFew rows per cache head go to the kernel of this file, those with more to the one for many rows.
-// The host knows the rows and the sequences of a call, not which has how many: where the mean is low it leaves all of
-// them to the first kernel (which is right for any), with one sequence all to one, otherwise it launches both.
-// 16 sequences of 4096 tokens, 8 cache heads, this kernel and the other one: D = 128, 40 rows 56 and 76 us, 64 rows 58 and 78,
-// 96 rows 105 and 83; D = 64, 64 rows 39 and 72, 96 rows 56 and 75; D = 256, 64 rows 72 and 93, 96 rows 106 and 96.
-constexpr int kFew = 64;
+// Sequences with at most this many rows per cache head go to the kernel of this file, those with more to the one for
+// many rows.  The host knows the rows and the sequences of a call, not which has how many: where the mean is low it leaves
+// all of them to the first kernel (which is right for any), with one sequence all to one, otherwise it launches both.
+// This kernel and the other one, 16 sequences of 4096 tokens, 32 cache heads: D = 64, 64 rows 101 and 221 us, 128 rows 181 and 219,
+// 160 rows 225 and 239; D = 128, 64 rows 176 and 242, 96 rows 248 and 243, 128 rows 329 and 256; D = 256, 64 rows 516 and
+// 555, 96 rows 754 and 561.  One sequence of 32768, 8 heads of 64: 64 rows 51 and 40 us, 128 rows 51 and 44.
+constexpr int few_rows(int D) { return D == 64 ? 128 : 64; }
 
 AttnPlan attn_plan(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t batch, int64_t max_len, int D) {
   AttnPlan p{};
   const int64_t rows_h = rows * (q_heads / kv_heads), nseq = batch > 1 ? batch : 1;
-  if (rows_h <= kFew * nseq) p.few = INT32_MAX;
-  else p.few = nseq == 1 ? 0 : kFew;
+  const int few = few_rows(D);
+  if (rows_h <= few * nseq) p.few = INT32_MAX;
+  else p.few = nseq == 1 ? 0 : few;
   // Tiles of 32 rows decode a token once for twice the rows, but make half the units: they are taken where sequences have more
-  // than 16 rows and every workgroup still has two units.  16 sequences of 4096, 8 cache heads of 128, 32 and 64
-  // rows of each: 39 and 58 us (43 and 70 with tiles of 16); one sequence 21 and 25 us (17 and 23).  D = 256 has no
-  // registers for it.
+  // than 16 rows and every workgroup still has two units.  8 cache heads of 128, 32 and 64 rows of each sequence: 16
+  // sequences of 4096 40 and 55 us (43 and 67 with tiles of 16), 4 of them 30 and 31 (23 and 28), one 21 and 22 (18 and
+  // 22).  D = 256 has no registers for it.
   const int64_t units32 = nseq * kv_heads * ((max_len >> kUnitShift) + 1);
   const int nr = D < 256 && rows_h > 16 * nseq && units32 >= 2 * kCUs * waves_of(D, 2) ? 2 : 1;
   p.tile = 16 * nr;

@@ -93,6 +93,8 @@ MANY = [
     # the tokens of a tile in parts, joined: long caches under few tiles
     ([1500], [40], 1, 2, 128, 64, 64, "nf4", True, 0),
     ([1027], [70], 2, 1, 64, 32, 16, "fp4", True, 0),
+    ([1027], [150], 2, 1, 64, 32, 16, "fp4", True, 0),
+    ([800], [45], 1, 3, 64, 64, 64, "nf4", False, 0),
     ([900], [35], 1, 2, 256, 128, 128, "int4", False, 0),
     ([1400, 1, 600], [90, 1, 100], 1, 2, 128, 32, 16, "nf4", True, 700),
     ([2000], [66], 1, 1, 128, 64, 256, "int4", True, 64),
@@ -123,7 +125,8 @@ def test_tiles_of_32_rows(lens, new, heads, group, dim, block, page, book, windo
     check(layout(lens, new, page, dim + group, spare_cols=4200), heads, group, dim, block, book, window=window)
 
 
-def test_many_rows_of_some_among_many_sequences():
+@pytest.mark.parametrize("dim", [64, 128])
+def test_many_rows_of_some_among_many_sequences(dim):
     """More sequences than one pass of the scan takes: most with a few rows, ten with many, so both kernels run."""
     require_gpu()
     rng = np.random.default_rng(1)
@@ -131,7 +134,7 @@ def test_many_rows_of_some_among_many_sequences():
     new = [int(min(n, m)) for n, m in zip(lens, rng.integers(0, 3, 600))]
     for i in (0, 5, 255, 256, 300, 511, 512, 513, 577, 599):
         lens[i], new[i] = 470 + i % 7, 460
-    check(layout(lens, new, 16, 2), 1, 8, 64, 64, "nf4")
+    check(layout(lens, new, 16, 2), 1, 8, dim, 64, "nf4")
 
 
 def test_rows_without_a_token():
@@ -219,10 +222,11 @@ def test_what_a_row_does_not_see_does_not_reach_it(dim, prefix):
     assert torch.equal(ow[70:90], refw[70:90]) and torch.isnan(ow[90:]).all()
 
 
-def test_wrong_entries_are_reported():
+@pytest.mark.parametrize("dim", [64, 128])
+def test_wrong_entries_are_reported(dim):
     """Pages, lengths and starts out of range: the bit set, NaN where a row needs what is not there, nothing else touched."""
     require_gpu()
-    dim, page, pages, rows = 64, 16, 16, 150
+    page, pages, rows = 16, 16, 150
     q = dev_bf16(bits(1, (rows, 2, dim)))
     x = dev_bf16(bits(2, (256, 1, dim)))
     cache = Q.kv_alloc(pages, page, 1, dim)
@@ -248,9 +252,12 @@ def test_wrong_entries_are_reported():
     for start in ([0, rows + 1], [-1, rows], [rows, 0], [0, 2 ** 31 - 1]):
         f, o, lse = run(start, [256], good)
         assert f == FAULT_START and torch.all(o == 5.0) and torch.all(lse == 5.0)
-    # starts that go back: the rows of the sequences in order are done, some by two sequences with the same result
+    # starts that go back: the rows of the sequences in order are done, some by two sequences with the same result: that
+    # of three sequences of which two are empty (of one sequence alone another kernel may take the rows, other bits)
+    three = run([0, rows, rows, rows], [256] * 3, np.repeat(good, 3, 0))
+    assert three[0] == 0
     f, o, lse = run([0, rows, 0, rows], [256] * 3, np.repeat(good, 3, 0))
-    assert f == FAULT_START and torch.equal(o, ref[1]) and torch.equal(lse, ref[2])
+    assert f == FAULT_START and torch.equal(o, three[1]) and torch.equal(lse, three[2])
 
 
 def test_strides_streams_and_one_workspace_for_two_calls():
