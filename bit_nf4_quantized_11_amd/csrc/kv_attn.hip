@@ -708,7 +708,7 @@ AttnPlan attn_plan(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t batc
     const int tr = many_threads(D) / 2;
     const int64_t most = rows_h / ((int64_t)p.few + 1) + 1;   // sequences that can have more than `few` rows
     p.many_wgs = (rows_h / tr + (most < nseq ? most : nseq)) * kv_heads;
-    p.sparse = p.many_wgs * tr >= 2 * rows_h * kv_heads;
+    p.sparse = p.many_wgs * tr * 3 >= 4 * rows_h * kv_heads;
     const int64_t least = (rows_h - p.few * nseq) / tr * kv_heads;   // tiles that there are, if all rows are a sequence's
     if (max_len >= 2 * kSplitTokens && least <= kSplitWgs / 2) {
       p.many_split = p.many_wgs < kSplitWgs / 2 ? p.many_wgs : kSplitWgs / 2;

@@ -20,9 +20,9 @@
 // One workgroup per tile of a sequence.  Each finds all tiles of the call from the device's lengths; where there are no more
 // than half as many as CUs, the tokens of every tile are cut into parts for all of them, whose sums k_kv_attn_many_join adds (2
 // sequences of 8192, 512 rows of each, 197 us; 290 with the tiles whole).
-// SKIP: waves pass over tokens that none of their rows sees, for tiles that are mostly empty: a wave without rows then decodes
-// only (64 sequences of 4096, 12 rows each of 4 query heads per cache head, 246 us; 319 without).  Full tiles do better without
-// the second loop body: 16384 rows 2.59 ms, 2.67 with it.
+// SKIP: waves pass over tokens that none of their rows sees, for tiles with many empty rows: a wave without rows then decodes
+// only (64 sequences of 4096, 8 cache heads of 128, 96 rows of each 252 us, 326 without it; 192 rows 331 and 351).  Full tiles do
+// better without the second loop body: 256 rows 370 us, 377 with it, 16384 rows of one sequence 2.52 and 2.58 ms.
 #include "kv_attn.h"
 
 namespace qlora {
@@ -571,8 +571,9 @@ static hipError_t launch_many(const AttnArgs& a, const AttnPlan& pl, hipStream_t
     ProfScope ps("k_kv_attn_many", s);
     const dim3 g((unsigned)pl.many_wgs), t(many_threads(D));
     const CodePlanes cp = code_planes(a.c.cb);
-    // (for D = 256 the second loop body spills registers: 16 sequences of 40 rows 305 us with it, 289 without)
-    if (D < 256 && pl.sparse) hipLaunchKernelGGL((k_kv_attn_many<D, NB, D < 256>), g, t, 0, s, a, cp, pl.many_split > 0);
+    // (for D = 64 such tiles are the other kernel's, 160 rows 83 us either way; for D = 256 the second loop body spills
+    // registers, 16 sequences of 40 rows 305 us with it, 289 without)
+    if (D == 128 && pl.sparse) hipLaunchKernelGGL((k_kv_attn_many<D, NB, D == 128>), g, t, 0, s, a, cp, pl.many_split > 0);
     else hipLaunchKernelGGL((k_kv_attn_many<D, NB, false>), g, t, 0, s, a, cp, pl.many_split > 0);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !pl.many_split) return e;
