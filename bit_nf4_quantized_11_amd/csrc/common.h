@@ -41,12 +41,13 @@ struct ThrLut {
 };
 
 // The bin of a normalized weight: floor(32 x + 32) computed with one fused multiply-add,
-// clamped to [0, 63] (NaN -> 0).  Host and device evaluate the same IEEE operations.
+// clamped to [0, 63] (NaN -> 0), so that dropping the fraction is the floor.  Host and device evaluate the same IEEE
+// operations.
 __host__ __device__ __forceinline__ int lut_bin(float x) {
   float y = __builtin_fmaf(x, 32.0f, 32.0f);
   y = __builtin_fmaxf(y, 0.0f);
   y = __builtin_fminf(y, (float)(kLutBins - 1));
-  return (int)__builtin_floorf(y);
+  return (int)y;
 }
 
 // Code of a normalized weight: the number of thresholds below x, read off the encoder's bin

@@ -10,8 +10,8 @@
 // hold of one head, so that the code dwords of rows that are neighbours in a page land side by side,
 // and grid.y spreads the heads.
 //
-// Measured: 8192 rows of 32 heads of 128 in blocks of 32 (172 MB each way): written in 43 to 45 us = 3.9 TB/s (50 us where each
-// head's row is loaded only when the last one is stored; the encoding, two fifths of the time by its instructions, hides behind
+// Measured: 8192 rows of 32 heads of 128 in blocks of 32 (172 MB each way): written in 38 to 41 us = 4.3 TB/s (5 us more where each
+// head's row is loaded only when the last one is stored; the encoding, two thirds of the time by its instructions, hides behind
 // the loads), read back in 37 us = 4.6 TB/s; 25385 rows of 16 heads read (266 MB) in 60 us = 4.4 TB/s; 64 rows of 8 heads
 // 4 us each, the chain of loads.
 #include "kernels.h"
@@ -78,6 +78,11 @@ __device__ __forceinline__ Slot<D> find_slot(const BatchView& b, const KvView& c
   return s;
 }
 
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
+}
+
 template <int D>
 __global__ __launch_bounds__(KT) void k_kv_write(Heads k, Heads v, KvView c, BatchView b, int bl, int zero, ThrLut lut) {
   constexpr int LR = D / 8, NT = KT / LR;   // lanes per row, rows per workgroup
@@ -89,11 +94,15 @@ __global__ __launch_bounds__(KT) void k_kv_write(Heads k, Heads v, KvView c, Bat
   const Slot<D> s = find_slot<D>(b, c, t0, r, cnt);
   if (!s.ok) return;
   const int nb = LR >> bl;   // blocks per row (1 << bl lanes each)
+  const uint16_t* const kp = k.data + (t0 + r) * k.rs + e * 8;
+  const uint16_t* const vp = v.data + (t0 + r) * v.rs + e * 8;
+  const int64_t row0 = ((s.page * c.heads) << c.pshift) + s.off;   // of head 0, in the cache's buffers
+  uint8_t* const kcp = c.kc + row0 * (D / 2) + 4 * key_dword<D>(e);
+  uint8_t* const vcp = c.vc + row0 * (D / 2) + 4 * e;
+  uint16_t* const ksp = c.ks + row0 * nb + (e >> bl);
+  uint16_t* const vsp = c.vs + row0 * nb + (e >> bl);
   auto load = [&](int item) {
-    const bool key = item < c.heads;
-    const int h = key ? item : item - c.heads;
-    const Heads& x = key ? k : v;
-    return *reinterpret_cast<const uint4*>(x.data + (t0 + r) * x.rs + h * x.hs + e * 8);
+    return *reinterpret_cast<const uint4*>(item < c.heads ? kp + item * k.hs : vp + (item - c.heads) * v.hs);
   };
   uint4 next = load(blockIdx.y);
   for (int item = blockIdx.y; item < 2 * c.heads; item += gridDim.y) {
@@ -106,7 +115,11 @@ __global__ __launch_bounds__(KT) void k_kv_write(Heads k, Heads v, KvView c, Bat
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, u[i] & 0x7FFFu);
-    for (int off = 1; off < (1 << bl); off <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
+    // over the block's lanes: 1 and 2 away, then the other half of 8 and of 16 (mirrored)
+    m = dpp_max<0xB1>(m);
+    m = dpp_max<0x4E>(m);
+    if (bl >= 3) m = dpp_max<0x141>(m);
+    if (bl >= 4) m = dpp_max<0x140>(m);
     if (m < 0x0080u) m = 0;   // below the smallest normal: a zero block
     uint32_t scale = m;
     if (m >= 0x7F80u) {       // an infinity or a NaN: the block reads back as NaN
@@ -125,10 +138,9 @@ __global__ __launch_bounds__(KT) void k_kv_write(Heads k, Heads v, KvView c, Bat
     } else {
       packed = (uint32_t)zero * 0x11111111u;
     }
-    const int64_t row = ((s.page * c.heads + h) << c.pshift) + s.off;   // row of the cache's buffers
-    uint8_t* codes = (key ? c.kc : c.vc) + row * (D / 2);
-    *reinterpret_cast<uint32_t*>(codes + 4 * (key ? key_dword<D>(e) : e)) = packed;
-    if ((e & ((1 << bl) - 1)) == 0) (key ? c.ks : c.vs)[row * nb + (e >> bl)] = (uint16_t)scale;
+    const int64_t ahead = (int64_t)h << c.pshift;   // rows from head 0's
+    *reinterpret_cast<uint32_t*>((key ? kcp : vcp) + ahead * (D / 2)) = packed;
+    if ((e & ((1 << bl) - 1)) == 0) (key ? ksp : vsp)[ahead * nb] = (uint16_t)scale;
   }
 }
 
