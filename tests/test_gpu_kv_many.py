@@ -98,6 +98,8 @@ MANY = [
     ([900], [35], 1, 2, 256, 128, 128, "int4", False, 0),
     ([1400, 1, 600], [90, 1, 100], 1, 2, 128, 32, 16, "nf4", True, 700),
     ([2000], [66], 1, 1, 128, 64, 256, "int4", True, 64),
+    ([2100], [230], 1, 1, 128, 32, 64, "int4", True, 0),
+    ([2200, 2070], [120, 130], 1, 2, 64, 64, 64, "nf4", True, 0),
 ]
 
 
@@ -194,7 +196,7 @@ def test_scales_of_all_sizes(dim, block, new):
         check(h, heads, 1, dim, block, "nf4", fro=False, cache=(cache, [vals["k"]], [vals["v"]]))
 
 
-@pytest.mark.parametrize("dim,prefix", [(64, 0), (128, 0), (256, 0), (128, 1500)], ids=str)
+@pytest.mark.parametrize("dim,prefix", [(64, 0), (128, 0), (256, 0), (128, 1500), (128, 2000), (64, 2000), (256, 500)], ids=str)
 def test_what_a_row_does_not_see_does_not_reach_it(dim, prefix):
     """NaN in later tokens of the same call stays with the rows and the blocks that see them, also where the tokens
     are attended in parts."""
