@@ -106,6 +106,7 @@ struct AttnPlan {
   int64_t wgs;                    // workgroups of the first kernel's ranges
   int64_t many_wgs;               // workgroups of the second kernel, its tiles x cache heads at most
   int64_t many_split;             // how many of these it may cut into parts: 0 (no join), or up to kSplitWgs / 2
+  int split_tokens;               // tokens of a part at least; 0: none is cut
   bool sparse;                    // a quarter of its tiles' rows or more are empty
   size_t part_floats, meta_ints;  // workspace, and where the second kernel's share of it begins
   size_t many_part, many_meta;

@@ -230,9 +230,13 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, int n, int rows, int
     a.lse[(mt[1] + i) * (int64_t)a.q.n + qh] = l == 0.0f ? neg_inf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// The kernel for many rows cuts the tokens of its tiles into parts of at least kSplitTokens, as many as kSplitWgs workgroups,
-// one per CU, are enough for.  One sequence of 4096, 8 cache heads, 32 rows: D = 128 24 us (parts of 512: 28), D = 256 41 (53).
-constexpr int kSplitTokens = 256, kSplitWgs = 256;
+// The kernel for many rows cuts the tokens of its tiles into as many parts as kSplitWgs workgroups, one per CU, are enough
+// for, of at least this many tokens.  A part's sums cost 130 KB written and read where all 256 rows of its tile are there
+// (8 cache heads of 128, 1024 rows of 1024 tokens: parts of 256 50 us, of 1024, so uncut, 48; D = 64 45 and 36; 512
+// rows of 4096 62 and 63, of 2048 94), little where few are (32 rows of 4096: D = 128 24 us with parts of 256, 28 of 512; D = 256,
+// whose tiles are half as large, 41 and 53).
+constexpr int kSplitWgs = 256;
+constexpr int split_tokens_of(int D, bool sparse) { return sparse || D == 256 ? 256 : 1024; }
 
 // Threads of a workgroup of the kernel for many rows: 32 rows of a tile to a wave, 8 waves where the registers allow two
 // waves per SIMD, 4 otherwise.

@@ -710,9 +710,11 @@ AttnPlan attn_plan(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t batc
     p.many_wgs = (rows_h / tr + (most < nseq ? most : nseq)) * kv_heads;
     p.sparse = p.many_wgs * tr * 3 >= 4 * rows_h * kv_heads;
     const int64_t least = (rows_h - p.few * nseq) / tr * kv_heads;   // tiles that there are, if all rows are a sequence's
-    if (max_len >= 2 * kSplitTokens && least <= kSplitWgs / 2) {
+    const int tokens = split_tokens_of(D, p.sparse);
+    if (max_len >= 2 * tokens && least <= kSplitWgs / 2) {
       p.many_split = p.many_wgs < kSplitWgs / 2 ? p.many_wgs : kSplitWgs / 2;
       if (p.many_wgs < kSplitWgs) p.many_wgs = kSplitWgs;
+      p.split_tokens = tokens;
       p.many_part = p.part_floats;
       p.many_meta = p.meta_ints;
       p.part_floats += (size_t)kSplitWgs * tr * (D + 2);
