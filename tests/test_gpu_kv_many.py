@@ -156,7 +156,7 @@ def test_windows_that_are_none():
         q = dev_bf16(bits(3, (n, 2, 64)))
         batch = device_batch(h) if n == 190 else Q.KVBatch(i32([0, 4, 6]), i32([3, 150]), i32(h.table))
         want = Q.qlora_kv_attn(q, cache, batch, lse=True)
-        for window in (2 ** 31 - 1, 2 ** 31 - 2, 2 ** 30, h.table.shape[1] * 16):
+        for window in (2 ** 32 + 5, 2 ** 31 - 1, 2 ** 31 - 2, 2 ** 30, h.table.shape[1] * 16):
             got = Q.qlora_kv_attn(q, cache, batch, window=window, lse=True)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
@@ -333,7 +333,7 @@ def test_binding_refusals():
     cache = Q.kv_alloc(4, 16, 2, 64)
     batch = Q.KVBatch(i32([0, 3]), i32([3]), i32([[0, 1]]))
     x = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
-    bad = [x.float(), x.cpu(), x[..., ::2], x[0], torch.zeros(3, 3, 64, dtype=torch.bfloat16, device="cuda"),
+    bad = [x.float(), x.cpu(), x[..., ::2], x[0], x[0, 0], x[0, 0, 0], torch.zeros(3, 3, 64, dtype=torch.bfloat16, device="cuda"),
            torch.zeros(3, 2, 128, dtype=torch.bfloat16, device="cuda")]
     for b in bad:
         with pytest.raises(Q.QLoRAError):
@@ -350,7 +350,7 @@ def test_binding_refusals():
     for ws in (small, small.cpu(), torch.empty(1 << 20, dtype=torch.uint8, device="cuda")[::2]):
         with pytest.raises(Q.QLoRAError):
             Q.qlora_kv_attn(x, cache, batch, workspace=ws)
-    for kw in ({"window": -1}, {"window": 4, "causal": False}, {"lse": torch.zeros(3, 3, device="cuda")},
+    for kw in ({"window": -1}, {"window": 5 - 2 ** 32}, {"window": 4, "causal": False}, {"lse": torch.zeros(3, 3, device="cuda")},
                {"lse": torch.zeros(3, 2, dtype=torch.bfloat16, device="cuda")}):
         with pytest.raises(Q.QLoRAError):
             Q.qlora_kv_attn(x, cache, batch, **kw)

@@ -225,7 +225,7 @@ def test_binding_refusals():
     x = torch.zeros(5, 3, 64, dtype=torch.bfloat16, device="cuda")
     pos, freq = torch.arange(5, device="cuda"), torch.ones(16, device="cuda")
     w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
-    for bad in (x.float(), x.cpu(), x[0], x[..., ::2], torch.zeros(5, 3, 96, dtype=torch.bfloat16, device="cuda")):
+    for bad in (x.float(), x.cpu(), x[0], x[0, 0], x[..., ::2], torch.zeros(5, 3, 96, dtype=torch.bfloat16, device="cuda")):
         with pytest.raises(Q.QLoRAError):
             Q.qlora_qk_norm_rope(bad, None, pos, freq)
         with pytest.raises(Q.QLoRAError):
@@ -242,8 +242,11 @@ def test_binding_refusals():
     for kw in ({"k_weight": w}, {"k_out": x.clone()}, {"eps": -1.0}, {"eps": float("nan")}):
         with pytest.raises(Q.QLoRAError):
             Q.qlora_qk_norm_rope(x, None, pos, freq, **kw)
-    with pytest.raises(Q.QLoRAError):
-        Q.qlora_qk_norm_rope(x, x[:4], pos, freq)
+    for bad in (x[:4], x[0], x[0, 0], x.cpu(), torch.zeros(5, 3, 128, dtype=torch.bfloat16, device="cuda")):
+        with pytest.raises(Q.QLoRAError):
+            Q.qlora_qk_norm_rope(x, bad, pos, freq)
+        with pytest.raises(Q.QLoRAError):
+            Q.qlora_qk_norm_rope_bwd(x, bad, None, None, pos, freq)
     for kw in ({"q_weight": w}, {"k_weight": w}, {"dk": x.clone()}, {"dq_weight": torch.zeros(64, device="cuda")},
                {"q_weight": w, "dq_weight": torch.zeros(32, device="cuda")},
                {"q_weight": w, "workspace": torch.empty(64, dtype=torch.uint8, device="cuda")}):
