@@ -419,6 +419,16 @@ def _same_device(cache: KVCache, batch: KVBatch):
     return cache.device
 
 
+def _keys(k, name: str, q):
+    """The view of k, or None: any number of heads, otherwise like q."""
+    if k is None:
+        return None
+    view = _heads(k, name, q.device)
+    if k.size(0) != q.size(0) or k.size(2) != q.size(2):
+        raise QLoRAError(f"{name} must have {q.size(0)} rows of head_dim {q.size(2)}, not {tuple(k.shape)}")
+    return view
+
+
 def _qk_inputs(q, k, positions, inv_freq, q_weight, k_weight):
     rows, _, dim = q.shape
     dev = q.device
@@ -446,7 +456,7 @@ def qlora_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch
     [rot_dim / 2] (fp32) of q, k [rows][heads][head_dim] bf16, any strides.  The outputs may be the inputs.
     Returns (q_out, k_out or None)."""
     hq = _heads(q, "q")
-    hk = None if k is None else _heads(k, "k", q.device, (q.shape[0], k.shape[1], q.shape[2]))
+    hk = _keys(k, "k", q)
     rows, dim, rot, dev = _qk_inputs(q, k, positions, inv_freq, q_weight, k_weight)
     if k is None and k_out is not None:
         raise QLoRAError("k_out needs k")
@@ -476,8 +486,7 @@ def qlora_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q:
     (needed where there is a weight).  dq may be dq_out and dk may be dk_out.  Returns (dq, dk or None,
     dq_weight or None, dk_weight or None), the weights' fp32 [head_dim]."""
     gq = _heads(dq_out, "dq_out")
-    gk = None if dk_out is None else _heads(dk_out, "dk_out", dq_out.device,
-                                            (dq_out.shape[0], dk_out.shape[1], dq_out.shape[2]))
+    gk = _keys(dk_out, "dk_out", dq_out)
     rows, dim, rot, dev = _qk_inputs(dq_out, dk_out, positions, inv_freq, q_weight, k_weight)
     if (q_weight is not None and q is None) or (k_weight is not None and k is None):
         raise QLoRAError("a weight's gradient needs the forward's input")
@@ -514,7 +523,7 @@ def qlora_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q:
 def qlora_kv_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, batch: KVBatch, stream=None):
     """Quantize the rows k, v [rows][heads][head_dim] (bf16, any strides) into the cache."""
     dev = _same_device(cache, batch)
-    shape = (k.shape[0], cache.heads, cache.head_dim)
+    shape = (len(k) if k.dim() else 0, cache.heads, cache.head_dim)
     hk, hv = _heads(k, "k", dev, shape), _heads(v, "v", dev, shape)
     _launch(k, stream, lambda stream: _check(
         lib().qlora_kv_write(_ref(hk), _ref(hv), shape[0], _ref(cache.desc()), _ref(batch.desc()), stream),
@@ -549,8 +558,13 @@ def qlora_kv_attn(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float 
     head_dim ** -0.5.  lse: True for a new fp32 [rows][q_heads], or a tensor to fill.  Returns (out, lse or
     None).  Rows of no sequence keep what out and lse hold (undefined if they are not given)."""
     dev = _same_device(cache, batch)
-    hq = _heads(q, "q", dev, (q.shape[0], q.shape[1], cache.head_dim))
-    rows, heads = q.shape[0], q.shape[1]
+    hq = _heads(q, "q", dev)
+    rows, heads, dim = q.shape
+    if dim != cache.head_dim:
+        raise QLoRAError(f"q must have the cache's head_dim {cache.head_dim}, not {dim}")
+    if window < 0:
+        raise QLoRAError("window must be 0 (none) or positive")
+    window = min(window, 2 ** 31 - 1)   # (past every cache's length, where a window is none)
 
     def run(stream):
         o, ho = _out(out, "out", dev, q.shape)

@@ -56,6 +56,12 @@ __device__ __forceinline__ int key_dword(int e) {
   const int r = e & (4 * N - 1);
   return (e & ~(4 * N - 1)) + (r & 3) * N + (r >> 2);
 }
+
+// the larger of a lane's value and that of the lane that the DPP control names
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
+}
 #endif
 
 // ---- head norms and rotation (qk_rope.hip) --------------------------------------------------

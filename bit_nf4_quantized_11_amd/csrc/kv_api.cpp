@@ -16,7 +16,7 @@ namespace {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int64_t kMaxRows = int64_t(1) << 26;
-constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxStride = int64_t(1) << 36;   // times the most rows: offsets stay within 62 bits
 constexpr int32_t kMaxHeads = 1024;
 
 bool head_dim_ok(int32_t d) { return d == 64 || d == 128 || d == 256; }

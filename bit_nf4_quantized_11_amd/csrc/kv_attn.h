@@ -58,10 +58,6 @@ __device__ __forceinline__ int exponent_of(uint32_t mag) { return min(max((int)(
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
-}
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   v = dpp_max<0xB1>(v);    // quad_perm [1, 0, 3, 2]
   v = dpp_max<0x4E>(v);    // quad_perm [2, 3, 0, 1]

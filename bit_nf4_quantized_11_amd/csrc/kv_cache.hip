@@ -78,11 +78,6 @@ __device__ __forceinline__ Slot<D> find_slot(const BatchView& b, const KvView& c
   return s;
 }
 
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
-}
-
 template <int D>
 __global__ __launch_bounds__(KT) void k_kv_write(Heads k, Heads v, KvView c, BatchView b, int bl, int zero, ThrLut lut) {
   constexpr int LR = D / 8, NT = KT / LR;   // lanes per row, rows per workgroup

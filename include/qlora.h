@@ -248,7 +248,7 @@ qlora_status qlora_state_page_in(const void* host, void* device, size_t bytes, h
  * ------------------------------------------------------------------------------------------- */
 
 /* A bf16 tensor [rows][heads][head_dim], as a projection leaves it: element (row, head, d) is
- * data[row * row_stride + head * head_stride + d].  Strides in elements, multiples of 8, >= 0;
+ * data[row * row_stride + head * head_stride + d].  Strides in elements, multiples of 8, 0 .. 2^36 - 1;
  * data 16-byte aligned.  So the queries and keys of one joint projection are two views of one
  * buffer, and [heads][rows][head_dim] is a view too.  An output's rows must not overlap: either
  * head_stride >= head_dim and row_stride >= (heads - 1) * head_stride + head_dim, or row_stride >=

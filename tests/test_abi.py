@@ -249,6 +249,9 @@ def test_qk_norm_rope_validation(lib):
     assert f(inter=2) == 4
     for eps in (-1.0, float("nan"), float("inf")):
         assert f(eps=eps) == 4
+    # strides whose offsets 64 bits might not hold
+    for s in ({"rs": 1 << 36}, {"hs": 1 << 36}, {"rs": -8}):
+        assert f(q=_hv(**s)) == 2 and f(qo=_hv(**s)) == 2
     # outputs whose rows overlap: neither row-major nor head-major
     for o in (_hv(hs=120), _hv(rs=256, hs=128), _hv(rs=0), _hv(hs=0)):
         assert f(qo=o) == 2
