@@ -14,7 +14,7 @@ import torch
 
 import bit_nf4_quantized_11_amd as Q
 from helpers import dev_bf16, host, log, require_gpu
-from kv_cases import bits, device_batch, fill_cache, i32, layout
+from kv_cases import Host, bits, device_batch, fill_cache, i32, layout
 from oracle import kv
 
 pytestmark = pytest.mark.gpu
@@ -137,6 +137,28 @@ def test_many_rows_of_some_among_many_sequences(dim):
     for i in (0, 5, 255, 256, 300, 511, 512, 513, 577, 599):
         lens[i], new[i] = 470 + i % 7, 460
     check(layout(lens, new, 16, 2), 1, 8, dim, 64, "nf4")
+
+
+def test_capacities_near_the_largest():
+    """Tables for 2^30 tokens a sequence, few of them used: the units of work get larger, so that their number fits 32
+    bits.  Four pages of 2^20 tokens that 300 sequences share, single tokens; then some with many rows."""
+    require_gpu()
+    dim, page, cols = 64, 1 << 20, 1024
+    four = layout([600] * 4, [600] * 4, 16, 3)          # (for its values alone)
+    rng = np.random.default_rng(4)
+    lens = [int(n) for n in rng.integers(1, 601, 300)]
+    _, ks, vs = fill_cache(layout([600], [1], 16, 3), 1, dim, 64, "nf4", 11)
+    cache = Q.kv_alloc(4, page, 1, dim)
+    x = {}
+    for t, seed in (("k", 11), ("v", 12)):
+        x[t] = dev_bf16(np.concatenate([bits(seed, (600, 1, dim))] * 4))
+    Q.qlora_kv_write(x["k"], x["v"], cache, Q.KVBatch(i32(four.start), i32([600] * 4), i32([[p] for p in range(4)])))
+    for new in ([1] * 300, [120] * 3 + [1] * 297):
+        n = [max(a, b) for a, b in zip(lens, new)]
+        table = np.full((300, cols), 2 ** 31 - 1, np.int32)
+        table[:, 0] = np.arange(300) % 4
+        h = Host(n, new, np.concatenate([[0], np.cumsum(new)]).astype(np.int32), table, 4, page)
+        check(h, 1, 4, dim, 64, "nf4", seed=5, cache=(cache, [ks[0][:a] for a in n], [vs[0][:a] for a in n]))
 
 
 def test_rows_without_a_token():
