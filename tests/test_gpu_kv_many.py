@@ -139,6 +139,17 @@ def test_many_rows_of_some_among_many_sequences(dim):
     check(layout(lens, new, 16, 2), 1, 8, dim, 64, "nf4")
 
 
+@pytest.mark.parametrize("dim,rows", [(64, 300), (128, 300), (256, 300), (128, 200)], ids=str)
+def test_one_prompt_among_single_tokens(dim, rows):
+    """A low mean of rows with one sequence of many: both kernels, or the one for few rows alone."""
+    require_gpu()
+    rng = np.random.default_rng(6)
+    lens = [int(n) for n in rng.integers(1, 90, 41)]
+    new = [1] * 41
+    lens[17], new[17] = rows + 30, rows
+    check(layout(lens, new, 16, 6), 1, 4, dim, 64, "int4")
+
+
 def test_capacities_near_the_largest():
     """Tables for 2^30 tokens a sequence, few of them used: the units of work get larger, so that their number fits 32
     bits.  Four pages of 2^20 tokens that 300 sequences share, single tokens; then some with many rows."""
