@@ -674,25 +674,32 @@ CodePlanes code_planes(int cb) {
 }
 
 // Sequences with at most this many rows per cache head go to the kernel of this file, those with more to the one for
-// many rows.  The host knows the rows and the sequences of a call, not which has how many: where the mean is low it leaves
-// all of them to the first kernel (which is right for any), with one sequence all to one, otherwise it launches both.
+// many rows.  The host knows the rows and the sequences of a call, not which has how many.  With one sequence it leaves all
+// to one kernel; with more, to the first (which is right for any) where the mean is low and no sequence can have more than
+// kAlone rows, each of the others having one; otherwise it launches both.
 // This kernel and the other one, 16 sequences of 4096 tokens, 32 cache heads: D = 64, 64 rows 101 and 221 us, 128 rows 181 and 219,
 // 160 rows 225 and 239; D = 128, 64 rows 176 and 242, 96 rows 248 and 243, 128 rows 329 and 256; D = 256, 64 rows 516 and
 // 555, 96 rows 754 and 561.  One sequence of 32768, 8 heads of 64: 64 rows 51 and 40 us, 128 rows 51 and 44.
 constexpr int few_rows(int D) { return D == 64 ? 128 : 64; }
+// 32 sequences of 4096, 8 cache heads of 128, one with 520 rows, the others with 4: 76 us by the first kernel, 91 by both; 64 of
+// 2000 and one of 8192 with 2048 rows 212 and 155; 300 of 1000 and one of 4096 with 16384 rows 809 and 343; 64 of 4096
+// with 32 rows each, where the second finds nothing to do, 100 and 104.
+constexpr int64_t kAlone = 1024;
 
 AttnPlan attn_plan(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t batch, int64_t max_len, int D) {
   AttnPlan p{};
-  const int64_t rows_h = rows * (q_heads / kv_heads), nseq = batch > 1 ? batch : 1;
+  const int64_t group = q_heads / kv_heads, rows_h = rows * group, nseq = batch > 1 ? batch : 1;
   const int few = few_rows(D);
-  if (rows_h <= few * nseq) p.few = INT32_MAX;
+  if (rows_h <= few * nseq && rows_h - (nseq - 1) * group <= kAlone) p.few = INT32_MAX;
   else p.few = nseq == 1 ? 0 : few;
   // Tiles of 32 rows decode a token once for twice the rows, but make half the units: they are taken where sequences have more
   // than 16 rows and every workgroup still has two units.  8 cache heads of 128, 32 and 64 rows of each sequence: 16
   // sequences of 4096 40 and 55 us (43 and 67 with tiles of 16), 4 of them 30 and 31 (23 and 28), one 21 and 22 (18 and
-  // 22).  D = 256 has no registers for it.
+  // 22).  Where the mean is that of a prompt, the sequences left for this kernel are taken to have single tokens (64 of them
+  // with 4096 tokens and 8 query heads per cache head beside a prompt: 69 us, 86 with tiles of 32).  D = 256 has no
+  // registers for it.
   const int64_t units32 = nseq * kv_heads * ((max_len >> kUnitShift) + 1);
-  const int nr = D < 256 && rows_h > 16 * nseq && units32 >= 2 * kCUs * waves_of(D, 2) ? 2 : 1;
+  const int nr = D < 256 && rows_h > 16 * nseq && rows_h <= few * nseq && units32 >= 2 * kCUs * waves_of(D, 2) ? 2 : 1;
   p.tile = 16 * nr;
   if (p.few > 0) {
     const int64_t tiles = ((rows_h + p.tile - 1) / p.tile + nseq) * kv_heads;
