@@ -8,6 +8,7 @@ CPU fallback: without the built library or a GPU the calls raise.
 from __future__ import annotations
 
 import ctypes as C
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -273,18 +274,22 @@ def qlora_state_page_in(host: torch.Tensor, dev: torch.Tensor, stream=None) -> t
 
 # ---- between the projections: head norms and rotation, the 4-bit key/value cache, its attention --------
 # These calls' kernels can take less time than a few lines of Python, so what every call does is kept short: the
-# stream's handle alone (a torch Stream object costs 2 us to make), and no context where none is needed.
+# stream's handle alone (a torch Stream object costs 2 us to make), no context where none is needed, and the views of
+# head tensors (qlora_heads) packed as bytes rather than made as ctypes structures.
+_view = struct.Struct("<Qqqii").pack   # data, row_stride, head_stride, heads, reserved
+
+
 def _launch(t: torch.Tensor, stream, run):
     """run(handle of the stream), with the tensor's device current and, where the caller named a stream, that
     stream current too, so that what `run` allocates belongs to it and is not reused before its kernels are done."""
     dev = t.device
     index = dev.index
     if stream is None and index == torch._C._cuda_getDevice():
-        return run(C.c_void_p(torch._C._cuda_getCurrentRawStream(index)))
+        return run(torch._C._cuda_getCurrentRawStream(index))
     if stream is not None and stream.device != dev:
         raise QLoRAError(f"the stream is on {stream.device}, the tensors on {dev}")
     with torch.cuda.device(dev), torch.cuda.stream(stream):
-        return run(C.c_void_p(torch._C._cuda_getCurrentRawStream(index)))
+        return run(torch._C._cuda_getCurrentRawStream(index))
 
 
 def _need(t, dtype, device, name, shape=None):
@@ -296,7 +301,7 @@ def _need(t, dtype, device, name, shape=None):
     return t
 
 
-def _heads(t: torch.Tensor, name: str, device=None, shape=None) -> _lib.qlora_heads:
+def _heads(t: torch.Tensor, name: str, device=None, shape=None) -> bytes:
     """The view of a bf16 [rows][heads][head_dim] tensor, any strides with a dense last dimension."""
     strides = t.stride()
     if t.dtype is not torch.bfloat16 or len(strides) != 3 or strides[2] != 1 or not t.is_cuda:
@@ -305,19 +310,19 @@ def _heads(t: torch.Tensor, name: str, device=None, shape=None) -> _lib.qlora_he
         raise QLoRAError(f"{name} must be on {device}")
     if shape is not None and t.shape != shape:
         raise QLoRAError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    return _lib.qlora_heads(t.data_ptr(), strides[0], strides[1], t.size(1), 0)
+    return _view(t.data_ptr(), strides[0], strides[1], t.size(1), 0)
 
 
-def _out(given, name: str, device, shape):
+def _out(given, name: str, device, rows: int, heads: int, dim: int):
     """An output and its view: the caller's, checked, or a new contiguous one."""
     if given is not None:
-        return given, _heads(given, name, device, shape)
-    t = torch.empty(shape, dtype=torch.bfloat16, device=device)
-    return t, _lib.qlora_heads(t.data_ptr(), shape[1] * shape[2], shape[2], shape[1], 0)
+        return given, _heads(given, name, device, (rows, heads, dim))
+    t = torch.empty(rows, heads, dim, dtype=torch.bfloat16, device=device)
+    return t, _view(t.data_ptr(), heads * dim, dim, heads, 0)
 
 
-def _ref(x):
-    return None if x is None else C.byref(x)
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _bytes(ws, device, need):
@@ -351,16 +356,13 @@ class KVCache:
         _need(self.v_codes, torch.uint8, c.device, "v_codes", tuple(c.shape))
         _need(self.k_scale, torch.bfloat16, c.device, "k_scale", scales)
         _need(self.v_scale, torch.bfloat16, c.device, "v_scale", scales)
-        # the fields are frozen, so the descriptor and the sizes are taken once
+        # the fields are frozen, so the descriptor (as an argument) and the sizes are taken once
         for name, value in (("pages", pages), ("heads", heads), ("page_size", page_size), ("head_dim", 2 * half),
                             ("device", c.device)):
             object.__setattr__(self, name, value)
-        object.__setattr__(self, "_desc", _lib.qlora_kv_cache(
+        object.__setattr__(self, "arg", C.byref(_lib.qlora_kv_cache(
             pages, page_size, heads, 2 * half, int(self.block), int(self.codebook), 0, self.k_codes.data_ptr(),
-            self.k_scale.data_ptr(), self.v_codes.data_ptr(), self.v_scale.data_ptr()))
-
-    def desc(self) -> _lib.qlora_kv_cache:
-        return self._desc
+            self.k_scale.data_ptr(), self.v_codes.data_ptr(), self.v_scale.data_ptr())))
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in (self.k_codes, self.k_scale, self.v_codes, self.v_scale))
@@ -405,12 +407,9 @@ class KVBatch:
         if self.fault is not None:
             _need(self.fault, torch.int32, dev, "fault", (1,))
         object.__setattr__(self, "device", dev)
-        object.__setattr__(self, "_desc", _lib.qlora_kv_batch(
+        object.__setattr__(self, "arg", C.byref(_lib.qlora_kv_batch(
             n, self.table.shape[1], self.start.data_ptr(), self.length.data_ptr(), self.table.data_ptr(),
-            None if self.fault is None else self.fault.data_ptr()))
-
-    def desc(self) -> _lib.qlora_kv_batch:
-        return self._desc
+            None if self.fault is None else self.fault.data_ptr())))
 
 
 def _same_device(cache: KVCache, batch: KVBatch):
@@ -419,33 +418,35 @@ def _same_device(cache: KVCache, batch: KVBatch):
     return cache.device
 
 
-def _keys(k, name: str, q):
-    """The view of k, or None: any number of heads, otherwise like q."""
+def _keys(k, name: str, device, rows: int, dim: int):
+    """(view, heads) of k, or (None, 0): any number of heads, otherwise like q."""
     if k is None:
-        return None
-    view = _heads(k, name, q.device)
-    if k.size(0) != q.size(0) or k.size(2) != q.size(2):
-        raise QLoRAError(f"{name} must have {q.size(0)} rows of head_dim {q.size(2)}, not {tuple(k.shape)}")
-    return view
+        return None, 0
+    view = _heads(k, name, device)
+    n, heads, d = k.shape
+    if n != rows or d != dim:
+        raise QLoRAError(f"{name} must have {rows} rows of head_dim {dim}, not {tuple(k.shape)}")
+    return view, heads
 
 
-def _qk_inputs(q, k, positions, inv_freq, q_weight, k_weight):
-    rows, _, dim = q.shape
-    dev = q.device
+def _qk_inputs(k, dev, rows, dim, positions, inv_freq, q_weight, k_weight) -> int:
+    """Checks what both directions take; the rotated elements of a head."""
     rot = 0
     if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        _need(inv_freq, torch.float32, dev, "inv_freq", (inv_freq.numel(),))
+        half = inv_freq.numel()
+        rot = 2 * half
+        _need(inv_freq, torch.float32, dev, "inv_freq", (half,))
     if rot:
         if positions is None:
             raise QLoRAError("inv_freq needs positions")
         _need(positions, torch.int64, dev, "positions", (rows,))
     if k is None and k_weight is not None:
         raise QLoRAError("k_weight needs k")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, torch.bfloat16, dev, name, (dim,))
-    return rows, dim, rot, dev
+    if q_weight is not None:
+        _need(q_weight, torch.bfloat16, dev, "q_weight", (dim,))
+    if k_weight is not None:
+        _need(k_weight, torch.bfloat16, dev, "k_weight", (dim,))
+    return rot
 
 
 def qlora_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor | None,
@@ -455,17 +456,18 @@ def qlora_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch
     """Norm of each head (where its weight is given) and rotation by positions [rows] (int64) * inv_freq
     [rot_dim / 2] (fp32) of q, k [rows][heads][head_dim] bf16, any strides.  The outputs may be the inputs.
     Returns (q_out, k_out or None)."""
-    hq = _heads(q, "q")
-    hk = _keys(k, "k", q)
-    rows, dim, rot, dev = _qk_inputs(q, k, positions, inv_freq, q_weight, k_weight)
+    hq, dev = _heads(q, "q"), q.device
+    rows, q_heads, dim = q.shape
+    hk, k_heads = _keys(k, "k", dev, rows, dim)
+    rot = _qk_inputs(k, dev, rows, dim, positions, inv_freq, q_weight, k_weight)
     if k is None and k_out is not None:
         raise QLoRAError("k_out needs k")
 
     def run(stream):
-        qo, oq = _out(q_out, "q_out", dev, q.shape)
-        ko, ok = (None, None) if k is None else _out(k_out, "k_out", dev, k.shape)
-        _check(lib().qlora_qk_norm_rope(_ref(hq), _ref(hk), rows, dim, _ptr(q_weight), _ptr(k_weight), eps,
-                                        _ptr(positions), _ptr(inv_freq), rot, interleaved, _ref(oq), _ref(ok), stream),
+        qo, oq = _out(q_out, "q_out", dev, rows, q_heads, dim)
+        ko, ok = (None, None) if k is None else _out(k_out, "k_out", dev, rows, k_heads, dim)
+        _check(lib().qlora_qk_norm_rope(hq, hk, rows, dim, _at(q_weight), _at(k_weight), eps,
+                                        _at(positions), _at(inv_freq), rot, interleaved, oq, ok, stream),
                "qlora_qk_norm_rope")
         return qo, ko
 
@@ -485,21 +487,22 @@ def qlora_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q:
     """Gradients of qlora_qk_norm_rope's inputs from those of its outputs; q, k are the forward's inputs
     (needed where there is a weight).  dq may be dq_out and dk may be dk_out.  Returns (dq, dk or None,
     dq_weight or None, dk_weight or None), the weights' fp32 [head_dim]."""
-    gq = _heads(dq_out, "dq_out")
-    gk = _keys(dk_out, "dk_out", dq_out)
-    rows, dim, rot, dev = _qk_inputs(dq_out, dk_out, positions, inv_freq, q_weight, k_weight)
+    gq, dev = _heads(dq_out, "dq_out"), dq_out.device
+    rows, q_heads, dim = dq_out.shape
+    gk, k_heads = _keys(dk_out, "dk_out", dev, rows, dim)
+    rot = _qk_inputs(dk_out, dev, rows, dim, positions, inv_freq, q_weight, k_weight)
     if (q_weight is not None and q is None) or (k_weight is not None and k is None):
         raise QLoRAError("a weight's gradient needs the forward's input")
-    xq = _heads(q, "q", dev, dq_out.shape) if q_weight is not None else None
-    xk = _heads(k, "k", dev, dk_out.shape) if k_weight is not None else None
+    xq = _heads(q, "q", dev, (rows, q_heads, dim)) if q_weight is not None else None
+    xk = _heads(k, "k", dev, (rows, k_heads, dim)) if k_weight is not None else None
     if dk_out is None and dk is not None:
         raise QLoRAError("dk needs dk_out")
     if (q_weight is None and dq_weight is not None) or (k_weight is None and dk_weight is not None):
         raise QLoRAError("a weight's gradient needs the weight")
 
     def run(stream):
-        oq, hq = _out(dq, "dq", dev, dq_out.shape)
-        ok, hk = (None, None) if dk_out is None else _out(dk, "dk", dev, dk_out.shape)
+        oq, hq = _out(dq, "dq", dev, rows, q_heads, dim)
+        ok, hk = (None, None) if dk_out is None else _out(dk, "dk", dev, rows, k_heads, dim)
         gwq, gwk = dq_weight, dk_weight
         if q_weight is not None:
             gwq = torch.empty(dim, dtype=torch.float32, device=dev) if gwq is None else \
@@ -509,11 +512,10 @@ def qlora_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q:
                 _need(gwk, torch.float32, dev, "dk_weight", (dim,))
         ws = None
         if q_weight is not None or k_weight is not None:
-            ws = _bytes(workspace, dev, lambda: qlora_qk_norm_rope_bwd_workspace(
-                rows, gq.heads, 0 if gk is None else gk.heads, dim))
-        _check(lib().qlora_qk_norm_rope_bwd(_ref(gq), _ref(gk), _ref(xq), _ref(xk), rows, dim, _ptr(q_weight),
-                                            _ptr(k_weight), eps, _ptr(positions), _ptr(inv_freq), rot, interleaved,
-                                            _ref(hq), _ref(hk), _ptr(gwq), _ptr(gwk), _ptr(ws),
+            ws = _bytes(workspace, dev, lambda: qlora_qk_norm_rope_bwd_workspace(rows, q_heads, k_heads, dim))
+        _check(lib().qlora_qk_norm_rope_bwd(gq, gk, xq, xk, rows, dim, _at(q_weight),
+                                            _at(k_weight), eps, _at(positions), _at(inv_freq), rot, interleaved,
+                                            hq, hk, _at(gwq), _at(gwk), _at(ws),
                                             0 if ws is None else ws.nbytes, stream), "qlora_qk_norm_rope_bwd")
         return oq, ok, gwq, gwk
 
@@ -526,7 +528,7 @@ def qlora_kv_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, batch: KVBa
     shape = (len(k) if k.dim() else 0, cache.heads, cache.head_dim)
     hk, hv = _heads(k, "k", dev, shape), _heads(v, "v", dev, shape)
     _launch(k, stream, lambda stream: _check(
-        lib().qlora_kv_write(_ref(hk), _ref(hv), shape[0], _ref(cache.desc()), _ref(batch.desc()), stream),
+        lib().qlora_kv_write(hk, hv, shape[0], cache.arg, batch.arg, stream),
         "qlora_kv_write"))
 
 
@@ -535,12 +537,11 @@ def qlora_kv_read(cache: KVCache, batch: KVBatch, rows: int, k: torch.Tensor | N
     """The batch's rows read back from the cache: (k, v) [rows][heads][head_dim] bf16.  Rows of no sequence
     keep what k and v hold (undefined if they are not given)."""
     dev = _same_device(cache, batch)
-    shape = (rows, cache.heads, cache.head_dim)
 
     def run(stream):
-        ko, hk = _out(k, "k", dev, shape)
-        vo, hv = _out(v, "v", dev, shape)
-        _check(lib().qlora_kv_read(_ref(cache.desc()), _ref(batch.desc()), rows, _ref(hk), _ref(hv), stream),
+        ko, hk = _out(k, "k", dev, rows, cache.heads, cache.head_dim)
+        vo, hv = _out(v, "v", dev, rows, cache.heads, cache.head_dim)
+        _check(lib().qlora_kv_read(cache.arg, batch.arg, rows, hk, hv, stream),
                "qlora_kv_read")
         return ko, vo
 
@@ -548,7 +549,7 @@ def qlora_kv_read(cache: KVCache, batch: KVBatch, rows: int, k: torch.Tensor | N
 
 
 def qlora_kv_attn_workspace(cache: KVCache, batch: KVBatch, rows: int, q_heads: int) -> int:
-    return lib().qlora_kv_attn_workspace(_ref(cache.desc()), _ref(batch.desc()), rows, q_heads)
+    return lib().qlora_kv_attn_workspace(cache.arg, batch.arg, rows, q_heads)
 
 
 def qlora_kv_attn(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float | None = None, causal: bool = True,
@@ -567,16 +568,16 @@ def qlora_kv_attn(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float 
     window = min(window, 2 ** 31 - 1)   # (past every cache's length, where a window is none)
 
     def run(stream):
-        o, ho = _out(out, "out", dev, q.shape)
+        o, ho = _out(out, "out", dev, rows, heads, dim)
         sums = None
         if lse is True:
             sums = torch.empty((rows, heads), dtype=torch.float32, device=dev)
         elif lse is not False and lse is not None:
             sums = _need(lse, torch.float32, dev, "lse", (rows, heads))
         ws = _bytes(workspace, dev, lambda: qlora_kv_attn_workspace(cache, batch, rows, heads))
-        _check(lib().qlora_kv_attn(_ref(hq), rows, _ref(cache.desc()), _ref(batch.desc()),
-                                   cache.head_dim ** -0.5 if scale is None else scale, causal, window, _ref(ho),
-                                   _ptr(sums), _ptr(ws), ws.nbytes, stream), "qlora_kv_attn")
+        _check(lib().qlora_kv_attn(hq, rows, cache.arg, batch.arg,
+                                   cache.head_dim ** -0.5 if scale is None else scale, causal, window, ho,
+                                   _at(sums), _at(ws), ws.nbytes, stream), "qlora_kv_attn")
         return o, sums
 
     return _launch(q, stream, run)

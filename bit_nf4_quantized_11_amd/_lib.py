@@ -56,6 +56,8 @@ class qlora_kernel_time(C.Structure):
     _fields_ = [("name", C.c_char * 48), ("launches", C.c_int64), ("total_ms", C.c_double)]
 
 
+_HEADS = C.c_void_p   # const qlora_heads*: a structure by reference, or its bytes
+
 # name -> (restype, argtypes); every name is declared in include/qlora.h
 SIGNATURES = {
     "qlora_status_str": (C.c_char_p, [C.c_int]),
@@ -83,24 +85,24 @@ SIGNATURES = {
                                    C.c_size_t, C.c_void_p]),
     "qlora_state_page_out": (C.c_int, [C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
     "qlora_state_page_in": (C.c_int, [C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
-    "qlora_qk_norm_rope": (C.c_int, [C.POINTER(qlora_heads), C.POINTER(qlora_heads), C.c_int64, C.c_int32, C.c_void_p,
+    "qlora_qk_norm_rope": (C.c_int, [_HEADS, _HEADS, C.c_int64, C.c_int32, C.c_void_p,
                                      C.c_void_p, C.c_float, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
-                                     C.POINTER(qlora_heads), C.POINTER(qlora_heads), C.c_void_p]),
+                                     _HEADS, _HEADS, C.c_void_p]),
     "qlora_qk_norm_rope_bwd_workspace": (C.c_size_t, [C.c_int64, C.c_int32, C.c_int32, C.c_int32]),
-    "qlora_qk_norm_rope_bwd": (C.c_int, [C.POINTER(qlora_heads), C.POINTER(qlora_heads), C.POINTER(qlora_heads),
-                                         C.POINTER(qlora_heads), C.c_int64, C.c_int32, C.c_void_p, C.c_void_p,
+    "qlora_qk_norm_rope_bwd": (C.c_int, [_HEADS, _HEADS, _HEADS,
+                                         _HEADS, C.c_int64, C.c_int32, C.c_void_p, C.c_void_p,
                                          C.c_float, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
-                                         C.POINTER(qlora_heads), C.POINTER(qlora_heads), C.c_void_p, C.c_void_p,
+                                         _HEADS, _HEADS, C.c_void_p, C.c_void_p,
                                          C.c_void_p, C.c_size_t, C.c_void_p]),
     "qlora_kv_sizes": (C.c_int, [C.POINTER(qlora_kv_cache), C.POINTER(C.c_size_t), C.POINTER(C.c_size_t)]),
-    "qlora_kv_write": (C.c_int, [C.POINTER(qlora_heads), C.POINTER(qlora_heads), C.c_int64, C.POINTER(qlora_kv_cache),
+    "qlora_kv_write": (C.c_int, [_HEADS, _HEADS, C.c_int64, C.POINTER(qlora_kv_cache),
                                  C.POINTER(qlora_kv_batch), C.c_void_p]),
     "qlora_kv_read": (C.c_int, [C.POINTER(qlora_kv_cache), C.POINTER(qlora_kv_batch), C.c_int64,
-                                C.POINTER(qlora_heads), C.POINTER(qlora_heads), C.c_void_p]),
+                                _HEADS, _HEADS, C.c_void_p]),
     "qlora_kv_attn_workspace": (C.c_size_t, [C.POINTER(qlora_kv_cache), C.POINTER(qlora_kv_batch), C.c_int64,
                                              C.c_int32]),
-    "qlora_kv_attn": (C.c_int, [C.POINTER(qlora_heads), C.c_int64, C.POINTER(qlora_kv_cache),
-                                C.POINTER(qlora_kv_batch), C.c_float, C.c_int32, C.c_int32, C.POINTER(qlora_heads),
+    "qlora_kv_attn": (C.c_int, [_HEADS, C.c_int64, C.POINTER(qlora_kv_cache),
+                                C.POINTER(qlora_kv_batch), C.c_float, C.c_int32, C.c_int32, _HEADS,
                                 C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
     "qlora_profile_enable": (C.c_int, [C.c_int32]),
     "qlora_profile_read": (C.c_int32, [C.POINTER(qlora_kernel_time), C.c_int32, C.c_int32]),
