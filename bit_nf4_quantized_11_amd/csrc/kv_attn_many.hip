@@ -440,7 +440,9 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
           if (n >= hi || n < lo) S[tt][i] = neg_inf();
         }
     }
-    const float f = rs * pow2(cur.k);
+    // Not 0 (zero queries and zero keys have exponents that add up to -200), which the -inf of a masked token would turn into
+    // NaN.  The products are below 2^14, so logits of a smaller factor are 0 all the same.
+    const float f = fmaxf(rs * pow2(cur.k), 0x1p-126f);
     float mx = S[0][0];
 #pragma unroll
     for (int tt = 0; tt < 2; ++tt)

@@ -1,0 +1,88 @@
+"""The 4-bit cache and its attention where ordinary data does not lead: rows of zeros and of infinities, scales at both
+ends, entries behind a window, starts out of order, workspaces of other calls."""
+import numpy as np
+import pytest
+import torch
+
+import bit_nf4_quantized_11_amd as Q
+import test_gpu_kv_many as many
+from helpers import dev_bf16, host, log, require_gpu
+from kv_cases import Host, bits, device_batch, i32, layout
+from oracle import kv
+
+pytestmark = pytest.mark.gpu
+
+FAULT_START, FAULT_LENGTH, FAULT_PAGE = 1, 2, 4
+
+
+def _word():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def written(h: Host, k16, v16, heads, dim, block):
+    """A cache that holds k16, v16 [b] -> [len][heads][dim] (bf16 bits), and what its rows stand for in float64."""
+    cache = Q.kv_alloc(h.pages, h.page, heads, dim, block)
+    for t in (cache.k_scale, cache.v_scale):
+        t.fill_(float("nan"))
+    full = Q.KVBatch(i32(np.concatenate([[0], np.cumsum(h.lens)])), i32(h.lens), i32(h.table))
+    Q.qlora_kv_write(*(dev_bf16(np.concatenate(x)) for x in (k16, v16)), cache, full)
+    value = lambda x: np.stack([[kv.row_values(*kv.quantize_row(r, block, "nf4"), "nf4") for r in t] for t in x])
+    return cache, [value(x) for x in k16], [value(x) for x in v16]
+
+
+def against_oracle(h, q16, cache, ks, vs, causal=True, window=0, scale=None):
+    """The attention of q16 [rows][q_heads][dim] within the tolerance derived for many rows (which holds for few)."""
+    heads, dim = cache.heads, cache.head_dim
+    scale = dim ** -0.5 if scale is None else scale
+    fault = _word()
+    o, lse = Q.qlora_kv_attn(dev_bf16(q16), cache, device_batch(h, fault), scale, causal, window, lse=True)
+    assert fault.item() == 0
+    got, gl = host(o.float()).astype(np.float64), host(lse).astype(np.float64)
+    want, wl, bound = np.zeros_like(got), np.zeros_like(gl), np.zeros_like(got)
+    for b in range(len(h.lens)):
+        r = slice(h.start[b], h.start[b + 1])
+        want[r], wl[r], bound[r] = kv.attention(kv.f64(q16[r]), ks[b], vs[b], h.lens[b], scale, causal, window)
+    tol, err = many.tolerance(h, q16, ks, vs, q16.shape[1] // heads, "nf4", scale, want, bound)
+    d = np.abs(got - want)
+    assert np.all(np.isfinite(got)), np.argwhere(~np.isfinite(got))[:3]
+    assert np.all(d <= tol), (d.max(), (d / np.maximum(tol, 1e-300)).max())
+    empty = np.isneginf(wl)
+    assert np.array_equal(empty, np.isneginf(gl)) and np.all(got[empty] == 0)
+    assert np.all(np.abs(gl - wl)[~empty] <= err[~empty] + 2.0 ** -20 * (1 + np.abs(wl[~empty])))
+
+
+ZERO = [
+    # dim, block, lens, new, causal, window: the kernel for many rows (and, for the last, both)
+    (64, 64, [150], [150], True, 0),
+    (128, 64, [333], [200], True, 0),
+    (256, 32, [130], [130], True, 0),
+    (64, 32, [201], [140], False, 0),
+    (128, 128, [201, 90], [80, 90], False, 0),
+    (256, 64, [100], [70], False, 0),
+    (128, 32, [300], [280], True, 17),
+    (64, 64, [300], [140], True, 100),
+    (128, 64, [1500], [40], True, 0),        # in parts
+    (256, 128, [900], [35], False, 0),       # in parts
+    (128, 64, [90, 150, 70], [1, 150, 3], True, 0),
+]
+
+
+@pytest.mark.parametrize("what", ["all", "tail", "tiny"])
+@pytest.mark.parametrize("dim,block,lens,new,causal,window", ZERO, ids=str)
+def test_zero_queries_over_zero_keys(dim, block, lens, new, causal, window, what):
+    """All queries and keys zero; those of the last 70 rows and tokens (padding); or both so small (2^-75) that their product
+    is no fp32 number.  Such rows attend what they see evenly."""
+    require_gpu()
+    log("zeros", dim, block, lens, new, causal, window, what)
+    heads, group = 1, 2
+    h = layout(lens, new, 16, dim + sum(new))
+    std = 2.0 ** -75 if what == "tiny" else 1.0
+    k = [bits(3 + b, (n, heads, dim), std) for b, n in enumerate(lens)]
+    v = [bits(30 + b, (n, heads, dim)) for b, n in enumerate(lens)]
+    q = bits(9, (h.rows, heads * group, dim), std)
+    for b, n in enumerate(new):
+        if what != "tiny":
+            at = 0 if what == "all" else max(0, n - 70)
+            q[h.start[b] + at:h.start[b + 1]] = 0
+            k[b][0 if what == "all" else max(0, lens[b] - 70):] = 0
+    against_oracle(h, q, *written(h, k, v, heads, dim, block), causal, window)
