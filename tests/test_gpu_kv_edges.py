@@ -86,3 +86,16 @@ def test_zero_queries_over_zero_keys(dim, block, lens, new, causal, window, what
             q[h.start[b] + at:h.start[b + 1]] = 0
             k[b][0 if what == "all" else max(0, lens[b] - 70):] = 0
     against_oracle(h, q, *written(h, k, v, heads, dim, block), causal, window)
+
+
+@pytest.mark.parametrize("dim,new", [(64, 1), (128, 5), (256, 1), (64, 150), (128, 150), (256, 80)], ids=str)
+@pytest.mark.parametrize("scale", [1e-20, 2.0 ** -149, 2.0 ** 127], ids=str)
+def test_scales_at_the_ends_of_their_range(dim, new, scale):
+    """Rows of zeros, whose logits are zero under any scale; and under a tiny one, ordinary rows."""
+    require_gpu()
+    log("scale", dim, new, scale)
+    h = layout([200], [new], 16, dim)
+    k, v = ([bits(s, (200, 1, dim))] for s in (3, 4))
+    q = bits(9, (new, 2, dim), 1.0 if scale < 1 else 0.0)
+    q[::2] = 0
+    against_oracle(h, q, *written(h, k, v, 1, dim, 64), scale=scale)
