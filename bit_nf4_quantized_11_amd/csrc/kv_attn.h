@@ -55,6 +55,9 @@ __device__ __forceinline__ u32x4 decode_pairs(const uint32_t* pair, uint32_t w) 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 <= e <= 127
 // exponent of a bf16 magnitude, kept where its power of two and the inverse are ordinary numbers
 __device__ __forceinline__ int exponent_of(uint32_t mag) { return min(max((int)(mag >> 7) - 127, -100), 126); }
+// What a row of q is multiplied with: 2^-e, or NaN where it holds an infinity (or a NaN): its logits have no softmax, but
+// where all of them are -inf they would pass for those of masked tokens.
+__device__ __forceinline__ float row_unit(uint32_t mag, int e) { return mag < 0x7F80u ? pow2(-e) : __builtin_nanf(""); }
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 

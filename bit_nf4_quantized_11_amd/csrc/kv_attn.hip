@@ -235,7 +235,7 @@ __global__ __launch_bounds__(AT, waves_of(D, NR)) void k_kv_attn(AttnArgs a, Cod
       mag = max(mag, (uint32_t)__shfl_xor((int)mag, 16, 64));
       mag = max(mag, (uint32_t)__shfl_xor((int)mag, 32, 64));
       const int e = exponent_of(mag);
-      const float f = pow2(-e);
+      const float f = row_unit(mag, e);
       // not 0, which a masked token's -inf would turn into NaN, and finite, so that products of 0 stay 0
       rs[r] = fminf(fmaxf(kmul * pow2(e), 0x1p-149f), 0x1.fffffep127f);
       // in the order that pairs decode to: 0, 4, 1, 5, 2, 6, 3, 7

@@ -367,7 +367,7 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
     }
     mag = max(mag, (uint32_t)__shfl_xor((int)mag, 32, 64));
     const int e = exponent_of(mag);
-    const float f = pow2(-e);
+    const float f = row_unit(mag, e);
     rs = a.scale * kLog2e * cp.inv * pow2(e);
 #pragma unroll
     for (int k = 0; k < KK; ++k)

@@ -99,3 +99,28 @@ def test_scales_at_the_ends_of_their_range(dim, new, scale):
     q = bits(9, (new, 2, dim), 1.0 if scale < 1 else 0.0)
     q[::2] = 0
     against_oracle(h, q, *written(h, k, v, 1, dim, 64), scale=scale)
+
+
+@pytest.mark.parametrize("dim,new", [(64, 3), (128, 3), (256, 3), (64, 150), (128, 150), (256, 80)], ids=str)
+def test_infinite_queries(dim, new):
+    """A row of q with an infinity has no softmax, also where every product is -infinity: NaN if it sees a token, nothing
+    if it sees none, and no other row is touched."""
+    require_gpu()
+    n = new - 1                              # the first row has no token
+    h = layout([n], [new], 16, dim)
+    k, v = ([bits(s, (n, 1, dim))] for s in (3, 4))
+    k[0][:, 0, 5] = 0x3F80                   # element 5 of every key is positive
+    cache, _, _ = written(h, k, v, 1, dim, 64)
+    q = bits(9, (new, 2, dim))
+    batch = device_batch(h)
+    ref, rl = Q.qlora_kv_attn(dev_bf16(q), cache, batch, lse=True)
+    for value in (0xFF80, 0x7F80, 0x7FC0):
+        x = q.copy()
+        for row in (0, 1, new - 1):
+            x[row, 1, 5] = value
+        o, lse = Q.qlora_kv_attn(dev_bf16(x), cache, batch, lse=True)
+        bad = torch.zeros(new, 2, dtype=torch.bool, device="cuda")
+        bad[1, 1] = bad[new - 1, 1] = True
+        assert torch.isnan(o[bad]).all() and torch.isnan(lse[bad]).all()
+        assert torch.equal(o[~bad], ref[~bad]) and torch.equal(lse[~bad], rl[~bad])
+        assert torch.all(o[0] == 0) and torch.isneginf(lse[0]).all()
