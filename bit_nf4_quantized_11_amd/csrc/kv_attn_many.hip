@@ -67,7 +67,7 @@ struct ManyLoads {
 
 template <int D, int NB, bool SKIP>
 __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_attn_many(AttnArgs a, CodePlanes cp0,
-                                                                                        int split) {
+                                                                                        int split, int cuts) {
   using Loads = ManyLoads<D, NB>;
   constexpr int T = Loads::T, MW = T / 64, TR = 32 * MW, B = D / NB, CH = Loads::CH, ITEMS = Loads::ITEMS;
   constexpr int NKS = Loads::NKS, KN = Loads::KN, KK = D / 16, DT = D / 32, RB = D / 2;
@@ -107,7 +107,8 @@ __global__ __launch_bounds__(many_threads(D), many_threads(D) / 256) void k_kv_a
   int splits = 1;
   if (split) {
     const int most = __builtin_amdgcn_readfirstlane(found) / split;
-    if (total <= kSplitWgs / a.c.heads) splits = max(min(most, kSplitWgs / max(total * a.c.heads, 1)), 1);
+    // (entries out of order can make more tiles than the workspace and the join were sized for: those stay whole)
+    if (total <= cuts / a.c.heads) splits = max(min(most, kSplitWgs / max(total * a.c.heads, 1)), 1);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       a.meta[0] = total;
       a.meta[1] = splits;
@@ -575,8 +576,11 @@ static hipError_t launch_many(const AttnArgs& a, const AttnPlan& pl, hipStream_t
     const CodePlanes cp = code_planes(a.c.cb);
     // (for D = 64 such tiles are the other kernel's, 160 rows 83 us either way; for D = 256 the second loop body spills
     // registers, 16 sequences of 40 rows 305 us with it, 289 without)
-    if (D == 128 && pl.sparse) hipLaunchKernelGGL((k_kv_attn_many<D, NB, D == 128>), g, t, 0, s, a, cp, pl.split_tokens);
-    else hipLaunchKernelGGL((k_kv_attn_many<D, NB, false>), g, t, 0, s, a, cp, pl.split_tokens);
+    const int cuts = (int)pl.many_split;
+    if (D == 128 && pl.sparse)
+      hipLaunchKernelGGL((k_kv_attn_many<D, NB, D == 128>), g, t, 0, s, a, cp, pl.split_tokens, cuts);
+    else
+      hipLaunchKernelGGL((k_kv_attn_many<D, NB, false>), g, t, 0, s, a, cp, pl.split_tokens, cuts);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !pl.many_split) return e;
   }

@@ -124,3 +124,26 @@ def test_infinite_queries(dim, new):
         assert torch.isnan(o[bad]).all() and torch.isnan(lse[bad]).all()
         assert torch.equal(o[~bad], ref[~bad]) and torch.equal(lse[~bad], rl[~bad])
         assert torch.all(o[0] == 0) and torch.isneginf(lse[0]).all()
+
+
+def test_starts_that_go_back_stay_inside_the_workspace():
+    """Starts that name the same 1500 rows eleven times: more tiles than the workspace of a call in order has room for
+    when they are cut into parts.  They are left whole, nothing is written past the workspace, and the rows hold the result."""
+    require_gpu()
+    dim, page, rows, length = 128, 64, 1500, 4096
+    one = layout([length], [rows], page, 5, spare_cols=0)
+    q = bits(9, (rows, 1, dim))
+    cache, ks, vs = written(one, [bits(3, (length, 1, dim))], [bits(4, (length, 1, dim))], 1, dim, 64)
+    start = [0, rows] * 11
+    n = len(start) - 1
+    fault = _word()
+    batch = Q.KVBatch(i32(start), i32([length] * n), i32(np.repeat(one.table, n, 0)), fault)
+    need = Q.qlora_kv_attn_workspace(cache, batch, rows, 1)
+    guarded = torch.full((need + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    o, lse = Q.qlora_kv_attn(dev_bf16(q), cache, batch, lse=True, workspace=guarded[:need])
+    assert fault.item() == FAULT_START
+    assert torch.all(guarded[need:] == 0xA5)
+    want, wl, bound = kv.attention(kv.f64(q), ks[0], vs[0], length, dim ** -0.5)
+    tol, err = many.tolerance(one, q, ks, vs, 1, "nf4", dim ** -0.5, want, bound)
+    assert np.all(np.abs(host(o.float()) - want) <= tol)
+    assert np.all(np.abs(host(lse) - wl) <= err + 2.0 ** -20 * (1 + np.abs(wl)))
