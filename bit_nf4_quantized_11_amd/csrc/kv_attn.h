@@ -154,7 +154,8 @@ __device__ __forceinline__ void check_batch_entries(const BatchView& b) {
 struct Tile {
   Seq s;
   int32_t b, h, rho0, nval;      // sequence, cache head, first row of the tile and rows it has
-  int32_t base, hi, hi_min, lo_max;   // tokens base .. hi - 1 are seen by some row, lo_max .. hi_min - 1 by all
+  int32_t base, hi, hi_min, lo_max;   // tokens base .. hi - 1 hold what its rows see, lo_max .. hi_min - 1 are seen by all
+  int32_t skip;                       // how many tokens from base on, fewer than 64, no row sees
 };
 
 // n / a.group for 0 <= n < 2^31 (a product and a shift: a division is 30 dependent instructions)
@@ -178,6 +179,7 @@ __device__ __forceinline__ Tile tile_of(const AttnArgs& a, const Seq& s, int b, 
   const int lo = a.window ? max(p0 + 1 - a.window, 0) : 0;
   t.lo_max = a.window ? max(p1 + 1 - a.window, 0) : 0;
   t.base = lo & ~63;
+  t.skip = lo & 63;
   return t;
 }
 

@@ -344,6 +344,13 @@ __global__ __launch_bounds__(AT, waves_of(D, NR)) void k_kv_attn(AttnArgs a, Cod
       const Pages pg = pages_of(pid);
       load_v(L, st, pid, pg);
       load_k(L, st, pid, pg);
+      // tokens at the front that no row sees (lane 0 has the tile's first row; held ready in the tile, it took 6 registers more)
+      const int skip = st == 0 && a.window ? __builtin_amdgcn_readfirstlane(r_lo[0]) - t.base : 0;
+      if (skip > 0 && lane < skip) {   // neither their scales nor their pages' entries count
+        pid = 0;
+#pragma unroll
+        for (int x = 0; x < (NB + 1) / 2; ++x) L.ks[x] = L.vs[x] = 0;
+      }
     }
     // this lane's token row of the transposing reads: row n of 16 is token 8 (n / 8) + (n % 8) / 2 + 4 (n % 2), so that a
     // dword of what comes back decodes in token order

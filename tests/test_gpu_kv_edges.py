@@ -147,3 +147,61 @@ def test_starts_that_go_back_stay_inside_the_workspace():
     tol, err = many.tolerance(one, q, ks, vs, 1, "nf4", dim ** -0.5, want, bound)
     assert np.all(np.abs(host(o.float()) - want) <= tol)
     assert np.all(np.abs(host(lse) - wl) <= err + 2.0 ** -20 * (1 + np.abs(wl)))
+
+
+BEHIND = [
+    # dim, page, lens, new, window: both kernels, with and without parts
+    (128, 16, [777], [1], 100),
+    (64, 32, [500, 90], [5, 2], 70),
+    (256, 16, [300], [3], 33),
+    (64, 16, [420], [150], 45),
+    (128, 32, [730], [140], 90),
+    (256, 16, [300], [70], 21),
+    (128, 16, [1400, 1, 600], [90, 1, 100], 700),
+]
+
+
+def _first_seen(h, b, window):
+    return max(0, h.lens[b] - h.new[b] + 1 - window)
+
+
+@pytest.mark.parametrize("dim,page,lens,new,window", BEHIND, ids=str)
+def test_pages_behind_the_window_may_be_gone(dim, page, lens, new, window):
+    """Pages that lie behind the window of every row, given back and their entries set to -1, are not needed."""
+    require_gpu()
+    log("behind", dim, page, lens, new, window)
+    h = layout(lens, new, page, dim)
+    k, v = ([bits(s + b, (n, 1, dim)) for b, n in enumerate(lens)] for s in (3, 30))
+    cache, ks, vs = written(h, k, v, 1, dim, 64)
+    q = bits(9, (h.rows, 4, dim))
+    want = Q.qlora_kv_attn(dev_bf16(q), cache, device_batch(h), window=window, lse=True)
+    gone = 0
+    for b in range(len(lens)):
+        first = _first_seen(h, b, window) // page
+        h.table[b, :first] = -1
+        gone += first
+    assert gone
+    fault = _word()
+    got = Q.qlora_kv_attn(dev_bf16(q), cache, device_batch(h, fault), window=window, lse=True)
+    assert fault.item() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    against_oracle(h, q, cache, ks, vs, True, window)
+
+
+@pytest.mark.parametrize("dim,page,lens,new,window", BEHIND, ids=str)
+@pytest.mark.parametrize("what", [2.0 ** 40, float("nan")], ids=str)
+def test_tokens_behind_the_window_do_not_reach_a_row(dim, page, lens, new, window, what):
+    """Slots behind the window of every row may hold anything, far larger scales among it: the same bits."""
+    require_gpu()
+    h = layout(lens, new, page, dim)
+    k, v = ([bits(s + b, (n, 1, dim)) for b, n in enumerate(lens)] for s in (3, 30))
+    cache, _, _ = written(h, k, v, 1, dim, 64)
+    q = dev_bf16(bits(9, (h.rows, 4, dim)))
+    want = Q.qlora_kv_attn(q, cache, device_batch(h), window=window, lse=True)
+    for b in range(len(lens)):
+        for p in range(_first_seen(h, b, window)):
+            at = int(h.table[b, p // page]), slice(None), p % page
+            cache.k_scale[at] *= what
+            cache.v_scale[at] *= what
+    got = Q.qlora_kv_attn(q, cache, device_batch(h), window=window, lse=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
