@@ -32,30 +32,38 @@ struct Slot {
   int32_t off;
 };
 
-// The slots of rows t0 .. t0 + NT - 1 (row t0 + r for the lanes of group r).  The sequence of a row
-// is the number of start[b + 1] that are not past it: all of them are read at once by the
-// workgroup and counted into the row where they begin to count, so a batch of any size costs one round trip
-// (a search by halves costs one per halving).
+// The slots of rows t0 .. t0 + NT - 1 (row t0 + r for the lanes of group r).  The sequence of a row is the first one whose
+// start entries are in order and name it: the workgroup reads all of them at once, and each that has rows here puts its
+// number to them, so a batch of any size costs one round trip (a search by halves costs one per halving), and a wrong
+// entry costs its own two sequences their rows and no other.  A thread puts its sequence's number to the first of its
+// rows, its wave to the others, lane k to row k (a loop of the thread over up to 32 rows: 1 us).
 template <int D>
-__device__ __forceinline__ Slot<D> find_slot(const BatchView& b, const KvView& c, int64_t t0, int r, int* cnt) {
+__device__ __forceinline__ Slot<D> find_slot(const BatchView& b, const KvView& c, int64_t t0, int r, int* own) {
   constexpr int NT = KT / (D / 8);
-  for (int i = threadIdx.x; i < NT; i += KT) cnt[i] = 0;
+  const int lane = threadIdx.x & 63;
+  for (int i = threadIdx.x; i < NT; i += KT) own[i] = INT32_MAX;
   __syncthreads();
-  for (int i = threadIdx.x; i < b.batch; i += KT) {
-    const int64_t s0 = b.start[i], e = b.start[i + 1];
-    if (s0 < 0 || e < s0 || e > b.rows) raise_fault(b, kFaultStart);
-    const int64_t at = e <= t0 ? 0 : e - t0;
-    if (at < NT) atomicAdd(&cnt[at], 1);
+  for (int i0 = 0; i0 < b.batch; i0 += KT) {
+    const int i = i0 + threadIdx.x;
+    int from = 0, to = 0;   // its rows here
+    if (i < b.batch) {
+      const int64_t s0 = b.start[i], e = b.start[i + 1];
+      if (s0 < 0 || e < s0 || e > b.rows) raise_fault(b, kFaultStart);
+      else if (s0 < t0 + NT && e > t0) from = (int)(s0 > t0 ? s0 - t0 : 0), to = (int)(e < t0 + NT ? e - t0 : NT);
+    }
+    if (from < to) atomicMin(&own[from], i);
+    for (uint64_t more = __ballot(to - from > 1); more; more &= more - 1) {
+      const int l = __builtin_ctzll(more);
+      const int f = __builtin_amdgcn_readlane(from, l), n = __builtin_amdgcn_readlane(to, l);
+      if (lane > f && lane < n) atomicMin(&own[lane], __builtin_amdgcn_readlane(i, l));
+    }
   }
   __syncthreads();
-  int seq = 0;
-  for (int i = 0; i <= r; ++i) seq += cnt[i];
+  const int seq = own[r];
   Slot<D> s{false, false, false, 0, 0};
-  const int64_t t = t0 + r;
-  if (t >= b.rows || seq >= b.batch) return s;
-  const int64_t s0 = b.start[seq], s1 = b.start[seq + 1];
+  if (seq == INT32_MAX) return s;
+  const int64_t t = t0 + r, s1 = b.start[seq + 1];
   const int len = b.length[seq];
-  if (s0 < 0 || s1 > b.rows || t < s0 || t >= s1) return s;
   if (len < 0 || len > b.max_len) {
     raise_fault(b, kFaultLength);
     s.poison = true;
@@ -82,11 +90,11 @@ template <int D>
 __global__ __launch_bounds__(KT) void k_kv_write(Heads k, Heads v, KvView c, BatchView b, int bl, int zero, ThrLut lut) {
   constexpr int LR = D / 8, NT = KT / LR;   // lanes per row, rows per workgroup
   __shared__ float2 slut[kLutBins];
-  __shared__ int cnt[NT];
+  __shared__ int own[NT];
   if (threadIdx.x < kLutBins) slut[threadIdx.x] = make_float2(lut.t[threadIdx.x], __uint_as_float(lut.base[threadIdx.x]));
   const int r = threadIdx.x / LR, e = threadIdx.x % LR;
   const int64_t t0 = (int64_t)blockIdx.x * NT;
-  const Slot<D> s = find_slot<D>(b, c, t0, r, cnt);
+  const Slot<D> s = find_slot<D>(b, c, t0, r, own);
   if (!s.ok) return;
   const int nb = LR >> bl;   // blocks per row (1 << bl lanes each)
   const uint16_t* const kp = k.data + (t0 + r) * k.rs + e * 8;
@@ -144,11 +152,11 @@ __global__ __launch_bounds__(KT) void k_kv_read(Heads k, Heads v, KvView c, Batc
   constexpr int LR = D / 8, NT = KT / LR;
   // 16 levels in 16 LDS banks: the lanes of a wave read any mix of them without a conflict
   __shared__ float lv[16];
-  __shared__ int cnt[NT];
+  __shared__ int own[NT];
   if (threadIdx.x < 16) lv[threadIdx.x] = tab.level[threadIdx.x];
   const int r = threadIdx.x / LR, e = threadIdx.x % LR;
   const int64_t t0 = (int64_t)blockIdx.x * NT;
-  const Slot<D> s = find_slot<D>(b, c, t0, r, cnt);
+  const Slot<D> s = find_slot<D>(b, c, t0, r, own);
   if (!s.ok && !s.poison && !s.empty) return;
   const int nb = LR >> bl;
   for (int item = blockIdx.y; item < 2 * c.heads; item += gridDim.y) {

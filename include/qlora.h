@@ -333,8 +333,9 @@ qlora_status qlora_kv_sizes(const qlora_kv_cache* cache, size_t* codes_bytes, si
  * Rows that belong to no sequence (before start[0], from start[batch] on) are left alone.  A row with a
  * negative position (length[b] < n) has no token: it is not written, reads zeros, and sees nothing where
  * attention is causal.
- * start is meant to ascend.  Rows that entries out of order give to several sequences are attended by one or more of
- * them, or left alone where these are too many for the launch.
+ * start is meant to ascend.  Where it does not, several sequences can name the same row: it is written and read as the first
+ * one's of those whose own two entries are in order, and attended by one or more of them, or left alone where these are
+ * too many for the launch.
  * The kernels check every entry and read and write nothing out of range; where one is wrong,
  *   - a sequence whose start entries are out of order or past `rows`: its rows are left alone (bit 0);
  *   - a length outside 0 .. max_pages * page_size: nothing is written, rows read and attend NaN (bit 1);

@@ -205,3 +205,46 @@ def test_tokens_behind_the_window_do_not_reach_a_row(dim, page, lens, new, windo
             cache.v_scale[at] *= what
     got = Q.qlora_kv_attn(q, cache, device_batch(h), window=window, lse=True)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+STARTS = [
+    # start, the sequence whose row each of 24 rows is (-1: none; rows that several name are the first one's)
+    ([0, 100, 5, 20, 24], [-1] * 5 + [2] * 15 + [3] * 4),             # one entry past the rows
+    ([0, -3, 5, 20, 24], [-1] * 5 + [2] * 15 + [3] * 4),              # before them
+    ([0, 10, 5, 20, 24], [0] * 10 + [2] * 10 + [3] * 4),              # out of order
+    ([7, 2, 9, 9, 16], [-1] * 2 + [1] * 7 + [3] * 7 + [-1] * 8),      # back before the first
+    ([0, 24, 3, 24, 24], [0] * 24),
+    ([3, 3, 8, 12, 20], [-1] * 3 + [1] * 5 + [2] * 4 + [3] * 8 + [-1] * 4),
+]
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("start,owner", STARTS, ids=str)
+def test_a_wrong_start_leaves_the_other_sequences_alone(start, owner, dim):
+    """Written and read: sequences whose own entries are in order have their rows, whatever stands before them."""
+    require_gpu()
+    rows, page, n = 24, 16, len(start) - 1
+    x = {t: bits(i, (rows, 1, dim)) for i, t in enumerate("kv")}
+    cache = Q.kv_alloc(2 * n, page, 1, dim)
+    for t in (cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale):
+        t.zero_()
+    fault = _word()
+    table = np.arange(2 * n).reshape(n, 2)
+    batch = Q.KVBatch(i32(start), i32([30] * n), i32(table), fault)
+    Q.qlora_kv_write(dev_bf16(x["k"]), dev_bf16(x["v"]), cache, batch)
+    order = all(0 <= a <= b <= rows for a, b in zip(start, start[1:]))
+    assert fault.item() == (0 if order else FAULT_START)
+    out = [torch.full((rows, 1, dim), 7.0, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    Q.qlora_kv_read(cache, batch, rows, *out)
+    slots = set()
+    for i, b in enumerate(owner):
+        if b < 0:
+            assert torch.all(out[0][i] == 7.0) and torch.all(out[1][i] == 7.0), i
+            continue
+        p = 30 - (start[b + 1] - i)
+        slots.add((int(table[b, p // page]), p % page))
+        for t, o in zip("kv", out):
+            want = kv.row_bf16(*kv.quantize_row(x[t][i, 0], 64, "nf4"), "nf4")
+            assert np.array_equal(host(o[i, 0].view(torch.int16)).view(np.uint16), want), (i, t)
+    held = torch.nonzero(cache.k_scale[:, 0, :, 0])
+    assert {tuple(s) for s in held.tolist()} == slots
