@@ -114,8 +114,7 @@ struct AttnPlan {
   int64_t many_split;             // how many of these it may cut into parts: 0 (no join), or up to kSplitWgs / 2
   int split_tokens;               // tokens of a part at least; 0: none is cut
   bool sparse;                    // a quarter of its tiles' rows or more are empty
-  size_t part_floats, meta_ints;  // workspace, and where the second kernel's share of it begins
-  size_t many_part, many_meta;
+  size_t part_floats, meta_ints;  // workspace: the most that a call with at most these rows, sequences and tokens uses
 };
 AttnPlan attn_plan(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t batch, int64_t max_len, int D);
 hipError_t launch_kv_attn(const AttnArgs& a, const AttnPlan& pl, int D, int block, hipStream_t s);

@@ -34,6 +34,8 @@
 // workgroup: 1200 to find it, 2400 for table, queries and codes, 6000 for the step, 1000 for the waves' sums; two workgroups
 // to a CU overlap half of that: 1000 sequences of one token 86 us, 512 of 128 tokens 53 (17 at copy rate), 16 of
 // 4096 21 (15), one of 777 tokens 6.
+#include <algorithm>
+
 #include "kv_attn.h"
 
 namespace qlora {
@@ -694,6 +696,26 @@ constexpr int few_rows(int D) { return D == 64 ? 128 : 64; }
 // with 32 rows each, where the second finds nothing to do, 100 and 104.
 constexpr int64_t kAlone = 1024;
 
+// A workspace made for the largest call serves smaller ones, which may be cut into parts where the large one is not: every
+// size at its most for up to these rows, sequences and tokens, so that it grows with each of them.
+static void size_workspace(AttnPlan& p, int64_t rows_h, int64_t nseq, int64_t kv_heads, int64_t max_len, int D) {
+  const int64_t units = (max_len >> kUnitShift) + 1;
+  // ranges of the kernel for few rows, with tiles of 16 rows and, where a call may have those, of 32
+  const int wide = D < 256 && rows_h > 16 && nseq * kv_heads * units >= 2 * kCUs * waves_of(D, 2) ? 2 : 1;
+  for (int nr = 1; nr <= wide; ++nr) {
+    const int tile = 16 * nr;
+    const int64_t tiles = ((rows_h + tile - 1) / tile + nseq) * kv_heads;
+    const size_t wgs = (size_t)std::min(tiles * units, kCUs * waves_of(D, nr));
+    p.part_floats = std::max(p.part_floats, wgs * 2 * tile * (D + 2));
+    p.meta_ints = std::max(p.meta_ints, wgs * kMetaInts);
+  }
+  // parts of the one for many rows, which runs before the other and leaves it the same memory
+  if (rows_h > few_rows(D) && max_len >= 2 * split_tokens_of(D, true)) {
+    p.part_floats = std::max(p.part_floats, (size_t)kSplitWgs * (many_threads(D) / 2) * (D + 2));
+    p.meta_ints = std::max(p.meta_ints, (size_t)(1 + kSplitWgs / 2) * kMetaInts);
+  }
+}
+
 AttnPlan attn_plan(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t batch, int64_t max_len, int D) {
   AttnPlan p{};
   const int64_t group = q_heads / kv_heads, rows_h = rows * group, nseq = batch > 1 ? batch : 1;
@@ -730,12 +752,11 @@ AttnPlan attn_plan(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t batc
       p.many_split = p.many_wgs < kSplitWgs / 2 ? p.many_wgs : kSplitWgs / 2;
       if (p.many_wgs < kSplitWgs) p.many_wgs = kSplitWgs;
       p.split_tokens = tokens;
-      p.many_part = p.part_floats;
-      p.many_meta = p.meta_ints;
-      p.part_floats += (size_t)kSplitWgs * tr * (D + 2);
-      p.meta_ints += (size_t)(1 + p.many_split) * kMetaInts;
+      p.part_floats = std::max(p.part_floats, (size_t)kSplitWgs * tr * (D + 2));
+      p.meta_ints = std::max(p.meta_ints, (size_t)(1 + p.many_split) * kMetaInts);
     }
   }
+  size_workspace(p, rows_h, nseq, kv_heads, max_len, D);
   return p;
 }
 
@@ -774,8 +795,6 @@ hipError_t launch_kv_attn(const AttnArgs& a, const AttnPlan& pl, int D, int bloc
   if (pl.few != INT32_MAX) {
     AttnArgs m = a;
     m.few = pl.few;
-    m.part = a.part + pl.many_part;
-    m.meta = a.meta + pl.many_meta;
     const hipError_t e = launch_kv_attn_many(m, pl, D, block, s);
     if (e != hipSuccess || pl.few == 0) return e;
   }

@@ -380,8 +380,9 @@ qlora_status qlora_kv_read(const qlora_kv_cache* cache, const qlora_kv_batch* ba
  * Requires: q_heads a multiple of cache.heads, at most 1024; scale finite and > 0; window >= 0, 0 if not
  * causal; o like q, not overlapping it; (rows * q_heads / cache.heads) < 2^30; ws of
  * qlora_kv_attn_workspace bytes, 16-byte aligned (the query reads the sizes of `cache` and `batch` only,
- * not their arrays, and gives 0 for sizes that the call refuses).  Calls that may run at the same time
- * need a workspace each.                                                                               */
+ * not their arrays, and gives 0 for sizes that the call refuses).  It grows with the rows, the batch and max_pages,
+ * so a workspace for the largest call serves all smaller ones of the same heads; it stays below 36 MB.  Calls that
+ * may run at the same time need a workspace each.                                                      */
 size_t qlora_kv_attn_workspace(const qlora_kv_cache* cache, const qlora_kv_batch* batch, int64_t rows,
                                int32_t q_heads);
 qlora_status qlora_kv_attn(const qlora_heads* q, int64_t rows, const qlora_kv_cache* cache,

@@ -335,3 +335,24 @@ def test_kv_attn_validation(lib):
         assert f(scale=scale) == 4
     assert f(causal=2) == 4 and f(causal=0, window=5) == 4 and f(c=_cache(dim=192)) == 4
     assert f(n=need - 1) == 5 and f(ws=None) == 5
+
+
+def test_kv_attn_workspace_grows_with_the_call(lib):
+    """A workspace made for the largest call serves every smaller one: the size falls neither with rows nor with
+    sequences nor with pages, across all choices of kernels, tiles and parts."""
+    size = lambda c, batch, max_pages, rows, q: lib.qlora_kv_attn_workspace(
+        C.byref(c), C.byref(_batch(batch=batch, max_pages=max_pages)), rows, q)
+    rows = sorted({n + d for n in [1 << k for k in range(15)] + [24, 48, 96, 200, 1500, 3000] for d in (-1, 0, 1)} - {0})
+    for dim in (64, 128, 256):
+        for heads, q in ((1, 1), (8, 32), (32, 32), (2, 40)):
+            c = _cache(page=64, heads=heads, dim=dim)
+            by_batch = {}
+            for batch in (0, 1, 2, 3, 8, 16, 21, 64, 300):
+                by_pages = {}
+                for max_pages in (1, 3, 4, 7, 8, 16, 31, 32, 64, 256, 512):
+                    got = [size(c, batch, max_pages, n, q) for n in rows]
+                    assert 0 < got[0] and got == sorted(got), (dim, heads, q, batch, max_pages)
+                    assert got[-1] < 36 << 20
+                    for before in (by_batch.get(max_pages), by_pages.get("last")):
+                        assert before is None or all(a <= b for a, b in zip(before, got)), (dim, heads, q, batch, max_pages)
+                    by_batch[max_pages] = by_pages["last"] = got

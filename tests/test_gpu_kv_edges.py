@@ -248,3 +248,23 @@ def test_a_wrong_start_leaves_the_other_sequences_alone(start, owner, dim):
             assert np.array_equal(host(o[i, 0].view(torch.int16)).view(np.uint16), want), (i, t)
     held = torch.nonzero(cache.k_scale[:, 0, :, 0])
     assert {tuple(s) for s in held.tolist()} == slots
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_one_workspace_for_the_largest_call_and_smaller_ones(dim):
+    """A workspace made for a prompt that is not cut into parts serves drafts, single tokens and short prompts, which are."""
+    require_gpu()
+    h = layout([2500, 300], [1, 1], 16, dim)
+    k, v = ([bits(s + b, (n, 1, dim)) for b, n in enumerate(h.lens)] for s in (3, 30))
+    cache, _, _ = written(h, k, v, 1, dim, 64)
+    table = i32(h.table)
+    need = Q.qlora_kv_attn_workspace(cache, Q.KVBatch(i32([0, 0, 0]), i32(h.lens), table), 40000, 4)
+    guarded = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    for new in ([1, 1], [9, 3], [40, 0], [150, 100], [2500, 1]):
+        rows = sum(new)
+        batch = Q.KVBatch(i32(np.concatenate([[0], np.cumsum(new)])), i32(h.lens), table)
+        q = dev_bf16(bits(9, (rows, 4, dim)))
+        want = Q.qlora_kv_attn(q, cache, batch, lse=True)
+        got = Q.qlora_kv_attn(q, cache, batch, lse=True, workspace=guarded[:need])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert torch.all(guarded[need:] == 0xA5)
