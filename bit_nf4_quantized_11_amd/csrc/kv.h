@@ -79,8 +79,9 @@ struct QkArgs {
   float* part;                    // backward: weight gradient partials [workgroup][2][D]
 };
 hipError_t launch_qk(const QkArgs& a, int D, bool interleaved, hipStream_t s);
-// workgroups of the backward launch = partial sums of each weight gradient
-int qk_bwd_grid(int64_t rows, int32_t q_heads, int32_t k_heads, int D);
+// partial sums of each weight gradient (workgroups of the backward) in a call with at most these rows: grows with them, as
+// the workgroups do not (fewer rows can be cut into more slices)
+int qk_bwd_partials(int64_t rows, int32_t q_heads, int32_t k_heads, int D);
 hipError_t launch_qk_bwd(const QkArgs& a, int D, bool interleaved, float* dwq, float* dwk, hipStream_t s);
 
 // ---- cache write and read (kv_cache.hip) ------------------------------------------------------

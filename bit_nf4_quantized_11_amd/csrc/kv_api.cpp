@@ -206,7 +206,7 @@ size_t qlora_qk_norm_rope_bwd_workspace(int64_t rows, int32_t q_heads, int32_t k
   if (rows < 0 || rows >= kMaxRows || q_heads < 1 || q_heads > kMaxHeads || k_heads < 0 || k_heads > kMaxHeads ||
       !head_dim_ok(head_dim))
     return 0;
-  return round_up((size_t)qk_bwd_grid(std::max<int64_t>(rows, 1), q_heads, k_heads, head_dim) * 2 * head_dim * sizeof(float),
+  return round_up((size_t)qk_bwd_partials(std::max<int64_t>(rows, 1), q_heads, k_heads, head_dim) * 2 * head_dim * sizeof(float),
                   256);
 }
 

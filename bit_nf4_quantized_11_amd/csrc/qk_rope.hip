@@ -288,16 +288,19 @@ hipError_t launch_qk(const QkArgs& a0, int D, bool inter, hipStream_t s) {
   return hipGetLastError();
 }
 
-int qk_bwd_grid(int64_t rows, int32_t q_heads, int32_t k_heads, int D) {
-  const int64_t items = rows * slices_for(rows, head_groups(q_heads, k_heads, D));
+static int bwd_grid(int64_t items) {
   const int64_t g = (items + QW - 1) / QW;
   return (int)(g < 1024 ? g : 1024);
+}
+
+int qk_bwd_partials(int64_t rows, int32_t q_heads, int32_t k_heads, int D) {
+  return bwd_grid(rows * head_groups(q_heads, k_heads, D));   // a row has as many slices as groups at most
 }
 
 hipError_t launch_qk_bwd(const QkArgs& a0, int D, bool inter, float* dwq, float* dwk, hipStream_t s) {
   QkArgs a = a0;
   a.slices = slices_for(a.rows, head_groups(a.q.n, a.k.n, D));
-  const int grid = qk_bwd_grid(a.rows, a.q.n, a.k.n, D);
+  const int grid = bwd_grid(a.rows * a.slices);
   {
     const dim3 g((unsigned)grid);
     ProfScope ps("k_qk_norm_rope_bwd", s);

@@ -285,7 +285,8 @@ qlora_status qlora_qk_norm_rope(const qlora_heads* q, const qlora_heads* k, int6
  * Where a weight is NULL, its input (q or k) may be NULL and its weight gradient must be NULL.
  * dq may be dq_out and dk may be dk_out (same data and strides); no other overlap.  With rows = 0 the
  * weight gradients are set to zero.  ws of qlora_qk_norm_rope_bwd_workspace bytes (needed only with
- * a weight).  dk_out NULL: no keys (k, dk, k_weight, dk_weight NULL too).                          */
+ * a weight; the size grows with rows and heads, so that of the largest call serves smaller ones).
+ * dk_out NULL: no keys (k, dk, k_weight, dk_weight NULL too).                                       */
 size_t qlora_qk_norm_rope_bwd_workspace(int64_t rows, int32_t q_heads, int32_t k_heads, int32_t head_dim);
 qlora_status qlora_qk_norm_rope_bwd(const qlora_heads* dq_out, const qlora_heads* dk_out, const qlora_heads* q,
                                     const qlora_heads* k, int64_t rows, int32_t head_dim, const uint16_t* q_weight,

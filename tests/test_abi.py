@@ -356,3 +356,14 @@ def test_kv_attn_workspace_grows_with_the_call(lib):
                     for before in (by_batch.get(max_pages), by_pages.get("last")):
                         assert before is None or all(a <= b for a, b in zip(before, got)), (dim, heads, q, batch, max_pages)
                     by_batch[max_pages] = by_pages["last"] = got
+
+
+def test_qk_norm_rope_bwd_workspace_grows_with_the_call(lib):
+    rows = sorted({n + d for n in [1 << k for k in range(14)] + [60, 700, 1500, 3000] for d in (-1, 0, 1)} - {-1})
+    for dim in (64, 128, 256):
+        before = None
+        for q, k in ((1, 0), (1, 1), (3, 1), (8, 8), (24, 8), (32, 32), (64, 64), (1024, 1024)):
+            got = [lib.qlora_qk_norm_rope_bwd_workspace(n, q, k, dim) for n in rows]
+            assert got == sorted(got) and (before is None or all(a <= b for a, b in zip(before, got))), (dim, q, k)
+            before = got
+        assert got[-1] == 1024 * 2 * dim * 4

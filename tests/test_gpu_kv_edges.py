@@ -268,3 +268,18 @@ def test_one_workspace_for_the_largest_call_and_smaller_ones(dim):
         got = Q.qlora_kv_attn(q, cache, batch, lse=True, workspace=guarded[:need])
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert torch.all(guarded[need:] == 0xA5)
+
+
+def test_one_workspace_for_the_largest_backward_and_smaller_ones():
+    require_gpu()
+    hq, hk, dim = 32, 32, 128
+    need = Q.qlora_qk_norm_rope_bwd_workspace(2048, hq, hk, dim)
+    guarded = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    w = [dev_bf16(bits(i, (dim,))) for i in (1, 2)]
+    t = [dev_bf16(bits(3 + i, (2048, h, dim))) for i, h in enumerate((hq, hk, hq, hk))]
+    for rows in (2048, 2047, 700, 1):
+        args = [x[:rows] for x in t]
+        want = Q.qlora_qk_norm_rope_bwd(*args, None, None, *w)
+        got = Q.qlora_qk_norm_rope_bwd(*args, None, None, *w, workspace=guarded[:need])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.all(guarded[need:] == 0xA5)
