@@ -336,7 +336,8 @@ def _bytes(ws, device, need):
 
 @dataclass(frozen=True)
 class KVCache:
-    """A key/value cache in 4 bits: caller-owned device buffers, laid out as include/qlora.h says."""
+    """A key/value cache in 4 bits: caller-owned device buffers, laid out as include/qlora.h says.  Their addresses are
+    taken when it is made: a tensor is not to be given other storage (resize_, set_, .data) while it lives."""
     k_codes: torch.Tensor    # uint8 [pages][heads][page_size][head_dim / 2]
     k_scale: torch.Tensor    # bf16 [pages][heads][page_size][head_dim / block]
     v_codes: torch.Tensor
@@ -363,6 +364,9 @@ class KVCache:
         object.__setattr__(self, "arg", C.byref(_lib.qlora_kv_cache(
             pages, page_size, heads, 2 * half, int(self.block), int(self.codebook), 0, self.k_codes.data_ptr(),
             self.k_scale.data_ptr(), self.v_codes.data_ptr(), self.v_scale.data_ptr())))
+
+    def __reduce__(self):   # copies and pickles: made anew from the fields, the descriptor points at their own buffers
+        return KVCache, (self.k_codes, self.k_scale, self.v_codes, self.v_scale, self.block, self.codebook)
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in (self.k_codes, self.k_scale, self.v_codes, self.v_scale))
@@ -391,7 +395,7 @@ def kv_alloc(pages: int, page_size: int, heads: int, head_dim: int, block: int =
 class KVBatch:
     """The tokens a call is about: rows start[b] .. start[b + 1] - 1 are the last ones of sequence b, whose
     length[b] tokens lie in the pages table[b].  Device tensors that the kernels read, so their contents may
-    change between calls (and between replays of a captured call)."""
+    change between calls (and between replays of a captured call), but not their storage, as that of a cache."""
     start: torch.Tensor               # int32 [batch + 1]
     length: torch.Tensor              # int32 [batch]
     table: torch.Tensor               # int32 [batch][max_pages]
@@ -410,6 +414,9 @@ class KVBatch:
         object.__setattr__(self, "arg", C.byref(_lib.qlora_kv_batch(
             n, self.table.shape[1], self.start.data_ptr(), self.length.data_ptr(), self.table.data_ptr(),
             None if self.fault is None else self.fault.data_ptr())))
+
+    def __reduce__(self):   # (as of a cache)
+        return KVBatch, (self.start, self.length, self.table, self.fault)
 
 
 def _same_device(cache: KVCache, batch: KVBatch):

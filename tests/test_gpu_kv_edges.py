@@ -1,5 +1,8 @@
 """The 4-bit cache and its attention where ordinary data does not lead: rows of zeros and of infinities, scales at both
 ends, entries behind a window, starts out of order, workspaces of other calls."""
+import copy
+import pickle
+
 import numpy as np
 import pytest
 import torch
@@ -283,3 +286,26 @@ def test_one_workspace_for_the_largest_backward_and_smaller_ones():
         got = Q.qlora_qk_norm_rope_bwd(*args, None, None, *w, workspace=guarded[:need])
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert torch.all(guarded[need:] == 0xA5)
+
+
+def test_copies_and_pickles_of_a_cache_and_a_batch():
+    """Copies have buffers of their own and describe those."""
+    require_gpu()
+    h = layout([40, 9], [3, 1], 16, 1)
+    k, v = ([bits(s + b, (n, 1, 64)) for b, n in enumerate(h.lens)] for s in (3, 30))
+    cache, _, _ = written(h, k, v, 1, 64, 32)
+    batch = device_batch(h, _word())
+    q = dev_bf16(bits(9, (h.rows, 2, 64)))
+    want = Q.qlora_kv_attn(q, cache, batch)[0]
+    copies = [(copy.deepcopy(cache), copy.deepcopy(batch)), pickle.loads(pickle.dumps((cache, batch)))]
+    shared = copy.copy(cache), copy.copy(batch)
+    assert shared[0].k_codes is cache.k_codes and shared[1].table is batch.table
+    for c, b in copies + [shared]:
+        assert (c.block, c.codebook, c.pages, c.heads, c.page_size, c.head_dim) == (32, 0, h.pages, 1, 16, 64)
+        assert torch.equal(Q.qlora_kv_attn(q, c, b)[0], want)
+    for c, b in copies:
+        assert c.k_codes.data_ptr() != cache.k_codes.data_ptr() and b.table.data_ptr() != batch.table.data_ptr()
+    for t in (cache.k_codes, cache.k_scale, cache.v_codes, cache.v_scale, batch.table):
+        t.zero_()
+    for c, b in copies:                      # (the first ones' buffers are not looked at)
+        assert torch.equal(Q.qlora_kv_attn(q, c, b)[0], want)
