@@ -689,7 +689,9 @@ CodePlanes code_planes(int cb) {
 // kAlone rows, each of the others having one; otherwise it launches both.
 // This kernel and the other one, 16 sequences of 4096 tokens, 32 cache heads: D = 64, 64 rows 101 and 221 us, 128 rows 181 and 219,
 // 160 rows 225 and 239; D = 128, 64 rows 176 and 242, 96 rows 248 and 243, 128 rows 329 and 256; D = 256, 64 rows 516 and
-// 555, 96 rows 754 and 561.  One sequence of 32768, 8 heads of 64: 64 rows 51 and 40 us, 128 rows 51 and 44.
+// 555, 96 rows 754 and 561.  With one sequence it depends on how long it is, which the host does not know: 8 heads of 64,
+// 2048 tokens, 64 rows 12.5 and 17.6 us, 128 rows 16.4 and 19.5; 32768 tokens, 49 and 41, 50 and 43; heads of 128 with 64 rows,
+// 15.9 and 20.2, 51 and 44; of 256, 22 and 33, 73 and 86.  So it goes by the same numbers of rows.
 constexpr int few_rows(int D) { return D == 64 ? 128 : 64; }
 // 32 sequences of 4096, 8 cache heads of 128, one with 520 rows, the others with 4: 76 us by the first kernel, 91 by both; 64 of
 // 2000 and one of 8192 with 2048 rows 212 and 155; 300 of 1000 and one of 4096 with 16384 rows 809 and 343; 64 of 4096

@@ -266,8 +266,9 @@ typedef struct {
  *   u = x * w / sqrt(mean(x^2) + eps)          (u = x where the weight is NULL)
  *   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = positions[row] * inv_freq[i],
  * for the pairs i < rot_dim / 2: (u[i], u[i + rot_dim / 2]), or (u[2i], u[2i + 1]) with `interleaved`;
- * elements from rot_dim on are not rotated.  fp32 arithmetic, angles reduced in float64, one rounding
- * to bf16 at the end.  k may be NULL (then k_out too).
+ * elements from rot_dim on are not rotated.  fp32 arithmetic (so the mean of a head with elements from 2^60 on can
+ * be infinite, which gives zeros), angles reduced in float64, one rounding to bf16 at the end.  k may be
+ * NULL (then k_out too).
  * Outputs may be the inputs themselves (same data and strides); they must not overlap otherwise.
  * Requires: head_dim 64, 128 or 256; rot_dim % 16 == 0, 0 <= rot_dim <= head_dim; q_weight, k_weight
  * bf16 [head_dim], 16-byte aligned; positions [rows], inv_freq [rot_dim / 2] (both may be NULL when
@@ -368,15 +369,20 @@ qlora_status qlora_kv_read(const qlora_kv_cache* cache, const qlora_kv_batch* ba
  *   o[row][h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q . k_j),
  * over the positions j that row sees: j <= its own position (causal) or all below length[b], and with
  * window > 0 (causal only) j > position - window.  Query head h reads cache head h / (q_heads / heads).
- * A row that sees nothing gives zeros and lse = -infinity.  What a row does not see does not reach it,
- * NaN included.  lse (or NULL): fp32 [rows][q_heads], the natural logarithm of sum_j p_j.
+ * A row that sees nothing gives zeros and lse = -infinity.  An infinity or a NaN that a row does not see
+ * does not reach it; one in its own q makes it NaN if it sees a token.  lse (or NULL): fp32 [rows][q_heads], the
+ * natural logarithm of sum_j p_j.
  * fp16 products with fp32 accumulation; maximum, sum and output held in fp32.  Rounded to fp16 for the
  * matrix instructions, each brought to about 1 by a power of two first: a row of q (by its largest
  * element), the levels (FP4's and Int4's exactly), the probabilities, and the scales, or levels times
  * scales.  What fp16's range then loses: an element of k or v below 2^-14 of the largest scale of its
  * 64 tokens (or, for v, of those so far) is off by up to 2^-25 of that scale; and a probability below
  * 2^-21 of the largest one is off by up to 2^-31 of it (times the largest value scale, in the output).
- * Value scales below 2^-100 are held in units of 2^-100.
+ * A finite scale counts there for all rows of a tile (up to 256 consecutive ones of a sequence) as soon as one of
+ * them sees its token: a later token of the same call whose scale is 2^14 and more times larger costs the rows
+ * before it bits, and at 2^40 times their sums.
+ * Key and value scales, and rows of q by their largest element, are held in units of 2^-100 where they are smaller.
+ * Logits are fp32 numbers: key scales from 2^115 on, and scale |q| |k| of the largest elements from 2^110 on, can give NaN.
  * The same call gives the same bits (no sum depends on the order in which workgroups run).
  * Requires: q_heads a multiple of cache.heads, at most 1024; scale finite and > 0; window >= 0, 0 if not
  * causal; o like q, not overlapping it; (rows * q_heads / cache.heads) < 2^30; ws of
