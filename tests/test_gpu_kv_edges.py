@@ -309,3 +309,54 @@ def test_copies_and_pickles_of_a_cache_and_a_batch():
         t.zero_()
     for c, b in copies:                      # (the first ones' buffers are not looked at)
         assert torch.equal(Q.qlora_kv_attn(q, c, b)[0], want)
+
+
+def test_the_largest_batch():
+    """65536 sequences of one token, attended and read back: the bits of calls with a thousand of them."""
+    require_gpu()
+    n, page, pages, dim = 65536, 64, 8, 64
+    rng = np.random.default_rng(0)
+    cache = Q.kv_alloc(pages, page, 1, dim)
+    k, v = (dev_bf16(bits(s, (pages * page, 1, dim))) for s in (1, 2))
+    Q.qlora_kv_write(k, v, cache, Q.KVBatch(i32([0, pages * page]), i32([pages * page]), i32([list(range(pages))])))
+    lens, table = i32(rng.integers(1, page + 1, n)), i32(rng.integers(0, pages, (n, 1)))
+    start = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    q = dev_bf16(bits(3, (n, 2, dim)))
+    fault = _word()
+    batch = Q.KVBatch(start, lens, table, fault)
+    o, lse = Q.qlora_kv_attn(q, cache, batch, lse=True)
+    back = Q.qlora_kv_read(cache, batch, n)
+    for i in range(0, n, 1024):
+        part = Q.KVBatch(start[:1025], lens[i:i + 1024], table[i:i + 1024])
+        po, pl = Q.qlora_kv_attn(q[i:i + 1024], cache, part, lse=True)
+        assert torch.equal(o[i:i + 1024], po) and torch.equal(lse[i:i + 1024], pl), i
+        for a, b in zip(back, Q.qlora_kv_read(cache, part, 1024)):
+            assert torch.equal(a[i:i + 1024], b), i
+    assert fault.item() == 0
+
+
+@pytest.mark.parametrize("dim,new", [(64, [2, 3]), (128, [150, 1]), (256, [70, 80])], ids=str)
+def test_rows_before_the_first_sequence_and_queries_of_one_row(dim, new):
+    """Starts that begin behind row 0, rows behind the last one, and q broadcast over rows (a stride of 0)."""
+    require_gpu()
+    h = layout([200, 90], new, 16, dim)
+    k, v = ([bits(s + b, (n, 1, dim)) for b, n in enumerate(h.lens)] for s in (3, 30))
+    cache, _, _ = written(h, k, v, 1, dim, 64)
+    rows = h.rows + 9
+    one = dev_bf16(bits(9, (1, 4, dim)))
+    ahead = Q.KVBatch(i32(h.start + 5), i32(h.lens), i32(h.table))
+    o, lse = torch.full((rows, 4, dim), 6.0, dtype=torch.bfloat16, device="cuda"), torch.full((rows, 4), 6.0, device="cuda")
+    Q.qlora_kv_attn(one.expand(rows, 4, dim), cache, ahead, out=o, lse=lse)
+    want, wl = Q.qlora_kv_attn(one.expand(h.rows, 4, dim).contiguous(), cache, device_batch(h), lse=True)
+    assert torch.equal(o[5:-4], want) and torch.equal(lse[5:-4], wl)
+    for t in (o, lse):
+        assert torch.all(t[:5] == 6.0) and torch.all(t[-4:] == 6.0)
+
+
+@pytest.mark.parametrize("dim,batch", [(64, 1), (128, 3), (256, 2)])
+def test_a_thousand_query_heads_of_one_cached_head(dim, batch):
+    require_gpu()
+    lens = [130, 1, 67][:batch]
+    h = layout(lens, [1] * batch, 16, dim)
+    k, v = ([bits(s + b, (n, 1, dim)) for b, n in enumerate(lens)] for s in (3, 30))
+    against_oracle(h, bits(9, (batch, 1024, dim)), *written(h, k, v, 1, dim, 64))
