@@ -28,12 +28,12 @@
 // 2^-17 of it stay), the scaled probabilities of a step by the largest scale so far of that
 // block of elements (a running exponent, like the running maximum, that all rows share).
 //
-// Measured: 16 sequences of up to 32768 tokens (311 k in all, 338 MB), 64 query on 8 cache heads of 128: 84 us of this
-// kernel = 4.0 TB/s and 2 of the join, where a large copy reaches 4.8: the steps are bound by HBM (a step's 18.9 MB in
-// 4 us when all 2048 waves are in theirs), VALU issue close behind.  A tile of a single step takes about 10500 cycles of one
-// workgroup: 1200 to find it, 2400 for table, queries and codes, 6000 for the step, 1000 for the waves' sums; two workgroups
-// to a CU overlap half of that: 1000 sequences of one token 86 us, 512 of 128 tokens 53 (17 at copy rate), 16 of
-// 4096 21 (15), one of 777 tokens 6.
+// Measured: 16 sequences of up to 32768 tokens (311 k in all, 338 MB), 64 query on 8 cache heads of 128: 84 us a pass =
+// 4.0 TB/s, where a large copy reaches 4.8 (in a trace 81 to 94 of this kernel and 5 of the join, where an empty kernel has
+// 2.5 to 4): the steps are bound by HBM (a step's 18.9 MB in 4 us when all 2048 waves are in theirs), VALU issue close behind.
+// A tile of a single step takes about 10500 cycles of one workgroup: 1200 to find it, 2400 for table, queries and codes, 6000
+// for the step, 1000 for the waves' sums; two workgroups to a CU overlap half of that: 1000 sequences of one token 84 us, 512
+// of 128 tokens 51 (17 at copy rate), 16 of 4096 23 (15), one of 777 tokens 9.
 #include <algorithm>
 
 #include "kv_attn.h"

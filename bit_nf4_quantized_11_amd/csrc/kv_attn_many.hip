@@ -13,9 +13,10 @@
 // wave 3700 with the exponentials' 16 each, LDS 2250: of 5800 in all.  Bound by the issue of VALU instructions, which
 // the matrix products of the other wave overlap in part.
 // Measured: 16384 rows of one sequence, 32 query on 8 cache heads of 128, causal, 2.49 to 2.6 ms = 850 to 884 TFLOP/s
-// (a square library product of 8192 reaches 1190); 4 x 4096 rows 0.78 ms, 705; heads of 64 0.51 ms, 543 (twice the
-// exponentials and decoding per product); heads of 256 447 (4 waves to a CU with 512 registers each: nothing overlaps a wave's
-// waits).  A workgroup's start, its first tile and its end cost 12 to 15 us, which is what short sequences pay: 1024 rows 46 us.
+// (a square library product of 8192 reaches 1190); 4 x 4096 rows 0.70 to 0.78 ms, 705 to 780.  Heads of 64: 1.75 ms, 627, and
+// 0.51 ms, 545 (twice the exponentials and decoding per product).  Heads of 256: 8.5 ms, 516, and 2.36 ms, 466 (4 waves to a CU
+// with 512 registers each: nothing overlaps a wave's waits).  A workgroup's start, its first tile and its end cost 12 to 15 us,
+// which is what short sequences pay: 1024 rows 46 us.
 //
 // One workgroup per tile of a sequence.  Each finds all tiles of the call from the device's lengths; where there are no more
 // than half as many as CUs, the tokens of every tile are cut into parts for all of them, whose sums k_kv_attn_many_join adds (2
