@@ -22,7 +22,9 @@ __all__ = [
     "qlora_linear_bwd", "qlora_merge_adapter", "qlora_adamw_step", "qlora_profile_enable", "qlora_profile_read", "lib",
     "KVCache", "KVBatch", "kv_alloc", "qlora_qk_norm_rope", "qlora_qk_norm_rope_bwd_workspace",
     "qlora_qk_norm_rope_bwd", "qlora_kv_sizes", "qlora_kv_write", "qlora_kv_read", "qlora_kv_attn_workspace",
-    "qlora_kv_attn",
+    "qlora_kv_attn", "qlora_rms_norm", "qlora_rms_norm_bwd_workspace", "qlora_rms_norm_bwd", "ACTIVATIONS",
+    "qlora_gated_workspace", "qlora_gated_fwd", "qlora_gated_bwd", "qlora_token_logprob_workspace", "qlora_token_logprob",
+    "qlora_token_logprob_bwd",
 ]
 
 
@@ -588,6 +590,242 @@ def qlora_kv_attn(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float 
         return o, sums
 
     return _launch(q, stream, run)
+
+
+# ---- around the projections: the residual's norm, the gated block, log probabilities ---------------------------
+def _rows(t: torch.Tensor, name: str, device=None, shape=None):
+    """(address, row stride) of a bf16 [rows][dim] tensor, any row stride with dense rows."""
+    strides = t.stride()
+    if t.dtype is not torch.bfloat16 or len(strides) != 2 or strides[1] != 1 or not t.is_cuda:
+        raise QLoRAError(f"{name} must be a bf16 [rows][dim] tensor on the GPU, dense along dim")
+    if device is not None and t.device != device:
+        raise QLoRAError(f"{name} must be on {device}")
+    if shape is not None and t.shape != shape:
+        raise QLoRAError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr(), strides[0]
+
+
+def _new_rows(given, name: str, device, shape):
+    """An output and its (address, row stride): the caller's, checked, or a new contiguous one."""
+    if given is not None:
+        return given, _rows(given, name, device, shape)
+    t = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    return t, (t.data_ptr(), shape[1])
+
+
+def qlora_rms_norm(x: torch.Tensor, weight: torch.Tensor | None, residual: torch.Tensor | None = None,
+                   eps: float = 1e-6, out: torch.Tensor | None = None, sum_out: torch.Tensor | None = None, stream=None):
+    """Residual addition and root-mean-square norm of x [rows][dim] (bf16, any row stride): h = bf16(x + residual),
+    out = bf16(h weight / sqrt(mean(h^2) + eps)).  out and sum_out may be x or residual.  Returns (out, h), h being x
+    without a residual."""
+    dev = x.device
+    px, sx = _rows(x, "x")
+    shape = x.shape
+    pr, sr = (None, 0) if residual is None else _rows(residual, "residual", dev, shape)
+    if weight is not None:
+        _need(weight, torch.bfloat16, dev, "weight", (shape[1],))
+    if residual is None and sum_out is not None:
+        raise QLoRAError("sum_out needs a residual")
+
+    def run(stream):
+        y, (py, sy) = _new_rows(out, "out", dev, shape)
+        h, (ph, sh) = (x, (None, 0)) if residual is None else _new_rows(sum_out, "sum_out", dev, shape)
+        _check(lib().qlora_rms_norm(px, sx, pr, sr, shape[0], shape[1], _at(weight), eps, py, sy, ph, sh, stream),
+               "qlora_rms_norm")
+        return y, h
+
+    return _launch(x, stream, run)
+
+
+def qlora_rms_norm_bwd_workspace(rows: int, dim: int) -> int:
+    return lib().qlora_rms_norm_bwd_workspace(rows, dim)
+
+
+def qlora_rms_norm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None, dh: torch.Tensor | None = None,
+                       eps: float = 1e-6, weight_grad: bool = True, dx: torch.Tensor | None = None,
+                       dweight: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of qlora_rms_norm from that of its output, its h and (where h goes on beside the norm) the gradient dh
+    of h.  dx, the gradient of x and of the residual, may be dy, h or dh.  Returns (dx, dweight fp32 [dim] or None:
+    without a weight, or with weight_grad=False)."""
+    dev = dy.device
+    pg, sg = _rows(dy, "dy")
+    shape = dy.shape
+    ph, sh = _rows(h, "h", dev, shape)
+    pd, sd = (None, 0) if dh is None else _rows(dh, "dh", dev, shape)
+    if weight is not None:
+        _need(weight, torch.bfloat16, dev, "weight", (shape[1],))
+    if weight is None or not weight_grad:
+        if dweight is not None:
+            raise QLoRAError("dweight needs the weight, and weight_grad")
+        weight_grad = False
+    elif dweight is not None:
+        _need(dweight, torch.float32, dev, "dweight", (shape[1],))
+
+    def run(stream):
+        out, (px, sx) = _new_rows(dx, "dx", dev, shape)
+        gw, ws = None, None
+        if weight_grad:
+            gw = torch.empty(shape[1], dtype=torch.float32, device=dev) if dweight is None else dweight
+            ws = _bytes(workspace, dev, lambda: qlora_rms_norm_bwd_workspace(shape[0], shape[1]))
+        _check(lib().qlora_rms_norm_bwd(pg, sg, ph, sh, pd, sd, shape[0], shape[1], _at(weight), eps, px, sx, _at(gw),
+                                        _at(ws), 0 if ws is None else ws.nbytes, stream), "qlora_rms_norm_bwd")
+        return out, gw
+
+    return _launch(dy, stream, run)
+
+
+# qlora_activation values
+ACTIVATIONS = {"silu": 0, "gelu": 1}
+
+
+def _activation(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise QLoRAError(f"activation must be one of {sorted(ACTIVATIONS)}, not {name!r}")
+    return ACTIVATIONS[name]
+
+
+def qlora_gated_workspace(M: int, d_in: int, d_out: int, r: int) -> int:
+    return lib().qlora_gated_workspace(M, d_in, d_out, r)
+
+
+def qlora_gated_fwd(X: torch.Tensor, gate: NF4Weight, up: NF4Weight, A_gate: torch.Tensor, B_gate: torch.Tensor,
+                    A_up: torch.Tensor, B_up: torch.Tensor, scale: float, activation: str = "silu", save: bool = True,
+                    H: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """H = act(G) U with G = X deq(gate)^T + scale (X A_gate) B_gate and U likewise, X [M][in] bf16.  save: also bf16 of G
+    and U, and of X A of each, for the backward.  Returns (H, G, U, T_gate, T_up), the last four None without save."""
+    dev, kind = X.device, _activation(activation)
+    if X.dim() != 2 or X.shape[1] != gate.cols or not X.is_cuda:
+        raise QLoRAError(f"X must be [M][{gate.cols}] on the GPU")
+    M, d_in, d_out = X.shape[0], gate.cols, gate.rows
+    _need(X, torch.bfloat16, dev, "X")
+    if A_gate.dim() != 2:
+        raise QLoRAError("A_gate must be [in][r]")
+    r = A_gate.shape[1]
+    for t, name, shape in ((A_gate, "A_gate", (d_in, r)), (A_up, "A_up", (d_in, r)), (B_gate, "B_gate", (r, d_out)),
+                           (B_up, "B_up", (r, d_out))):
+        _need(t, torch.bfloat16, dev, name, shape)
+    for w, name in ((gate, "gate"), (up, "up")):
+        if w.codes.device != dev:
+            raise QLoRAError(f"{name} must be on {dev}")
+    if H is not None:
+        _need(H, torch.bfloat16, dev, "H", (M, d_out))
+
+    def run(stream):
+        new = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out = new(M, d_out) if H is None else H
+        saved = (new(M, d_out), new(M, d_out), new(M, r), new(M, r)) if save else (None,) * 4
+        ws = _bytes(workspace, dev, lambda: qlora_gated_workspace(M, d_in, d_out, r))
+        g, u = gate.desc(), up.desc()
+        _check(lib().qlora_gated_fwd(X.data_ptr(), M, C.byref(g), C.byref(u), A_gate.data_ptr(), B_gate.data_ptr(),
+                                     A_up.data_ptr(), B_up.data_ptr(), r, scale, kind, out.data_ptr(),
+                                     *[_at(t) for t in saved], ws.data_ptr(), ws.nbytes, stream), "qlora_gated_fwd")
+        return out, *saved
+
+    return _launch(X, stream, run)
+
+
+def qlora_gated_bwd(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, activation: str = "silu",
+                    H: torch.Tensor | bool = False, dG: torch.Tensor | None = None, dU: torch.Tensor | None = None,
+                    stream=None):
+    """Gradients of the gated block's G and U from that of H = act(G) U and the saved G, U [M][out]; qlora_linear_bwd of each
+    projection goes on from them.  H: True for H itself again in a new tensor, or a tensor to fill.  Outputs may be the
+    inputs, one each.  Returns (dG, dU, H or None)."""
+    dev, kind = dH.device, _activation(activation)
+    if dH.dim() != 2 or not dH.is_cuda:
+        raise QLoRAError("dH must be [M][out] on the GPU")
+    shape = dH.shape
+    for t, name in ((dH, "dH"), (G, "G"), (U, "U"), (dG, "dG"), (dU, "dU"), (H, "H")):
+        if isinstance(t, torch.Tensor):
+            _need(t, torch.bfloat16, dev, name, shape)
+
+    def run(stream):
+        new = lambda: torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        g = new() if dG is None else dG
+        u = new() if dU is None else dU
+        h = new() if H is True else H if isinstance(H, torch.Tensor) else None
+        _check(lib().qlora_gated_bwd(dH.data_ptr(), G.data_ptr(), U.data_ptr(), shape[0], shape[1], kind, g.data_ptr(),
+                                     u.data_ptr(), _at(h), stream), "qlora_gated_bwd")
+        return g, u, h
+
+    return _launch(dH, stream, run)
+
+
+_LOGIT_TYPES = {torch.bfloat16: 0, torch.float32: 1}   # qlora_dtype values
+
+
+def _logits(t: torch.Tensor, name: str, device=None, like=None):
+    """(address, row stride, qlora_dtype) of [rows][vocab] logits, any row stride with dense rows."""
+    strides = t.stride()
+    kind = _LOGIT_TYPES.get(t.dtype)
+    if kind is None or len(strides) != 2 or strides[1] != 1 and t.shape[1] != 1 or not t.is_cuda:
+        raise QLoRAError(f"{name} must be a bf16 or float32 [rows][vocab] tensor on the GPU, dense along vocab")
+    if like is not None and (t.device != device or t.shape != like.shape or t.dtype != like.dtype):
+        raise QLoRAError(f"{name} must be like the logits")
+    return t.data_ptr(), strides[0], kind
+
+
+def qlora_token_logprob_workspace(rows: int, vocab: int, top: int = 0) -> int:
+    return lib().qlora_token_logprob_workspace(rows, vocab, top)
+
+
+def qlora_token_logprob(logits: torch.Tensor, token: torch.Tensor | None, scale: float = 1.0, entropy: bool = False,
+                        top: int = 0, workspace: torch.Tensor | None = None, stream=None):
+    """Log probabilities of the tokens [rows] (int64; negative: none) under the softmax of scale * logits [rows][vocab]
+    (bf16 or fp32, any row stride).  Returns (logprob [rows] or None without tokens, stats [rows][2] = largest scaled logit
+    and sum of exponentials from it, entropy [rows] or None, top_logprob and top_index [rows][top] or None), all
+    fp32 but the indices (int64)."""
+    dev = logits.device
+    px, sx, kind = _logits(logits, "logits")
+    rows, vocab = logits.shape
+    if token is not None:
+        _need(token, torch.int64, dev, "token", (rows,))
+
+    def run(stream):
+        new = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)
+        lp = None if token is None else new(rows)
+        stats = new(rows, 2)
+        ent = new(rows) if entropy else None
+        tlp = new(rows, top) if top else None
+        tix = torch.empty((rows, top), dtype=torch.int64, device=dev) if top else None
+        ws = _bytes(workspace, dev, lambda: qlora_token_logprob_workspace(rows, vocab, top))
+        _check(lib().qlora_token_logprob(px, sx, rows, vocab, kind, _at(token), scale, top, _at(lp), stats.data_ptr(),
+                                         _at(ent), _at(tlp), _at(tix), ws.data_ptr(), ws.nbytes, stream),
+               "qlora_token_logprob")
+        return lp, stats, ent, tlp, tix
+
+    if top < 0:
+        raise QLoRAError("top must be 0 (none) or positive")
+    return _launch(logits, stream, run)
+
+
+def qlora_token_logprob_bwd(logits: torch.Tensor, token: torch.Tensor | None, stats: torch.Tensor,
+                            dlogprob: torch.Tensor | None, entropy: torch.Tensor | None = None,
+                            dentropy: torch.Tensor | None = None, scale: float = 1.0, out: torch.Tensor | None = None,
+                            stream=None):
+    """Gradient of the logits from those of qlora_token_logprob's logprob and entropy (fp32 [rows], either may be None), its
+    stats and, with dentropy, its entropy.  out may be the logits.  Returns it, in the logits' type."""
+    dev = logits.device
+    px, sx, kind = _logits(logits, "logits")
+    rows, vocab = logits.shape
+    if dlogprob is not None and token is None:
+        raise QLoRAError("dlogprob needs the tokens")
+    if dentropy is not None and entropy is None:
+        raise QLoRAError("dentropy needs the entropy")
+    if token is not None:
+        _need(token, torch.int64, dev, "token", (rows,))
+    _need(stats, torch.float32, dev, "stats", (rows, 2))
+    for t, name in ((dlogprob, "dlogprob"), (entropy, "entropy"), (dentropy, "dentropy")):
+        if t is not None:
+            _need(t, torch.float32, dev, name, (rows,))
+
+    def run(stream):
+        d = torch.empty((rows, vocab), dtype=logits.dtype, device=dev) if out is None else out
+        pd, sd, _ = _logits(d, "out", dev, logits)
+        _check(lib().qlora_token_logprob_bwd(px, sx, rows, vocab, kind, _at(token), scale, stats.data_ptr(), _at(dlogprob),
+                                             _at(entropy), _at(dentropy), pd, sd, stream), "qlora_token_logprob_bwd")
+        return d
+
+    return _launch(logits, stream, run)
 
 
 def qlora_profile_enable(enable: bool = True):

@@ -104,6 +104,25 @@ SIGNATURES = {
     "qlora_kv_attn": (C.c_int, [_HEADS, C.c_int64, C.POINTER(qlora_kv_cache),
                                 C.POINTER(qlora_kv_batch), C.c_float, C.c_int32, C.c_int32, _HEADS,
                                 C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qlora_rms_norm": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int32, C.c_void_p, C.c_float,
+                                 C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p]),
+    "qlora_rms_norm_bwd_workspace": (C.c_size_t, [C.c_int64, C.c_int32]),
+    "qlora_rms_norm_bwd": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64,
+                                     C.c_int32, C.c_void_p, C.c_float, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p,
+                                     C.c_size_t, C.c_void_p]),
+    "qlora_gated_workspace": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int64, C.c_int32]),
+    "qlora_gated_fwd": (C.c_int, [C.c_void_p, C.c_int64, C.POINTER(qlora_nf4), C.POINTER(qlora_nf4), C.c_void_p, C.c_void_p,
+                                  C.c_void_p, C.c_void_p, C.c_int32, C.c_float, C.c_int32, C.c_void_p, C.c_void_p,
+                                  C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qlora_gated_bwd": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_int32, C.c_void_p,
+                                  C.c_void_p, C.c_void_p, C.c_void_p]),
+    "qlora_token_logprob_workspace": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int32]),
+    "qlora_token_logprob": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_int32, C.c_void_p, C.c_float,
+                                      C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                      C.c_size_t, C.c_void_p]),
+    "qlora_token_logprob_bwd": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_int32, C.c_void_p, C.c_float,
+                                          C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64,
+                                          C.c_void_p]),
     "qlora_profile_enable": (C.c_int, [C.c_int32]),
     "qlora_profile_read": (C.c_int32, [C.POINTER(qlora_kernel_time), C.c_int32, C.c_int32]),
 }

@@ -240,6 +240,37 @@ BwdWs bwd_layout(void* base, int64_t M, int64_t in, int64_t out, int32_t r) {
   return ws;
 }
 
+// Both projections of the gated block are one launch of twice the feature tiles or workgroups.
+int64_t gated_split_stages(int64_t M, int64_t in, int64_t out) { return split_stages(M, in, (out + 63) / 64 * 128); }
+
+struct GatedWs {
+  uint16_t *Tg, *Tu;         // bf16(s X A), padded
+  float *gate, *up;          // partial sums of each side
+  LoraProblem t;
+  GemvPlan gv;
+  size_t bytes;
+};
+
+GatedWs gated_layout(void* base, int64_t M, int64_t in, int64_t out, int32_t r) {
+  Carve c(base);
+  const int64_t rp = rank_pad(r), Mm = std::max<int64_t>(M, 1);
+  GatedWs ws;
+  ws.t = lora_problem(gemm_T(nullptr, nullptr, Mm, in, r), epi_none(), kMaxSplits);
+  const int64_t st = gated_split_stages(M, in, out);
+  ws.gv = gemv_plan(Mm, in, out, rp, st != 0, true);
+  if (st) {
+    ws.gv.splits = (int)split_count(in, st);
+    ws.gv.tpart = (size_t)ws.gv.splits * Mm * ws.gv.npad;
+  }
+  const size_t pf = use_gemv(M) || st ? gemv_partial_floats(ws.gv, Mm) : lora_partial_floats(ws.t);
+  ws.Tg = c.take<uint16_t>((size_t)Mm * rp);
+  ws.Tu = c.take<uint16_t>((size_t)Mm * rp);
+  ws.gate = c.take<float>(std::max<size_t>(pf, 1));
+  ws.up = c.take<float>(std::max<size_t>(pf, 1));
+  ws.bytes = round_up(c.off, 256);
+  return ws;
+}
+
 struct QuantWs {
   unsigned long long* sums;   // one exact partial sum of the block constants per quantize workgroup
   float* absmax;
@@ -487,6 +518,72 @@ qlora_status qlora_linear_bwd(const uint16_t* dY, const uint16_t* X, const uint1
     else
       QL_HIP(launch_lora_reduce(pa.splits > 1 ? pa : pb, nullptr, "k_lora_da_db_reduce", stream));
   }
+  return QLORA_OK;
+}
+
+size_t qlora_gated_workspace(int64_t M, int64_t in, int64_t out, int32_t r) {
+  if (M < 0 || M >= (int64_t(1) << 26) || in < 64 || out < 8 || in > (int64_t(1) << 22) || out > (int64_t(1) << 22) || r < 8 ||
+      r > 256)
+    return 0;
+  return gated_layout(nullptr, M, in, out, r).bytes;
+}
+
+qlora_status qlora_gated_fwd(const uint16_t* X, int64_t M, const qlora_nf4* gate, const qlora_nf4* up,
+                             const uint16_t* A_gate, const uint16_t* B_gate, const uint16_t* A_up, const uint16_t* B_up,
+                             int32_t r, float scale, int32_t activation, uint16_t* H, uint16_t* G, uint16_t* U,
+                             uint16_t* T_gate, uint16_t* T_up, void* ws, size_t ws_bytes, hipStream_t stream) {
+  qlora_status st = check_linear(M, gate, r);
+  if (st != QLORA_OK) return st;
+  if ((st = check_linear(M, up, r)) != QLORA_OK) return st;
+  if (gate->rows != up->rows || gate->cols != up->cols) return QLORA_ERR_SHAPE;
+  if (gate->double_quant != up->double_quant || gate->codebook != up->codebook ||
+      block_of(gate->block_size) != block_of(up->block_size))
+    return QLORA_ERR_UNSUPPORTED;
+  if (activation != QLORA_ACT_SILU && activation != QLORA_ACT_GELU) return QLORA_ERR_UNSUPPORTED;
+  if (!A_gate || !B_gate || !A_up || !B_up || (M > 0 && (!X || !H))) return QLORA_ERR_NULL;
+  if ((G == nullptr) != (U == nullptr) || (T_gate == nullptr) != (T_up == nullptr)) return QLORA_ERR_NULL;
+  for (const void* p : {(const void*)X, (const void*)A_gate, (const void*)B_gate, (const void*)A_up, (const void*)B_up,
+                        (const void*)H, (const void*)G, (const void*)U, (const void*)T_gate, (const void*)T_up})
+    if (!aligned16(p)) return QLORA_ERR_ALIGN;
+  const int64_t in = gate->cols, out = gate->rows, rp = rank_pad(r);
+  const GatedWs need = gated_layout(nullptr, M, in, out, r);
+  if (!ws || ws_bytes < need.bytes) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+  if (M == 0) return QLORA_OK;
+  const GatedWs L = gated_layout(ws, M, in, out, r);
+  const NF4View vg = view_of(gate), vu = view_of(up);
+  const int64_t stages = gated_split_stages(M, in, out);
+  if (use_gemv(M) || stages) {
+    // few tokens: one pass over both packed weights that also forms the partials of X A; or, where the tiles are few, X A's
+    // partials alone and the products in K-slices; then the epilogue
+    const GemvUp side{vu, A_up, L.up};
+    QL_HIP(launch_gemv(X, M, in, out, vg, A_gate, r, L.gv, L.gate, stream, stages != 0, &side));
+    if (stages) QL_HIP(launch_gated_gemm_split(X, M, in, out, vg, vu, (int)stages, L.gate, L.up, L.gv.npad, stream));
+    QL_HIP(launch_gated_epilogue(GatedSide{L.gate, B_gate, G, T_gate}, GatedSide{L.up, B_up, U, T_up}, L.gv, M, out, r, scale,
+                                 activation, H, stream));
+    return QLORA_OK;
+  }
+  LoraProblem pg = lora_problem(gemm_T(X, A_gate, M, in, r), LoraEpi{T_gate, r, 1.0f, L.Tg, rp, scale, nullptr, 0.0f}, kMaxSplits);
+  LoraProblem pu = lora_problem(gemm_T(X, A_up, M, in, r), LoraEpi{T_up, r, 1.0f, L.Tu, rp, scale, nullptr, 0.0f}, kMaxSplits);
+  pg.partial = L.gate;
+  pu.partial = L.up;
+  QL_HIP(launch_lora(pg, &pu, "k_lora_xa", stream));
+  if (pg.splits > 1) QL_HIP(launch_lora_reduce(pg, &pu, "k_lora_xa_reduce", stream));
+  QL_HIP(launch_gated_gemm(X, M, in, out, vg, vu, L.Tg, L.Tu, rp, B_gate, B_up, r, activation, H, G, U, stream));
+  return QLORA_OK;
+}
+
+qlora_status qlora_gated_bwd(const uint16_t* dH, const uint16_t* G, const uint16_t* U, int64_t M, int64_t out_features,
+                             int32_t activation, uint16_t* dG, uint16_t* dU, uint16_t* H, hipStream_t stream) {
+  if (M < 0 || M >= (int64_t(1) << 26) || out_features < 8 || out_features > (int64_t(1) << 22) || out_features % 8 != 0)
+    return QLORA_ERR_SHAPE;
+  if (activation != QLORA_ACT_SILU && activation != QLORA_ACT_GELU) return QLORA_ERR_UNSUPPORTED;
+  if (M == 0) return QLORA_OK;
+  if (!dH || !G || !U || !dG || !dU) return QLORA_ERR_NULL;
+  if (!aligned16(dH) || !aligned16(G) || !aligned16(U) || !aligned16(dG) || !aligned16(dU) || !aligned16(H))
+    return QLORA_ERR_ALIGN;
+  if (dG == dU || H == dG || H == dU) return QLORA_ERR_SHAPE;
+  QL_HIP(launch_gated_bwd(dH, G, U, M * out_features, activation, dG, dU, H, stream));
   return QLORA_OK;
 }
 

@@ -11,7 +11,13 @@
 // quarter of one 64-weight block (the block's scaled 16-entry table is built by the
 // four threads of the block together, the lookups are byte permutes) straight into
 // the LDS feature tile.
+//
+// The gated block's forward, H = bf16(act(G) U) with G and U two such products of the same X, runs through the same code: the 128
+// features of a tile are 64 of the gate's weight and the same 64 of the up projection's, so the waves of one feature half
+// hold G and those of the other U, and meet in LDS after the reduction.  X is read once for both, and G and U
+// reach memory only where the backward wants them.
 #include "common.h"
+#include "gated.h"
 #include "gemm_core.h"
 #include "kernels.h"
 
@@ -36,6 +42,14 @@ struct FwdParams {
   float* partial;
   int64_t npad;
   uint32_t spl;
+  // gated: the up projection's weight (w, Ts, B, partial are the gate's), outputs besides Y = H
+  NF4View w2;
+  const uint16_t* Ts2;
+  const uint16_t* B2;
+  float* partial2;
+  uint16_t* G;   // or NULL, with U
+  uint16_t* U;
+  int act;
 };
 
 struct WRegs {
@@ -55,17 +69,19 @@ struct Stage {
 // SPLIT: a workgroup covers stages [spl s, spl (s + 1)) of its tile's reduction and writes
 // fp32 partial sums (few tokens: the K-slices give the GPU enough workgroups); the adapter
 // term and the final sum come from the weight-streaming path's epilogue.
-template <bool DQ, int BM, bool SPLIT>
+// GATED: a tile has 64 features of each of two weights (p.w, p.w2); see above.
+template <bool DQ, int BM, bool SPLIT, bool GATED>
 __global__ __launch_bounds__(NT) void k_fwd_nf4_gemm(FwdParams p) {
   __shared__ __attribute__((aligned(16))) uint16_t smem[SMEM_ELEMS];
   uint16_t* const sT[2] = {smem, smem + TILE_T};
   uint16_t* const sF[2] = {smem + 2 * TILE_T, smem + 2 * TILE_T + TILE_F};
 
   int64_t tt, tf;
-  const int64_t tiles_t = (p.M + BT - 1) / BT, tiles_f = (p.N + BF - 1) / BF;
+  constexpr int FT = GATED ? BF / 2 : BF;   // features of a tile
+  const int64_t tiles_t = (p.M + BT - 1) / BT, tiles_f = (p.N + FT - 1) / FT;
   const uint32_t split = SPLIT ? (uint32_t)(blockIdx.x / (tiles_t * tiles_f)) : 0u;
   tile_of(tiles_t, tiles_f, tt, tf, SPLIT ? (int64_t)blockIdx.x - (int64_t)split * tiles_t * tiles_f : -1);
-  const uint32_t m0 = (uint32_t)(tt * BT), n0 = (uint32_t)(tf * BF);
+  const uint32_t m0 = (uint32_t)(tt * BT), n0 = (uint32_t)(tf * FT);
   const uint32_t nkb_all = (uint32_t)(p.K / 64);
   const uint32_t it0 = SPLIT ? split * p.spl : 0u;                       // first stage
   const uint32_t nkb = SPLIT ? min(nkb_all, it0 + p.spl) - it0 : nkb_all;   // stages of this workgroup
@@ -73,15 +89,17 @@ __global__ __launch_bounds__(NT) void k_fwd_nf4_gemm(FwdParams p) {
   // weight row t/4 of the tile, quarter t%4 of its block (groups 2q and 2q+1 -> chunks
   // 2q, 2q+1 of the LDS row); rows past N read as zero (their outputs are not stored)
   const int wrow = t >> 2, wq = t & 3;
-  const uint32_t wblk0 = (n0 + wrow) * nkb_all;
+  const uint32_t wblk0 = (n0 + (GATED ? wrow & (BF / 2 - 1) : wrow)) * nkb_all;
   const uint32_t code_off = wblk0 * kBlockBytes + wq * 8;
 
   const TokenSrc xs = token_src(p.X, (uint64_t)p.M * p.K * 2, (uint32_t)p.K, m0);
-  const rsrc_t rC = make_rsrc(p.w.codes, p.codes_bytes);
-  const rsrc_t rA = make_rsrc(p.w.absmax, p.absmax_bytes);
-  const rsrc_t rC1 = make_rsrc(p.w.c1, p.c1_bytes);
+  // (waves 4 .. 7 load rows 64 .. 127 of the tile)
+  const bool up = GATED && __builtin_amdgcn_readfirstlane(t >> 6) >= 4;
+  const rsrc_t rC = make_rsrc(up ? p.w2.codes : p.w.codes, p.codes_bytes);
+  const rsrc_t rA = make_rsrc(up ? p.w2.absmax : p.w.absmax, p.absmax_bytes);
+  const rsrc_t rC1 = make_rsrc(up ? p.w2.c1 : p.w.c1, p.c1_bytes);
   constexpr bool dq = DQ;
-  const float mu = dq ? *p.w.mu : 0.0f;
+  const float mu = dq ? *(up ? p.w2.mu : p.w.mu) : 0.0f;
   const QuadLevels lev = quad_levels(p.tab);
 
   const uint32_t bsh = (uint32_t)(p.w.bshift - 6);   // BM == 1: 64-chunks per block, log2
@@ -179,6 +197,13 @@ __global__ __launch_bounds__(NT) void k_fwd_nf4_gemm(FwdParams p) {
     __syncthreads();
   }
 
+  if constexpr (SPLIT && GATED) {
+    // this wave's 64 features of its weight start at n0 (store_out_f32 adds the feature half's offset)
+    if (combine_halves(acc, smem))
+      store_out_f32(acc, (wave_f() ? p.partial2 : p.partial) + (int64_t)split * p.M * p.npad, p.npad, m0, p.M,
+                    (int64_t)n0 - wave_f() * 64, p.N);
+    return;
+  }
   if constexpr (SPLIT) {
     if (combine_halves(acc, smem))
       store_out_f32(acc, p.partial + (int64_t)split * p.M * p.npad, p.npad, m0, p.M, n0, p.N);
@@ -187,23 +212,117 @@ __global__ __launch_bounds__(NT) void k_fwd_nf4_gemm(FwdParams p) {
 
   // adapter stages: Ts [M][rp] against rows of B, kept as stored ([j][n]) in the natural
   // tile and read with transposing loads.  Rows j >= r lie past the end of B and read zero.
+  // (Gated: each feature half has its own Ts, in the other token buffer, and its half of the natural tile.)
   const TokenSrc ts = token_src(p.Ts, (uint64_t)p.M * p.rp * 2, (uint32_t)p.rp, m0);
-  const rsrc_t rB = make_rsrc(p.B, (uint64_t)p.r * p.N * 2);
+  const uint64_t bbytes = (uint64_t)p.r * p.N * 2;
+  const rsrc_t rB = make_rsrc(p.B, bbytes);
   const int bj = t >> 3, be = t & 7;
   for (uint32_t j0 = 0; j0 < (uint32_t)p.rp; j0 += 64) {
     TokenRegs T;
     load_tokens(T, ts, j0);
-    const uint32_t boff = ((j0 + bj) * (uint32_t)p.N + n0 + be * 16) * 2;
-    const uint4 b0 = ld16(rB, boff), b1 = ld16(rB, boff + 16);
+    uint4 b0, b1;
+    if constexpr (GATED) {
+      const TokenSrc ts2 = token_src(p.Ts2, (uint64_t)p.M * p.rp * 2, (uint32_t)p.rp, m0);
+      TokenRegs T2;
+      load_tokens(T2, ts2, j0);
+      const rsrc_t rB2 = make_rsrc(p.B2, bbytes);
+      const uint32_t boff = ((j0 + bj) * (uint32_t)p.N + n0 + (be & 3) * 16) * 2;
+      const uint32_t og = be < 4 ? boff : (uint32_t)bbytes, ou = be < 4 ? (uint32_t)bbytes : boff;
+      const uint4 g0 = ld16(rB, og), g1 = ld16(rB, og + 16), u0 = ld16(rB2, ou), u1 = ld16(rB2, ou + 16);
+      b0 = make_uint4(g0.x | u0.x, g0.y | u0.y, g0.z | u0.z, g0.w | u0.w);   // (one of the two is zero)
+      b1 = make_uint4(g1.x | u1.x, g1.y | u1.y, g1.z | u1.z, g1.w | u1.w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) store_tokens_part(T2, sT[1], i);
+    } else {
+      const uint32_t boff = ((j0 + bj) * (uint32_t)p.N + n0 + be * 16) * 2;
+      b0 = ld16(rB, boff), b1 = ld16(rB, boff + 16);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) store_tokens_part(T, sT[0], i);
     *reinterpret_cast<uint4*>(sF[0] + swzN(bj, 2 * be)) = b0;
     *reinterpret_cast<uint4*>(sF[0] + swzN(bj, 2 * be + 1)) = b1;
     __syncthreads();
-    mma_stage<true>(acc, sT[0], sF[0]);
+    mma_stage<true>(acc, GATED && wave_f() ? sT[1] : sT[0], sF[0]);
     __syncthreads();
   }
-  if (combine_halves(acc, smem)) store_out(acc, p.Y, p.N, m0, p.M, n0, p.N);
+  if constexpr (!GATED) {
+    if (combine_halves(acc, smem)) store_out(acc, p.Y, p.N, m0, p.M, n0, p.N);
+  } else {
+    const bool holds = combine_halves(acc, smem);
+    // the wave of G keeps features 0 .. 31 of the tile and takes U's from the wave of U, which keeps 32 .. 63
+    const int lane = t & 63, q = wave_id() & 3, wf = wave_f();
+    float4* const x = reinterpret_cast<float4*>(smem);
+    if (holds) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int v4 = 0; v4 < 4; ++v4) {
+          const f32x16 c = wf ? acc.c[0][m] : acc.c[1][m];
+          x[((q * 4 + m) * 4 + v4) * 64 + lane] = make_float4(c[4 * v4], c[4 * v4 + 1], c[4 * v4 + 2], c[4 * v4 + 3]);
+        }
+    }
+    __syncthreads();
+    if (!holds) return;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int64_t tok = (int64_t)m0 + wave_t() * 128 + m * 32 + (lane & 31);
+      const f32x16 own = wf ? acc.c[1][m] : acc.c[0][m];
+      if (tok >= p.M) continue;
+#pragma unroll
+      for (int v4 = 0; v4 < 4; ++v4) {
+        const int64_t feat = (int64_t)n0 + wf * 32 + 8 * v4 + 4 * (lane >> 5);
+        if (feat >= p.N) continue;
+        const float4 o = x[(((q ^ 2) * 4 + m) * 4 + v4) * 64 + lane];
+        const float mine[4] = {own[4 * v4], own[4 * v4 + 1], own[4 * v4 + 2], own[4 * v4 + 3]};
+        const float other[4] = {o.x, o.y, o.z, o.w};
+        float g[4], u[4], h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          g[i] = wf ? other[i] : mine[i];
+          u[i] = wf ? mine[i] : other[i];
+          h[i] = activate(g[i], p.act) * u[i];
+        }
+        const int64_t at = tok * p.N + feat;
+        *reinterpret_cast<uint2*>(p.Y + at) = make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
+        if (p.G) {
+          *reinterpret_cast<uint2*>(p.G + at) = make_uint2(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]));
+          *reinterpret_cast<uint2*>(p.U + at) = make_uint2(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]));
+        }
+      }
+    }
+  }
+}
+
+template <bool SPLIT, bool GATED>
+void launch_variant(const FwdParams& p, unsigned wgs, hipStream_t s) {
+  const dim3 grid(wgs), block(NT);
+  const int bm = p.w.bshift == 6 ? 0 : p.w.bshift > 6 ? 1 : 2;
+  if (p.w.dq) {
+    if (bm == 0) hipLaunchKernelGGL((k_fwd_nf4_gemm<true, 0, SPLIT, GATED>), grid, block, 0, s, p);
+    else if (bm == 1) hipLaunchKernelGGL((k_fwd_nf4_gemm<true, 1, SPLIT, GATED>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((k_fwd_nf4_gemm<true, 2, SPLIT, GATED>), grid, block, 0, s, p);
+  } else {
+    if (bm == 0) hipLaunchKernelGGL((k_fwd_nf4_gemm<false, 0, SPLIT, GATED>), grid, block, 0, s, p);
+    else if (bm == 1) hipLaunchKernelGGL((k_fwd_nf4_gemm<false, 1, SPLIT, GATED>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((k_fwd_nf4_gemm<false, 2, SPLIT, GATED>), grid, block, 0, s, p);
+  }
+}
+
+// What the launches share: the weight's buffers and their sizes.
+FwdParams params_of(const uint16_t* X, int64_t M, int64_t K, int64_t N, const NF4View& w) {
+  // 64-element code chunks, and blocks (one constant each; in is a multiple of the block size)
+  const uint64_t nchunk = (uint64_t)N * K / 64, nblk = ((uint64_t)N * K) >> w.bshift;
+  FwdParams p{};
+  p.X = X;
+  p.M = M;
+  p.K = K;
+  p.N = N;
+  p.w = w;
+  p.codes_bytes = nchunk * kBlockBytes;
+  p.absmax_bytes = w.dq ? nblk : nblk * 4;
+  p.c1_bytes = w.dq ? ((nblk + 255) / 256) * 4 : 0;
+  p.tab = nf4_table(w.cb);
+  return p;
 }
 
 }  // namespace
@@ -211,47 +330,60 @@ __global__ __launch_bounds__(NT) void k_fwd_nf4_gemm(FwdParams p) {
 hipError_t launch_fwd_gemm(const uint16_t* X, int64_t M, int64_t K, int64_t N, const NF4View& w,
                            const uint16_t* Ts, int64_t rp, const uint16_t* B, int64_t r, uint16_t* Y,
                            hipStream_t s) {
-  // 64-element code chunks, and blocks (one constant each; in is a multiple of the block size)
-  const uint64_t nchunk = (uint64_t)N * K / 64, nblk = ((uint64_t)N * K) >> w.bshift;
-  FwdParams p{X, M, K, N, w, nchunk * kBlockBytes, w.dq ? nblk : nblk * 4, w.dq ? ((nblk + 255) / 256) * 4 : 0,
-              Ts, rp, B, r, Y, nf4_table(w.cb), nullptr, 0, 0};
-  const int64_t tiles = ((M + BT - 1) / BT) * ((N + BF - 1) / BF);
-  const int bm = w.bshift == 6 ? 0 : w.bshift > 6 ? 1 : 2;
+  FwdParams p = params_of(X, M, K, N, w);
+  p.Ts = Ts;
+  p.rp = rp;
+  p.B = B;
+  p.r = r;
+  p.Y = Y;
   ProfScope ps("k_fwd_nf4_gemm", s);
-  const dim3 grid((unsigned)tiles), block(NT);
-  if (w.dq) {
-    if (bm == 0) hipLaunchKernelGGL((k_fwd_nf4_gemm<true, 0, false>), grid, block, 0, s, p);
-    else if (bm == 1) hipLaunchKernelGGL((k_fwd_nf4_gemm<true, 1, false>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((k_fwd_nf4_gemm<true, 2, false>), grid, block, 0, s, p);
-  } else {
-    if (bm == 0) hipLaunchKernelGGL((k_fwd_nf4_gemm<false, 0, false>), grid, block, 0, s, p);
-    else if (bm == 1) hipLaunchKernelGGL((k_fwd_nf4_gemm<false, 1, false>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((k_fwd_nf4_gemm<false, 2, false>), grid, block, 0, s, p);
-  }
+  launch_variant<false, false>(p, (unsigned)(((M + BT - 1) / BT) * ((N + BF - 1) / BF)), s);
   return hipGetLastError();
 }
 
 hipError_t launch_fwd_gemm_split(const uint16_t* X, int64_t M, int64_t K, int64_t N, const NF4View& w, int stages,
                                  float* partial, int64_t npad, hipStream_t s) {
-  const uint64_t nchunk = (uint64_t)N * K / 64, nblk = ((uint64_t)N * K) >> w.bshift;
-  const uint32_t nkb = (uint32_t)(K / 64);
-  const uint32_t spl = (uint32_t)stages;
-  FwdParams p{X, M, K, N, w, nchunk * kBlockBytes, w.dq ? nblk : nblk * 4, w.dq ? ((nblk + 255) / 256) * 4 : 0,
-              nullptr, 0, nullptr, 0, nullptr, nf4_table(w.cb), partial, npad, spl};
-  const int64_t tiles = ((M + BT - 1) / BT) * ((N + BF - 1) / BF);
-  const int64_t used = (nkb + spl - 1) / spl;   // splits that get at least one stage
+  FwdParams p = params_of(X, M, K, N, w);
+  p.partial = partial;
+  p.npad = npad;
+  p.spl = (uint32_t)stages;
+  const int64_t used = (K / 64 + stages - 1) / stages;   // splits that get at least one stage
   ProfScope ps("k_fwd_nf4_gemm", s);
-  const dim3 grid((unsigned)(tiles * used)), block(NT);
-  const int bm = w.bshift == 6 ? 0 : w.bshift > 6 ? 1 : 2;
-  if (w.dq) {
-    if (bm == 0) hipLaunchKernelGGL((k_fwd_nf4_gemm<true, 0, true>), grid, block, 0, s, p);
-    else if (bm == 1) hipLaunchKernelGGL((k_fwd_nf4_gemm<true, 1, true>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((k_fwd_nf4_gemm<true, 2, true>), grid, block, 0, s, p);
-  } else {
-    if (bm == 0) hipLaunchKernelGGL((k_fwd_nf4_gemm<false, 0, true>), grid, block, 0, s, p);
-    else if (bm == 1) hipLaunchKernelGGL((k_fwd_nf4_gemm<false, 1, true>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((k_fwd_nf4_gemm<false, 2, true>), grid, block, 0, s, p);
-  }
+  launch_variant<true, false>(p, (unsigned)(((M + BT - 1) / BT) * ((N + BF - 1) / BF) * used), s);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_gemm(const uint16_t* X, int64_t M, int64_t K, int64_t N, const NF4View& gate, const NF4View& up,
+                             const uint16_t* Tg, const uint16_t* Tu, int64_t rp, const uint16_t* Bg, const uint16_t* Bu,
+                             int64_t r, int act, uint16_t* H, uint16_t* G, uint16_t* U, hipStream_t s) {
+  FwdParams p = params_of(X, M, K, N, gate);
+  p.w2 = up;
+  p.Ts = Tg;
+  p.Ts2 = Tu;
+  p.rp = rp;
+  p.B = Bg;
+  p.B2 = Bu;
+  p.r = r;
+  p.act = act;
+  p.Y = H;
+  p.G = G;
+  p.U = U;
+  ProfScope ps("k_gated_nf4_gemm", s);
+  launch_variant<false, true>(p, (unsigned)(((M + BT - 1) / BT) * ((N + BF / 2 - 1) / (BF / 2))), s);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_gemm_split(const uint16_t* X, int64_t M, int64_t K, int64_t N, const NF4View& gate, const NF4View& up,
+                                   int stages, float* gate_partial, float* up_partial, int64_t npad, hipStream_t s) {
+  FwdParams p = params_of(X, M, K, N, gate);
+  p.w2 = up;
+  p.partial = gate_partial;
+  p.partial2 = up_partial;
+  p.npad = npad;
+  p.spl = (uint32_t)stages;
+  const int64_t used = (K / 64 + stages - 1) / stages;
+  ProfScope ps("k_gated_nf4_gemm", s);
+  launch_variant<true, true>(p, (unsigned)(((M + BT - 1) / BT) * ((N + BF / 2 - 1) / (BF / 2)) * used), s);
   return hipGetLastError();
 }
 

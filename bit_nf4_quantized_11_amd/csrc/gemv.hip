@@ -77,6 +77,17 @@ struct GemvParams {
   NF4Table tab;
 };
 
+// Gated: what the up projection's half of the launch takes in place of the gate's
+struct GemvSide {
+  const uint8_t* codes;
+  const void* absmax;
+  const float* c1;
+  const float* mu;
+  const uint16_t* A;
+  float* partial;
+  float* tpartial;
+};
+
 // Natural [ACH][64] tile of A: row k = 128 bytes of eight 16-byte chunks; chunk q of row
 // k sits at q ^ 2 f(k), f(k) = ((k >> 1) & 1) | ((k >> 2) & 2), which keeps the
 // transposing reads (4 rows x 32 bytes per 16 lanes, two such row quads 8 apart per 32
@@ -404,6 +415,29 @@ __global__ __launch_bounds__(GT) void k_fwd_nf4_gemv(GemvParams p) {
     weight_group<DQ, BM, TG>(p, (int)blockIdx.x - n_adapter, lds);
 }
 
+// The gated block's two projections in one launch: the first half of the workgroups is the gate's, the second the up
+// projection's.
+template <bool DQ, int BM, int TG>
+__global__ __launch_bounds__(GT) void k_gated_nf4_gemv(GemvParams p, GemvSide up) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int n_adapter = (int)(p.agroups * p.asplits) * p.ngr, half = (int)(gridDim.x / 2);
+  int bid = (int)blockIdx.x;
+  if (bid >= half) {
+    bid -= half;
+    p.w.codes = up.codes;
+    p.w.absmax = up.absmax;
+    p.w.c1 = up.c1;
+    p.w.mu = up.mu;
+    p.A = up.A;
+    p.partial = up.partial;
+    p.tpartial = up.tpartial;
+  }
+  if (bid < n_adapter)
+    adapter_group(p, bid, lds);
+  else
+    weight_group<DQ, BM, TG>(p, bid - n_adapter, lds);
+}
+
 // Y[m][n] = bf16( sum over slices of partial[slice][m][n] + sum_j Ts[m][j] B[j][n] ),
 // Ts = bf16(s T), T = sum over adapter slices of tpartial[slice][m][j] (formed again by every
 // workgroup: 16 r values); column block 0 also writes T_save = bf16(T).  A workgroup covers
@@ -521,22 +555,29 @@ __global__ __launch_bounds__(256) void k_gemv_epilogue(const float* __restrict__
   }
 }
 
-// dispatch over the template flags (DQ, BM, TG)
+// dispatch over the template flags (DQ, BM, TG); `up`: of the gated block
 template <int TG>
-void launch_gemv_variant(bool dq, int bm, int tg, dim3 grid, size_t lds, const GemvParams& p, hipStream_t s) {
+void launch_gemv_variant(bool dq, int bm, int tg, dim3 grid, size_t lds, const GemvParams& p, const GemvSide* up,
+                         hipStream_t s) {
   if constexpr (TG < 4) {
-    if (tg != TG) return launch_gemv_variant<TG * 2>(dq, bm, tg, grid, lds, p, s);
+    if (tg != TG) return launch_gemv_variant<TG * 2>(dq, bm, tg, grid, lds, p, up, s);
   }
   const dim3 block(GT);
+#define GEMV_LAUNCH(DQ, BM)                                                                           \
+  do {                                                                                                \
+    if (up) hipLaunchKernelGGL((k_gated_nf4_gemv<DQ, BM, TG>), grid, block, lds, s, p, *up);          \
+    else hipLaunchKernelGGL((k_fwd_nf4_gemv<DQ, BM, TG>), grid, block, lds, s, p);                    \
+  } while (0)
   if (dq) {
-    if (bm == 0) hipLaunchKernelGGL((k_fwd_nf4_gemv<true, 0, TG>), grid, block, lds, s, p);
-    else if (bm == 1) hipLaunchKernelGGL((k_fwd_nf4_gemv<true, 1, TG>), grid, block, lds, s, p);
-    else hipLaunchKernelGGL((k_fwd_nf4_gemv<true, 2, TG>), grid, block, lds, s, p);
+    if (bm == 0) GEMV_LAUNCH(true, 0);
+    else if (bm == 1) GEMV_LAUNCH(true, 1);
+    else GEMV_LAUNCH(true, 2);
   } else {
-    if (bm == 0) hipLaunchKernelGGL((k_fwd_nf4_gemv<false, 0, TG>), grid, block, lds, s, p);
-    else if (bm == 1) hipLaunchKernelGGL((k_fwd_nf4_gemv<false, 1, TG>), grid, block, lds, s, p);
-    else hipLaunchKernelGGL((k_fwd_nf4_gemv<false, 2, TG>), grid, block, lds, s, p);
+    if (bm == 0) GEMV_LAUNCH(false, 0);
+    else if (bm == 1) GEMV_LAUNCH(false, 1);
+    else GEMV_LAUNCH(false, 2);
   }
+#undef GEMV_LAUNCH
 }
 
 }  // namespace
@@ -544,21 +585,21 @@ void launch_gemv_variant(bool dq, int bm, int tg, dim3 grid, size_t lds, const G
 // Weight slices of SLB blocks, each split into contiguous ranges of 16-row groups, and
 // adapter slices of KA rows of A.  The grid fills kSlotsPerCU workgroups per CU in one round.
 // adapters_only (a launch of X A alone): slices of at least 256 rows, as many as it takes for
-// the adapter workgroups to reach about one per CU.
-GemvPlan gemv_plan(int64_t M, int64_t K, int64_t N, int64_t rp, bool adapters_only) {
+// the adapter workgroups to reach about one per CU.  gated: two such weights share the launch.
+GemvPlan gemv_plan(int64_t M, int64_t K, int64_t N, int64_t rp, bool adapters_only, bool gated) {
   const int64_t nkb = K / 64;
   const int64_t Mm = std::max<int64_t>(M, 1);
   GemvPlan pl;
   pl.ngr = (int)((Mm + 15) / 16);
   pl.tg = pl.ngr == 1 ? 1 : pl.ngr == 2 ? 2 : 4;
-  const int64_t slots = 256 * (pl.tg == 1 ? kSlotsPerCU : 1);   // TG > 1: 256 VGPRs, one per CU
+  const int64_t slots = 256 * (pl.tg == 1 ? kSlotsPerCU : 1) / (gated ? 2 : 1);   // TG > 1: 256 VGPRs, one per CU
   pl.splits = (int)((nkb + SLB - 1) / SLB);
   pl.rgroups = (N + RGR - 1) / RGR;
   pl.npad = pl.rgroups * RGR;
   pl.agroups = rp / GROWS;
   int64_t ka = KA;
   if (adapters_only) {
-    const int64_t want = std::max<int64_t>(1, 256 / (pl.agroups * pl.ngr));
+    const int64_t want = std::max<int64_t>(1, (gated ? 128 : 256) / (pl.agroups * pl.ngr));
     ka = std::max<int64_t>(256, ((K + want - 1) / want + 255) / 256 * 256);
   }
   pl.ka = (int)std::min<int64_t>(ka, (K + 63) / 64 * 64);
@@ -574,7 +615,8 @@ size_t gemv_partial_floats(const GemvPlan& pl, int64_t M) {
 }
 
 hipError_t launch_gemv(const uint16_t* X, int64_t M, int64_t K, int64_t N, const NF4View& w, const uint16_t* A,
-                       int64_t r, const GemvPlan& pl, float* partial, hipStream_t s, bool adapters_only) {
+                       int64_t r, const GemvPlan& pl, float* partial, hipStream_t s, bool adapters_only,
+                       const GemvUp* up) {
   // 64-element code chunks, and blocks (one constant each; in is a multiple of the block size)
   const uint64_t nchunk = (uint64_t)N * K / 64, nblk = ((uint64_t)N * K) >> w.bshift;
   GemvParams p{X, M, K, N, w, nchunk * kBlockBytes, w.dq ? nblk : nblk * 4, w.dq ? ((nblk + 255) / 256) * 4 : 0,
@@ -582,11 +624,13 @@ hipError_t launch_gemv(const uint16_t* X, int64_t M, int64_t K, int64_t N, const
                pl.rranges, pl.agroups, pl.asplits, pl.ka, pl.ngr, nf4_table(w.cb)};
   // X A alone: the TG = 1 code (the adapter workgroups do not depend on TG) and their LDS only
   const size_t lds = adapters_only ? kLdsAdapter : std::max(kLdsWeight, kLdsAdapter);
-  ProfScope ps("k_fwd_nf4_gemv", s);
+  GemvSide side{};
+  if (up) side = GemvSide{up->w.codes, up->w.absmax, up->w.c1, up->w.mu, up->A, up->partial, up->partial + pl.tpart};
+  ProfScope ps(up ? "k_gated_nf4_gemv" : "k_fwd_nf4_gemv", s);
   const int64_t n_adapter = pl.agroups * pl.asplits * pl.ngr;
-  const dim3 grid((unsigned)((adapters_only ? 0 : pl.rranges * pl.splits) + n_adapter));
+  const dim3 grid((unsigned)(((adapters_only ? 0 : pl.rranges * pl.splits) + n_adapter) * (up ? 2 : 1)));
   const int bm = w.bshift == 6 ? 0 : w.bshift > 6 ? 1 : 2;
-  launch_gemv_variant<1>(w.dq != 0, bm, adapters_only ? 1 : pl.tg, grid, lds, p, s);
+  launch_gemv_variant<1>(w.dq != 0, bm, adapters_only ? 1 : pl.tg, grid, lds, p, up ? &side : nullptr, s);
   return hipGetLastError();
 }
 

@@ -113,14 +113,41 @@ struct GemvPlan {
   int tg;                     // token groups each weight lane feeds (1, 2 or 4 >= ngr)
   size_t tpart;               // float offset of the adapter partials
 };
-GemvPlan gemv_plan(int64_t M, int64_t K, int64_t N, int64_t rp, bool adapters_only = false);
+GemvPlan gemv_plan(int64_t M, int64_t K, int64_t N, int64_t rp, bool adapters_only = false, bool gated = false);
 size_t gemv_partial_floats(const GemvPlan& pl, int64_t M);
 // adapters_only: launch only the X A workgroups (their partials feed the epilogue after the
 // split large-M forward)
+// up: the gated block's second projection in the same launch (its weight has w's format, pl is a gated plan)
+struct GemvUp {
+  NF4View w;
+  const uint16_t* A;
+  float* partial;
+};
 hipError_t launch_gemv(const uint16_t* X, int64_t M, int64_t K, int64_t N, const NF4View& w, const uint16_t* A,
-                       int64_t r, const GemvPlan& pl, float* partial, hipStream_t s, bool adapters_only = false);
+                       int64_t r, const GemvPlan& pl, float* partial, hipStream_t s, bool adapters_only = false,
+                       const GemvUp* up = nullptr);
 hipError_t launch_gemv_epilogue(const float* partial, const GemvPlan& pl, int64_t M, int64_t N, const uint16_t* B,
                                 int64_t r, float scale, uint16_t* Y, uint16_t* T_save, hipStream_t s);
+
+// ---- gated block (fwd_gemm.hip, gated.hip): H = bf16(act(G) U), G and U two products as above of one X and two weights of
+// one format.  act: qlora_activation.  G, U in bf16 where wanted (both or neither).
+hipError_t launch_gated_gemm(const uint16_t* X, int64_t M, int64_t K, int64_t N, const NF4View& gate, const NF4View& up,
+                             const uint16_t* Tg, const uint16_t* Tu, int64_t rp, const uint16_t* Bg, const uint16_t* Bu,
+                             int64_t r, int act, uint16_t* H, uint16_t* G, uint16_t* U, hipStream_t s);
+hipError_t launch_gated_gemm_split(const uint16_t* X, int64_t M, int64_t K, int64_t N, const NF4View& gate, const NF4View& up,
+                                   int stages, float* gate_partial, float* up_partial, int64_t npad, hipStream_t s);
+// the epilogue of both few-token forms: partials of the two sides as launch_gemv and launch_gated_gemm_split leave them
+struct GatedSide {
+  const float* partial;
+  const uint16_t* B;
+  uint16_t* out;      // G or U, or NULL
+  uint16_t* T_save;   // or NULL
+};
+hipError_t launch_gated_epilogue(const GatedSide& gate, const GatedSide& up, const GemvPlan& pl, int64_t M, int64_t N,
+                                 int64_t r, float scale, int act, uint16_t* H, hipStream_t s);
+// dG = bf16(dH U act'(G)), dU = bf16(dH act(G)), H = bf16(act(G) U) or NULL; n elements, a multiple of 8
+hipError_t launch_gated_bwd(const uint16_t* dH, const uint16_t* G, const uint16_t* U, int64_t n, int act, uint16_t* dG,
+                            uint16_t* dU, uint16_t* H, hipStream_t s);
 
 // ---- backward dX (dx_gemm.hip) --------------------------------------------------------------
 // dX[M][K] = bf16( dY[M][N] deq(W) + Gs[M][rp] A^T ), A [K][r].

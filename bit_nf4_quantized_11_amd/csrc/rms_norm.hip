@@ -1,0 +1,290 @@
+// Residual addition and root-mean-square norm of rows, and the backward.
+//
+//   h = bf16(x + residual),  y = bf16(h w r),  r = 1 / sqrt(mean(h^2) + eps)
+//   dx = bf16(dh + r (w dy - h r^2 mean(w dy h))),  dw = sum over rows of dy h r
+//
+// Bound by HBM: 4 to 8 B per element in either direction.  A row stays in the registers of the T threads that
+// hold it (a wave for short rows, a workgroup for long ones), 8 elements to a load, so each tensor is read or written once.
+// The backward walks over rows with the weight's gradient in registers, one partial per group of T threads,
+// summed by a second kernel in a fixed order.
+#include "kernels.h"
+#include "rows.h"
+
+namespace qlora {
+
+namespace {
+
+constexpr int NT = 256;   // threads of a workgroup of several rows
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+__device__ __forceinline__ const uint4* row_of(const RowsView& v, int64_t row) {
+  return reinterpret_cast<const uint4*>(v.data + row * v.stride);
+}
+__device__ __forceinline__ uint4* out_row(const RowsView& v, int64_t row) {
+  return reinterpret_cast<uint4*>(v.data + row * v.stride);
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+// Sums of N values over the T threads of a row, the same in all of them.  `buf`: [T / 64][N] floats, free again
+// after the barrier of the next call but one (two buffers).
+template <int T, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float* buf) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if constexpr (T > 64) {
+    const int w = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) buf[w * N + i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = buf[i];
+#pragma unroll
+      for (int j = 1; j < T / 64; ++j) v[i] += buf[j * N + i];
+    }
+  }
+}
+
+template <int T, int C, bool RES>
+__global__ __launch_bounds__(T < NT ? NT : T) void k_rms_norm(NormArgs a) {
+  __shared__ float buf[T / 64];
+  const int t = threadIdx.x % T, chunks = a.dim >> 3;
+  const int64_t row = (int64_t)blockIdx.x * (T < NT ? NT / T : 1) + threadIdx.x / T;
+  if (row >= a.rows) return;   // (a whole wave, and never one of several that wait for each other)
+  const uint4 zero = make_uint4(0, 0, 0, 0), one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+  uint4 xv[C], rv[C], wv[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int c = t + i * T;
+    const bool in = c < chunks;
+    xv[i] = in ? row_of(a.x, row)[c] : zero;
+    if (RES) rv[i] = in ? row_of(a.res, row)[c] : zero;
+  }
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int c = t + i * T;
+    wv[i] = one;
+    if (a.w && c < chunks) wv[i] = reinterpret_cast<const uint4*>(a.w)[c];
+  }
+  float ss[1] = {0.0f};
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    float f[8];
+    unpack8(xv[i], f);
+    if (RES) {
+      float g[8];
+      unpack8(rv[i], g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] += g[j];
+      xv[i] = pack8(f);   // the norm is that of the sum as it is kept
+      if (t + i * T < chunks) out_row(a.sum, row)[t + i * T] = xv[i];
+      unpack8(xv[i], f);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss[0] = __builtin_fmaf(f[j], f[j], ss[0]);
+  }
+  row_sum<T, 1>(ss, buf);
+  const float r = 1.0f / sqrtf(ss[0] * a.inv_dim + a.eps);
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    if (t + i * T >= chunks) continue;
+    float f[8], w[8];
+    unpack8(xv[i], f);
+    unpack8(wv[i], w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = f[j] * r * w[j];
+    out_row(a.y, row)[t + i * T] = pack8(f);
+  }
+}
+
+template <int T, int C, bool DH>
+__global__ __launch_bounds__(T < NT ? NT : T) void k_rms_norm_bwd(NormArgs a) {
+  constexpr int G = T < NT ? NT / T : 1;   // rows of a workgroup at a time
+  __shared__ float buf[2][T / 64 * 2];
+  const int t = threadIdx.x % T, chunks = a.dim >> 3;
+  const uint4 zero = make_uint4(0, 0, 0, 0), one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+  float acc[C][8];
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+  uint4 wv[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int c = t + i * T;
+    wv[i] = one;
+    if (a.w && c < chunks) wv[i] = reinterpret_cast<const uint4*>(a.w)[c];
+  }
+  const int64_t group = (int64_t)blockIdx.x * G + threadIdx.x / T, step = (int64_t)gridDim.x * G;
+  int turn = 0;
+  for (int64_t row = group; row < a.rows; row += step, turn ^= 1) {
+    uint4 gv[C], hv[C], dv[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int c = t + i * T;
+      const bool in = c < chunks;
+      gv[i] = in ? row_of(a.x, row)[c] : zero;
+      hv[i] = in ? row_of(a.res, row)[c] : zero;
+      if (DH) dv[i] = in ? row_of(a.dh, row)[c] : zero;
+    }
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float g[8], h[8], w[8];
+      unpack8(gv[i], g);
+      unpack8(hv[i], h);
+      unpack8(wv[i], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[0] = __builtin_fmaf(h[j], h[j], s[0]);
+        s[1] = __builtin_fmaf(g[j] * h[j], w[j], s[1]);
+      }
+    }
+    row_sum<T, 2>(s, buf[turn]);
+    const float r = 1.0f / sqrtf(s[0] * a.inv_dim + a.eps);
+    const float m = s[1] * a.inv_dim * r * r;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float g[8], h[8], w[8], d[8];
+      unpack8(gv[i], g);
+      unpack8(hv[i], h);
+      unpack8(wv[i], w);
+      if (DH) unpack8(dv[i], d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        acc[i][j] = __builtin_fmaf(g[j] * h[j], r, acc[i][j]);
+        const float v = __builtin_fmaf(-h[j], m, g[j] * w[j]);
+        g[j] = DH ? __builtin_fmaf(r, v, d[j]) : r * v;
+      }
+      if (t + i * T < chunks) out_row(a.y, row)[t + i * T] = pack8(g);
+    }
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int c = t + i * T;
+    if (c >= chunks) continue;
+    float* const p = a.part + group * a.dim + c * 8;
+    *reinterpret_cast<f32x4*>(p) = f32x4{acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{acc[i][4], acc[i][5], acc[i][6], acc[i][7]};
+  }
+}
+
+// dw[c] = sum over n partials [n][dim]: 32 columns per workgroup (128 B of a partial), 32 threads per column.
+constexpr int WT = 1024, WC = 32, WR = WT / WC, WL = 8;
+__global__ __launch_bounds__(WT) void k_norm_weight_grad(const float* __restrict__ part, int n, int dim, float* __restrict__ dw) {
+  __shared__ float sum[WR][WC + 1];
+  const int c = threadIdx.x % WC, r = threadIdx.x / WC, col = blockIdx.x * WC + c;
+  const int cc = col < dim ? col : dim - 1;
+  float s = 0.0f;
+  for (int i0 = r; i0 < n; i0 += WR * WL) {
+    float v[WL];
+#pragma unroll
+    for (int j = 0; j < WL; ++j) {
+      const int i = i0 + j * WR;
+      v[j] = i < n ? part[(int64_t)i * dim + cc] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < WL; ++j) s += v[j];
+  }
+  sum[r][c] = s;
+  __syncthreads();
+  if (r == 0 && col < dim) {
+#pragma unroll
+    for (int j = 1; j < WR; ++j) s += sum[j][c];
+    dw[col] = s;
+  }
+}
+
+// threads and loads of a row
+struct Shape {
+  int t, c;
+};
+Shape shape_of(int32_t dim) {
+  const int chunks = dim / 8;
+  if (chunks <= 64) return {64, 1};
+  if (chunks <= 128) return {64, 2};
+  if (chunks <= 256) return {64, 4};
+  if (chunks <= 512) return {256, 2};
+  if (chunks <= 1024) return {256, 4};
+  if (chunks <= 2048) return {1024, 2};
+  return {1024, 4};
+}
+
+int64_t bwd_groups(int64_t rows, const Shape& s) {
+  const int per = s.t < NT ? NT / s.t : 1;
+  const int64_t wgs = (rows + per - 1) / per, most = s.t == 1024 ? 256 : 512;
+  return (wgs < most ? wgs : most) * per;
+}
+
+}  // namespace
+
+// K<threads, loads, flag> launched for the run-time shape
+#define NORM_LAUNCH(K, sh, flag, grid, ...)                                                             \
+  do {                                                                                                   \
+    const dim3 g_((unsigned)(grid)), b_((unsigned)(sh.t < NT ? NT : sh.t));                              \
+    if (flag) {                                                                                          \
+      if (sh.t == 64 && sh.c == 1) hipLaunchKernelGGL((K<64, 1, true>), g_, b_, 0, s, __VA_ARGS__);      \
+      else if (sh.t == 64 && sh.c == 2) hipLaunchKernelGGL((K<64, 2, true>), g_, b_, 0, s, __VA_ARGS__); \
+      else if (sh.t == 64) hipLaunchKernelGGL((K<64, 4, true>), g_, b_, 0, s, __VA_ARGS__);              \
+      else if (sh.t == 256 && sh.c == 2) hipLaunchKernelGGL((K<256, 2, true>), g_, b_, 0, s, __VA_ARGS__); \
+      else if (sh.t == 256) hipLaunchKernelGGL((K<256, 4, true>), g_, b_, 0, s, __VA_ARGS__);            \
+      else if (sh.c == 2) hipLaunchKernelGGL((K<1024, 2, true>), g_, b_, 0, s, __VA_ARGS__);             \
+      else hipLaunchKernelGGL((K<1024, 4, true>), g_, b_, 0, s, __VA_ARGS__);                            \
+    } else {                                                                                             \
+      if (sh.t == 64 && sh.c == 1) hipLaunchKernelGGL((K<64, 1, false>), g_, b_, 0, s, __VA_ARGS__);     \
+      else if (sh.t == 64 && sh.c == 2) hipLaunchKernelGGL((K<64, 2, false>), g_, b_, 0, s, __VA_ARGS__); \
+      else if (sh.t == 64) hipLaunchKernelGGL((K<64, 4, false>), g_, b_, 0, s, __VA_ARGS__);             \
+      else if (sh.t == 256 && sh.c == 2) hipLaunchKernelGGL((K<256, 2, false>), g_, b_, 0, s, __VA_ARGS__); \
+      else if (sh.t == 256) hipLaunchKernelGGL((K<256, 4, false>), g_, b_, 0, s, __VA_ARGS__);           \
+      else if (sh.c == 2) hipLaunchKernelGGL((K<1024, 2, false>), g_, b_, 0, s, __VA_ARGS__);            \
+      else hipLaunchKernelGGL((K<1024, 4, false>), g_, b_, 0, s, __VA_ARGS__);                           \
+    }                                                                                                    \
+  } while (0)
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
+  const Shape sh = shape_of(a.dim);
+  const int per = sh.t < NT ? NT / sh.t : 1;
+  ProfScope ps("k_rms_norm", s);
+  NORM_LAUNCH(k_rms_norm, sh, a.res.data != nullptr, (a.rows + per - 1) / per, a);
+  return hipGetLastError();
+}
+
+size_t norm_part_floats(int64_t rows, int32_t dim) { return (size_t)bwd_groups(rows, shape_of(dim)) * dim; }
+
+hipError_t launch_rms_norm_bwd(const NormArgs& a, float* dw, hipStream_t s) {
+  const Shape sh = shape_of(a.dim);
+  const int per = sh.t < NT ? NT / sh.t : 1;
+  const int64_t groups = bwd_groups(a.rows, sh);
+  {
+    ProfScope ps("k_rms_norm_bwd", s);
+    NORM_LAUNCH(k_rms_norm_bwd, sh, a.dh.data != nullptr, groups / per, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (!a.part) return hipSuccess;
+  ProfScope ps("k_norm_weight_grad", s);
+  hipLaunchKernelGGL(k_norm_weight_grad, dim3((unsigned)((a.dim + WC - 1) / WC)), dim3(WT), 0, s, a.part, (int)groups, a.dim, dw);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

@@ -1,0 +1,81 @@
+// Internal launch interface of the operators on whole rows: the residual norm and the log
+// probabilities.  Launchers validate nothing: rows_api.cpp has already.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.h"
+#include "qlora.h"
+
+namespace qlora {
+
+// bf16 [rows][dim], rows `stride` elements apart
+struct RowsView {
+  uint16_t* data;
+  int64_t stride;
+};
+
+// ---- residual addition and norm (rms_norm.hip) ------------------------------------------------
+struct NormArgs {
+  RowsView x, res;    // forward: input and residual (or none); backward: dy and the forward's sum
+  RowsView dh;        // backward: gradient of the sum besides (or none)
+  RowsView y, sum;    // forward: outputs; backward: dx in y
+  const uint16_t* w;  // or NULL
+  int64_t rows;
+  int32_t dim;
+  float eps, inv_dim;
+  float* part;        // backward: partial weight gradients [groups][dim], or NULL
+};
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s);
+// grows with the rows
+size_t norm_part_floats(int64_t rows, int32_t dim);
+hipError_t launch_rms_norm_bwd(const NormArgs& a, float* dw, hipStream_t s);
+
+// ---- log probabilities of given tokens (logprob.hip) --------------------------------------------
+constexpr int kLpMaxTop = 32;
+constexpr int kLpMaxSegs = 32;       // parts of a row at most
+constexpr int64_t kLpMaxVocab = int64_t(1) << 20;
+// One part of a row: largest scaled logit, sum of exponentials from it, sum of exponential times logit from it.
+struct LpPart {
+  float m, z, s;
+  uint32_t pad_;
+};
+struct LpArgs {
+  const void* x;              // bf16 or fp32 [rows][vocab]
+  int64_t stride;             // elements between rows
+  int64_t rows;
+  int32_t vocab;
+  int32_t fp32;
+  float scale;
+  int32_t top;
+  const int64_t* token;       // or NULL
+  float* logprob;             // or NULL
+  float* stats;               // [rows][2]
+  float* entropy;             // or NULL
+  float* top_lp;              // [rows][top]
+  int64_t* top_index;
+  LpPart* part;               // several parts: [rows][segs]
+  unsigned long long* cand;   // and [rows][segs][top] candidates (order, then index)
+  int32_t segs;
+};
+int lp_segments(int64_t rows, int64_t vocab, bool fp32);
+hipError_t launch_logprob(const LpArgs& a, hipStream_t s);
+
+struct LpBwdArgs {
+  const void* x;
+  void* dx;
+  int64_t stride, dx_stride;
+  int64_t rows;
+  int32_t vocab;
+  int32_t fp32;
+  float scale;
+  const int64_t* token;
+  const float* stats;
+  const float* dlp;       // or NULL
+  const float* entropy;   // with dent
+  const float* dent;      // or NULL
+};
+hipError_t launch_logprob_bwd(const LpBwdArgs& a, hipStream_t s);
+
+}  // namespace qlora

@@ -396,6 +396,95 @@ qlora_status qlora_kv_attn(const qlora_heads* q, int64_t rows, const qlora_kv_ca
                            const qlora_kv_batch* batch, float scale, int32_t causal, int32_t window,
                            const qlora_heads* o, float* lse, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Around the projections: the residual's norm, the gated feed-forward block, and the log
+ * probabilities at the model's end, each with its backward.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Residual addition and root-mean-square norm of rows [rows][dim] of bf16, `*_stride` elements apart:
+ *   h = bf16(x + residual)  (h = x without one),   y = bf16(h w / sqrt(mean(h^2) + eps))
+ * in fp32 (so the mean of a row with elements from 2^60 on can be infinite, which gives zeros); h is written to `sum`
+ * where there is a residual (both or neither), w is 1 where the weight is NULL.  y or sum may be x or residual (same
+ * data and stride), not each other; no other overlap.
+ * Requires: 8 <= dim <= 32768, dim % 8 == 0; strides multiples of 8, 0 .. 2^36 - 1, at least dim for outputs (of one row:
+ * anything); pointers 16-byte aligned; weight bf16 [dim]; eps >= 0 and finite (with 0, a row of zeros gives NaN); 0 <= rows < 2^22.
+ * rows = 0 is a no-op.                                                                                   */
+qlora_status qlora_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual, int64_t residual_stride,
+                            int64_t rows, int32_t dim, const uint16_t* weight, float eps, uint16_t* y, int64_t y_stride,
+                            uint16_t* sum, int64_t sum_stride, hipStream_t stream);
+
+/* Its backward, from the gradient of y, the forward's h and, where h goes on beside the norm (a residual stream), its
+ * gradient dh (or NULL):
+ *   r = 1 / sqrt(mean(h^2) + eps),   dx = bf16(dh + r (w dy - h r^2 mean(w dy h))),   dweight = sum over rows of dy h r
+ * dx is the gradient of x and of the residual alike.  dweight: fp32 [dim], overwritten, summed in a fixed order; NULL
+ * where it is not wanted (then ws may be NULL too).  dx may be dy, h or dh (same data and stride).  With rows = 0
+ * dweight is set to zero.  ws of qlora_rms_norm_bwd_workspace bytes, 16-byte aligned (it grows with the rows, so that of the
+ * largest call of a dim serves smaller ones).                                                             */
+size_t qlora_rms_norm_bwd_workspace(int64_t rows, int32_t dim);
+qlora_status qlora_rms_norm_bwd(const uint16_t* dy, int64_t dy_stride, const uint16_t* h, int64_t h_stride,
+                                const uint16_t* dh, int64_t dh_stride, int64_t rows, int32_t dim, const uint16_t* weight,
+                                float eps, uint16_t* dx, int64_t dx_stride, float* dweight, void* ws, size_t ws_bytes,
+                                hipStream_t stream);
+
+/* Activations of the gated block: g / (1 + e^-g), and g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2. */
+typedef enum { QLORA_ACT_SILU = 0, QLORA_ACT_GELU = 1 } qlora_activation;
+
+/* The gated feed-forward block in front of its last projection, on two quantized weights [out][in] with adapters:
+ *   G = X deq(gate)^T + scale (X A_gate) B_gate,   U = X deq(up)^T + scale (X A_up) B_up,   H = bf16(act(G) U)
+ * in one launch of products (the tokens are read once for both weights; G and U stay in registers, fp32).  For the backward
+ * bf16 of G and U [M][out] (both or neither) and of T = X A of each [M][r] (both or neither) are written where their pointers
+ * are not NULL.  M = 0 is a no-op.
+ * Requires: what qlora_linear_fwd does of X, H, each weight and its adapters; both weights of one shape and format
+ * (UNSUPPORTED otherwise); adapters of one rank; ws of qlora_gated_workspace(M, in, out, r) bytes.           */
+size_t qlora_gated_workspace(int64_t M, int64_t in_features, int64_t out_features, int32_t r);
+qlora_status qlora_gated_fwd(const uint16_t* X, int64_t M, const qlora_nf4* gate, const qlora_nf4* up,
+                             const uint16_t* A_gate, const uint16_t* B_gate, const uint16_t* A_up, const uint16_t* B_up,
+                             int32_t r, float scale, int32_t activation, uint16_t* H, uint16_t* G, uint16_t* U,
+                             uint16_t* T_gate, uint16_t* T_up, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Backward of its activation and product, from the gradient of H and the saved G, U [M][out] (finite):
+ *   dG = bf16(dH U act'(G)),   dU = bf16(dH act(G)),   H = bf16(act(G) U) again where H is not NULL
+ * (so that the forward's H, the input of the next projection, need not be kept).  qlora_linear_bwd of each projection
+ * goes on from dG and dU.  Outputs may be the inputs, one each; no other overlap.
+ * Requires: out_features % 8 == 0, 8 .. 2^22; 0 <= M < 2^26; pointers 16-byte aligned.  M = 0 is a no-op.      */
+qlora_status qlora_gated_bwd(const uint16_t* dH, const uint16_t* G, const uint16_t* U, int64_t M, int64_t out_features,
+                             int32_t activation, uint16_t* dG, uint16_t* dU, uint16_t* H, hipStream_t stream);
+
+/* Element types of the logits. */
+typedef enum { QLORA_BF16 = 0, QLORA_FP32 = 1 } qlora_dtype;
+
+/* Log probabilities of given tokens under the softmax of scale * logits (scale = 1 / temperature), per row of logits
+ * [rows][vocab] of `dtype`, `stride` elements apart.  With x = fl32(scale logit), m the largest of the row and
+ * z = sum of e^(x - m):
+ *   logprob[row] = x_token - m - ln z       (0 where token < 0: a row without one; NaN where token >= vocab)
+ *   stats[row]   = (m, z)                   (ln sum e^x is m + ln z; the backward reads them)
+ *   entropy[row] = -sum p ln p              (or entropy = NULL)
+ *   top_logprob, top_index [row][top]: the `top` most likely tokens and their log probabilities, in descending order; equal
+ *   logits by the lower index, NaN before all.
+ * logprob may be NULL (then token may be too).  Logits of -infinity have probability 0.  A row of nothing else has
+ * m = -infinity, z = 0, logprob and top_logprob -infinity, entropy 0.  A NaN or +infinity makes its row's logprob and
+ * entropy NaN.  fp32 throughout; the same call gives the same bits.
+ * Requires: 1 <= vocab <= 2^20, 0 <= rows < 2^22, rows * vocab < 2^35; any stride from 0 to 2^36 - 1 and pointers aligned to their elements (rows may
+ * start anywhere); 0 <= top <= 32, top <= vocab; scale finite and > 0; ws of qlora_token_logprob_workspace bytes, 16-byte
+ * aligned (it grows with rows, vocab and top, so that of the largest call serves smaller ones; 0 for sizes that are
+ * refused).  rows = 0 is a no-op.                                                                        */
+size_t qlora_token_logprob_workspace(int64_t rows, int64_t vocab, int32_t top);
+qlora_status qlora_token_logprob(const void* logits, int64_t stride, int64_t rows, int64_t vocab, int32_t dtype,
+                                 const int64_t* token, float scale, int32_t top, float* logprob, float* stats,
+                                 float* entropy, float* top_logprob, int64_t* top_index, void* ws, size_t ws_bytes,
+                                 hipStream_t stream);
+
+/* Its backward: from the gradients of logprob and of entropy (fp32 [rows], either may be NULL, not both), the forward's
+ * stats and, with dentropy, its entropy:
+ *   dlogits[row][v] = scale (dlogprob (1[v = token] - p_v) - dentropy p_v (ln p_v + entropy)),   p_v = e^(x_v - m) / z
+ * in the logits' type.  A row with token < 0 has no gradient from dlogprob, one with token >= vocab is NaN; a row without a
+ * logit above -infinity has gradient 0.  dlogits may be the logits (same data and stride); no other overlap.
+ * Requires: as the forward; dlogits_stride >= vocab.                                                     */
+qlora_status qlora_token_logprob_bwd(const void* logits, int64_t stride, int64_t rows, int64_t vocab, int32_t dtype,
+                                     const int64_t* token, float scale, const float* stats, const float* dlogprob,
+                                     const float* entropy, const float* dentropy, void* dlogits, int64_t dlogits_stride,
+                                     hipStream_t stream);
+
 /* Optional per-kernel timing, for benchmarking.  While enabled, every kernel
  * launch of this library is bracketed by HIP events on its stream.
  * qlora_profile_read synchronizes those events and returns, per kernel name,

@@ -1,0 +1,206 @@
+"""GPU parity of the gated block with the float64 oracle on the bit-exact dequantized weights.
+
+Tolerances, from the arithmetic.  G (and U): products of bf16 are exact in fp32 and K of them are added in some order, at
+most K 2^-24 of the sum of magnitudes off; s T is rounded to bf16 before its product with B (2^-8 of each, from a T
+that is itself K 2^-24 off, and r more additions).  Then one rounding to bf16 (2^-8).  H = act(G) U of the unrounded two: the
+activations have slopes below 1.13, and one exponential of an argument below 2^7 in fp32 is 2^-16 off at most, the rest of the
+fp32 arithmetic below 2^-20: 2^-15 of the value in all, and one rounding.  Backward: the same of act and of its
+slope s + g s (1 - s) x'(g), where 1 - s is off by 2^-24 and |g x'| is below 2^5 wherever s is not 1."""
+import numpy as np
+import pytest
+import torch
+
+import bit_nf4_quantized_11_amd as Q
+from helpers import dev_bf16, host, log, require_gpu
+from kv_cases import bits
+from oracle import rows as oracle
+
+pytestmark = pytest.mark.gpu
+
+BF16, ACT, E24 = 2.0 ** -8, 2.0 ** -15, 2.0 ** -24
+TINY = 2.0 ** -126   # (values below it are zeros)
+
+# M, in, out, r, activation, codebook, block, double quantization: the three forms (up to 64 tokens; K-slices; whole
+# tiles) with partial tiles, several token groups, odd feature counts and ranks
+CASES = [
+    (1, 64, 8, 8, "silu", "nf4", 64, True),
+    (1, 4096, 136, 16, "silu", "nf4", 64, True),
+    (7, 512, 264, 64, "gelu", "fp4", 32, False),
+    (16, 2112, 1000, 72, "silu", "int4", 64, True),
+    (17, 256, 520, 136, "gelu", "nf4", 128, True),
+    (33, 1024, 88, 256, "silu", "nf4", 256, False),
+    (64, 2048, 648, 24, "silu", "fp4", 32, True),
+    (65, 64, 8, 8, "gelu", "nf4", 64, True),
+    (100, 1024, 200, 200, "silu", "nf4", 128, False),
+    (200, 2048, 2000, 64, "gelu", "int4", 32, True),
+    (257, 512, 72, 8, "silu", "nf4", 64, False),
+    (300, 192, 1096, 80, "silu", "fp4", 64, True),
+    (513, 4096, 72, 64, "silu", "nf4", 256, True),
+    (1025, 128, 328, 264 - 8, "gelu", "nf4", 32, False),
+    (1100, 320, 1288, 40, "silu", "nf4", 64, True),
+]
+
+
+def f64(t):
+    return host(t.float()).astype(np.float64)
+
+
+def _make(case, seed=0):
+    M, K, N, r, act, book, block, dq = case
+    X = dev_bf16(bits(seed + 1, (M, K)))
+    w = [Q.qlora_quantize_nf4(dev_bf16(bits(seed + 2 + i, (N, K), 0.02)), dq, codebook=Q.CODEBOOKS[book], block=block)
+         for i in range(2)]
+    A = [dev_bf16(bits(seed + 4 + i, (K, r), 0.05)) for i in range(2)]
+    B = [dev_bf16(bits(seed + 6 + i, (r, N), 0.05)) for i in range(2)]
+    return X, w, A, B
+
+
+def _run(X, w, A, B, scale, act, **kw):
+    return Q.qlora_gated_fwd(X, w[0], w[1], A[0], B[0], A[1], B[1], scale, act, **kw)
+
+
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_forward(case):
+    require_gpu()
+    log("gated", case)
+    M, K, N, r, act, book, block, dq = case
+    scale = 16 / r
+    X, w, A, B = _make(case)
+    H, G, U, Tg, Tu = _run(X, w, A, B, scale, act)
+    x = f64(X)
+    sums, tols = [], []
+    for i, (got, gotT) in enumerate(((G, Tg), (U, Tu))):
+        W, a, b = f64(Q.qlora_dequant(w[i])), f64(A[i]), f64(B[i])
+        T = x @ a
+        magT = np.abs(x) @ np.abs(a)
+        assert np.all(np.abs(f64(gotT) - T) <= BF16 * np.abs(T) + 1.01 * K * E24 * magT), i
+        s32 = float(np.float32(scale))
+        want = x @ W.T + s32 * T @ b
+        dT = 1.01 * (BF16 * np.abs(s32 * T) + K * E24 * s32 * magT)
+        mag = np.abs(x) @ np.abs(W).T + s32 * np.abs(T) @ np.abs(b)
+        tol = 1.01 * (K + r + 16) * E24 * mag + dT @ np.abs(b)
+        assert np.all(np.abs(f64(got) - want) <= (BF16 * 1.01) * (np.abs(want) + tol) + tol), i
+        sums.append(want)
+        tols.append(tol)
+    g, u = sums
+    a, _ = oracle.activation(g, act)
+    want = a * u
+    tol = 1.13 * tols[0] * (np.abs(u) + tols[1]) + np.abs(a) * tols[1] + ACT * np.abs(want)
+    assert np.all(np.abs(f64(H) - want) <= BF16 * 1.01 * (np.abs(want) + tol) + tol + TINY)
+    # without what the backward needs: the same H; and the same bits again
+    alone = _run(X, w, A, B, scale, act, save=False)
+    assert torch.equal(alone[0], H) and all(t is None for t in alone[1:])
+    assert all(torch.equal(a, b) for a, b in zip(_run(X, w, A, B, scale, act), (H, G, U, Tg, Tu)))
+
+
+def test_forward_agrees_with_two_linear_calls():
+    """G and T are those of qlora_linear_fwd on the same weight, up to the order of sums (both within the tolerance of the
+    module's head): here, at rank 64, bit for bit in T and within two roundings in G."""
+    require_gpu()
+    for M in (4, 40, 150, 700):
+        X, w, A, B = _make((M, 1024, 512, 64, "silu", "nf4", 64, True), 50)
+        _, G, U, Tg, Tu = _run(X, w, A, B, 0.25, "silu")
+        for i, (got, T) in enumerate(((G, Tg), (U, Tu))):
+            Y, t = Q.qlora_linear_fwd(X, w[i], A[i], B[i], 0.25)
+            assert (t.float() - T.float()).abs().max() <= 2.0 ** -7 * T.float().abs().max()
+            tol = 2 * BF16 * Y.float().abs() + 2 * 1024 * E24 * (X.float().abs() @ Q.qlora_dequant(w[i]).float().abs().t()) + 2.0 ** -7
+            assert torch.all((Y.float() - got.float()).abs() <= tol)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("shape", [(1, 8), (3, 40), (65, 1000), (2048, 264)], ids=str)
+def test_backward(act, shape):
+    require_gpu()
+    log("gated_bwd", act, shape)
+    dH, G, U = dev_bf16(bits(1, shape)), dev_bf16(bits(2, shape, 3.0)), dev_bf16(bits(3, shape, 2.0))
+    flat = G.view(-1)
+    edge = torch.tensor([0.0, -0.0, 90.0, -90.0, 1e4, -1e4, 1e19, -1e19], device="cuda").bfloat16()
+    flat[:8] = edge
+    dG, dU, H = Q.qlora_gated_bwd(dH, G, U, act, H=True)
+    g, u, d = f64(G), f64(U), f64(dH)
+    with np.errstate(over="ignore", invalid="ignore"):
+        a, slope = oracle.activation(g, act)
+        # (at the edges: the value g or 0, the slope 1 or 0)
+        far = np.abs(g) > 80
+        a, slope = np.where(far, np.maximum(g, 0), a), np.where(far, (g > 0) * 1.0, slope)
+        near = np.where(far, 0, np.abs(g))
+        x1 = 1.0 if act == "silu" else 2 * 0.7978845608 * (1 + 3 * 0.044715 * near * near)
+        arg = near if act == "silu" else 2 * 0.7978845608 * (near + 0.044715 * near ** 3)
+        s = 1 / (1 + np.exp(-np.sign(g) * np.minimum(arg, 600)))
+        mag = s + near * s * (1 - s) * x1
+    tol = ACT * mag + 2.0 ** -19
+    assert np.all(np.abs(f64(dG) - d * u * slope) <= np.abs(d * u) * (BF16 * 1.01 * (np.abs(slope) + tol) + tol) + TINY)
+    low = 2.0 ** -120 * np.abs(d)   # (an activation below the smallest normal number)
+    assert np.all(np.abs(f64(dU) - d * a) <= (BF16 * 1.01 + ACT) * np.abs(d * a) + low + TINY)
+    assert np.all(np.abs(f64(H) - a * u) <= (BF16 * 1.01 + ACT) * np.abs(a * u) + 2.0 ** -120 * np.abs(u) + TINY)
+    none = Q.qlora_gated_bwd(dH, G, U, act)
+    assert none[2] is None and torch.equal(none[0], dG) and torch.equal(none[1], dU)
+    # written over the inputs
+    for order in (("G", "U", "dH"), ("dH", "G", "U"), ("U", "dH", "G")):
+        t = {"dH": dH.clone(), "G": G.clone(), "U": U.clone()}
+        got = Q.qlora_gated_bwd(t["dH"], t["G"], t["U"], act, dG=t[order[0]], dU=t[order[1]], H=t[order[2]])
+        assert all(torch.equal(x, y) for x, y in zip(got, (dG, dU, H)))
+
+
+def test_empty_captured_and_other_streams():
+    require_gpu()
+    case = (40, 512, 264, 16, "silu", "nf4", 64, True)
+    X, w, A, B = _make(case, 20)
+    empty = _run(X[:0], w, A, B, 1.0, "silu")
+    assert [tuple(t.shape) for t in empty] == [(0, 264)] * 3 + [(0, 16)] * 2
+    assert Q.qlora_gated_bwd(empty[0], empty[1], empty[2], H=True)[2].shape == (0, 264)
+    for M in (5, 150, 1200):   # the three forms
+        X = dev_bf16(bits(30, (M, 512)))
+        dH = dev_bf16(bits(31, (M, 264)))
+        ws = torch.empty(Q.qlora_gated_workspace(M, 512, 264, 16), dtype=torch.uint8, device="cuda")
+
+        def run():
+            out = _run(X, w, A, B, 0.5, "gelu", workspace=ws)
+            return (*out, *Q.qlora_gated_bwd(dH, out[1], out[2], "gelu", H=True))
+
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            captured = run()
+        for k in (1, 2, 3):
+            X.copy_(dev_bf16(bits(40 + k, X.shape)))
+            dH.copy_(dev_bf16(bits(50 + k, dH.shape)))
+            eager = [t.clone() for t in run()]
+            ws.fill_(0xFF)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(captured, eager)), M
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        other = _run(X, w, A, B, 0.5, "gelu", stream=side)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(other, eager))
+
+
+def test_binding_refusals():
+    require_gpu()
+    case = (4, 128, 64, 8, "silu", "nf4", 64, True)
+    X, w, A, B = _make(case)
+    other = Q.qlora_quantize_nf4(dev_bf16(bits(1, (64, 128))), False)
+    wide = Q.qlora_quantize_nf4(dev_bf16(bits(1, (72, 128))), True)
+    for bad in (X.float(), X.cpu(), X[:, :64], X[0], X[:, ::2], X.t().contiguous().t()):
+        with pytest.raises(Q.QLoRAError):
+            _run(bad, w, A, B, 1.0, "silu")
+    for ww in ([w[0], other], [w[0], wide], [wide, w[1]]):
+        with pytest.raises(Q.QLoRAError):
+            _run(X, ww, A, B, 1.0, "silu")
+    for i, bad in ((0, A[0][:, :4]), (1, A[1].float()), (1, A[1].cpu()), (0, A[0][:64]), (1, dev_bf16(bits(1, (128, 16))))):
+        with pytest.raises(Q.QLoRAError):
+            _run(X, w, [bad, A[1]] if i == 0 else [A[0], bad], B, 1.0, "silu")
+    for kw in ({"act": "relu"}, {"H": X}, {"workspace": torch.empty(64, dtype=torch.uint8, device="cuda")},
+               {"workspace": torch.empty(1 << 20, dtype=torch.uint8)}):
+        with pytest.raises(Q.QLoRAError):
+            _run(X, w, A, B, 1.0, kw.pop("act", "silu"), **kw)
+    d = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    for args in ((d.float(), d, d), (d, d[:3], d), (d, d, d.cpu()), (d[0], d[0], d[0]), (d[:, :60], d[:, :60], d[:, :60])):
+        with pytest.raises(Q.QLoRAError):
+            Q.qlora_gated_bwd(*args)
+    for kw in ({"activation": "tanh"}, {"dG": d, "dU": d}, {"H": d, "dU": d}, {"dG": d.float()}):
+        with pytest.raises(Q.QLoRAError):
+            Q.qlora_gated_bwd(d, d.clone(), d.clone(), **kw)
