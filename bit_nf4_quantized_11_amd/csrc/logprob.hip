@@ -19,8 +19,6 @@ namespace qlora {
 
 namespace {
 
-constexpr int NT = 512;       // threads of a part
-constexpr int NW = NT / 64;
 constexpr int CAP = 1024;     // candidates that the list holds
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -69,15 +67,32 @@ __device__ __forceinline__ uint4 load_any(const void* p) {
 }
 __device__ __forceinline__ void store_any(void* p, const uint4& v) { __builtin_memcpy(p, &v, 16); }
 
-// Elements col .. col + E - 1 of a row of n; -infinity behind its end.
+// Elements col .. col + E - 1 of a row of n, one by one; -infinity behind its end.
 template <bool F32>
-__device__ __forceinline__ uint4 load_chunk(const typename Elem<F32>::T* row, int col, int n) {
+__device__ __forceinline__ uint4 load_edge(const typename Elem<F32>::T* row, int col, int n) {
   typedef Elem<F32> X;
-  if (col + X::E <= n) return load_any(row + col);
   float f[X::E];
 #pragma unroll
   for (int j = 0; j < X::E; ++j) f[j] = col + j < n ? X::value(row + col + j) : -INFINITY;
   return X::pack(f);
+}
+template <bool F32>
+__device__ __forceinline__ uint4 load_piece(const typename Elem<F32>::T* row, int col, int n) {
+  if (col + Elem<F32>::E <= n) return load_any(row + col);
+  return load_edge<F32>(row, col, n);
+}
+// C such pieces, `step` elements apart.  All are loaded first, without a branch between the loads (behind the row's end,
+// its last piece); then those at the end again.
+template <bool F32, int C>
+__device__ __forceinline__ void load_pieces(uint4 (&v)[C], const typename Elem<F32>::T* row, int col, int step, int n) {
+  constexpr int E = Elem<F32>::E;
+  if (n >= E) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = load_any(row + min(col + i * step, n - E));
+  }
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+    if (col + i * step + E > n) v[i] = load_edge<F32>(row, col + i * step, n);
 }
 
 // Larger numbers for larger values; NaN above all, both zeros the same.  Never 0.
@@ -94,44 +109,35 @@ __device__ __forceinline__ float value_of(u64 e) {
 }
 __device__ __forceinline__ int col_of(u64 e) { return (int)(0xFFFFFFFFu - (uint32_t)e); }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int off = 32; off; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
-  return v;
-}
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
-}
+// The given token of a row and its logit, asked for early.
+template <bool F32>
+struct Given {
+  int64_t token;
+  float x;
+  __device__ Given(const LpArgs& a, int64_t row, int64_t token) : token(token), x(0.0f) {
+    typedef Elem<F32> X;
+    if (token >= 0 && token < a.vocab) x = X::value(static_cast<const typename X::T*>(a.x) + row * a.stride + token);
+  }
+};
 
-// What the forward leaves of a row, from its whole sums.
+// What the forward leaves of a row, from its whole sums (the largest logit, and the others for scaled ones).
 struct RowEnd {
   float m, logz;
   bool empty;   // no logit above -infinity
 };
 template <bool F32>
-__device__ __forceinline__ RowEnd finish_row(const LpArgs& a, int64_t row, float m, float z, float s, bool write) {
-  typedef Elem<F32> X;
+__device__ __forceinline__ RowEnd finish_row(const LpArgs& a, int64_t row, const Given<F32>& g, float top, float z, float s,
+                                             bool write) {
   RowEnd r;
-  r.m = m;
+  r.m = top * a.scale;
   r.empty = z == 0.0f;
   r.logz = logf(z);
   if (!write) return r;
-  a.stats[2 * row] = m;
+  a.stats[2 * row] = r.m;
   a.stats[2 * row + 1] = z;
-  if (a.entropy) a.entropy[row] = r.empty ? 0.0f : r.logz - s / z;
-  if (a.logprob) {
-    const int64_t t = a.token[row];
-    float lp = 0.0f;
-    if (t >= a.vocab) {
-      lp = NAN;
-    } else if (t >= 0) {
-      const float x = X::value(static_cast<const typename X::T*>(a.x) + row * a.stride + t) * a.scale;
-      lp = r.empty ? -INFINITY : (x - m) - r.logz;
-    }
-    a.logprob[row] = lp;
-  }
+  if (a.entropy) a.entropy[row] = r.empty ? 0.0f : r.logz - s * (a.scale / z);
+  if (a.logprob)
+    a.logprob[row] = g.token >= a.vocab ? NAN : g.token < 0 ? 0.0f : r.empty ? -INFINITY : (g.x * a.scale - r.m) - r.logz;
   return r;
 }
 __device__ __forceinline__ void write_top(const LpArgs& a, int64_t row, int rank, u64 e, const RowEnd& r) {
@@ -139,23 +145,75 @@ __device__ __forceinline__ void write_top(const LpArgs& a, int64_t row, int rank
   a.top_index[row * a.top + rank] = col_of(e);
 }
 
-// One part of one row.  C: 16-byte loads of a thread.
-template <bool F32, int C, bool TOP>
+// The k-th largest of a wave's lanes' orders, or a lower bound of it with the lower half zero.
+template <int LOW>
+__device__ __forceinline__ uint32_t kth_largest(uint32_t mine, int k) {
+  uint32_t b = 0;
+#pragma unroll
+  for (int bit = 31; bit >= LOW; --bit) {
+    const uint32_t next = b | 1u << bit;
+    if (__popcll(__ballot(mine >= next)) >= k) b = next;
+  }
+  return b;
+}
+
+// Where this lane's `mine` places begin in a list that all waves share.
+__device__ __forceinline__ int places(int mine, int* count) {
+  if (!__ballot(mine > 0)) return 0;
+  const int incl = wave_prefix(mine);
+  int base = 0;
+  if ((threadIdx.x & 63) == 63) base = atomicAdd(count, incl);
+  return __builtin_amdgcn_readlane(base, 63) + incl - mine;
+}
+
+// Each of the n entries of an LDS list with its rank, `out(rank, entry)`, for ranks below k; T threads, all of which call.
+// 8 neighbouring lanes share the comparisons of an entry, 8 of which are read at a time: the list ends in zeros
+// (kPad places behind n).
+constexpr int kLanes = 8, kPad = 8 * kLanes;
+template <int T, class F>
+__device__ __forceinline__ void rank_list(u64* list, int n, int k, F out) {
+  if (threadIdx.x < kPad) list[n + threadIdx.x] = 0;
+  __syncthreads();
+  const int sub = threadIdx.x & (kLanes - 1);
+  for (int i0 = 0; i0 < n; i0 += T / kLanes) {
+    const int i = i0 + threadIdx.x / kLanes;
+    const u64 e = list[min(i, n - 1)];
+    int rank = 0;
+    for (int j = sub; j < n; j += kPad) {
+      u64 o[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) o[u] = list[j + u * kLanes];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) rank += o[u] > e;
+    }
+    // the lanes' sum: neighbours, pairs, and the other half of 8
+    rank += (int)dpp_or<0xB1, 0xF>(0u, (uint32_t)rank);
+    rank += (int)dpp_or<0x4E, 0xF>(0u, (uint32_t)rank);
+    rank += (int)dpp_or<0x141, 0xF>(0u, (uint32_t)rank);
+    if (i < n && sub == 0 && rank < k) out(rank, e);
+  }
+}
+
+// One part of one row.  C: 16-byte loads of each of the NT threads.  Every wave sums from its own maximum, so that none waits for
+// another's loads; the waves' sums are joined at the end.
+template <bool F32, int C, bool TOP, int NT>
 __global__ __launch_bounds__(NT) void k_token_logprob(LpArgs a) {
   typedef Elem<F32> X;
-  constexpr int E = X::E;
+  constexpr int E = X::E, NW = NT / 64;
   __shared__ float red[3][NW];
-  __shared__ u64 list[TOP ? CAP : 1];
+  __shared__ u64 list[TOP ? CAP + kPad : 1];
   __shared__ uint32_t bound[NW];
   __shared__ int count;
+  const bool whole = a.segs == 1;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int64_t row = blockIdx.x / (unsigned)a.segs;
   const int seg = (int)(blockIdx.x - row * a.segs);
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const auto* const x = static_cast<const typename X::T*>(a.x) + row * a.stride;
   const int col0 = (seg * C * NT + t) * E;
+  const int64_t token = whole && a.logprob ? a.token[row] : -1;
+  const auto* const x = static_cast<const typename X::T*>(a.x) + row * a.stride;
   uint4 v[C];
-#pragma unroll
-  for (int i = 0; i < C; ++i) v[i] = load_chunk<F32>(x, col0 + i * NT * E, a.vocab);
+  load_pieces<F32, C>(v, x, col0, NT * E, a.vocab);
+  const Given<F32> given(a, row, token);
   float top = -INFINITY;   // (NaN are passed over)
 #pragma unroll
   for (int i = 0; i < C; ++i) {
@@ -164,28 +222,8 @@ __global__ __launch_bounds__(NT) void k_token_logprob(LpArgs a) {
 #pragma unroll
     for (int j = 0; j < E; ++j) top = fmaxf(top, f[j]);
   }
-  {
-    const float w = wave_max(top);
-    if (lane == 0) red[0][wave] = w;
-  }
-  if (TOP) {
-    // the wave's k-th largest lane maximum, by the upper half of its order (a lower bound is as good)
-    const uint32_t mine = order_of(top) >> 16;
-    uint32_t b = 0;
-#pragma unroll
-    for (int bit = 15; bit >= 0; --bit) {
-      const uint32_t next = b | 1u << bit;
-      if (__popcll(__ballot(mine >= next)) >= a.top) b = next;
-    }
-    if (lane == 0) bound[wave] = b << 16;
-    if (t == 0) count = 0;
-  }
-  __syncthreads();
-  float m = red[0][0];
-#pragma unroll
-  for (int w = 1; w < NW; ++w) m = fmaxf(m, red[0][w]);
-  m *= a.scale;
-  const float from = m == -INFINITY ? 0.0f : m;
+  const float mine_m = wave_max(top);
+  const float from = mine_m == -INFINITY ? 0.0f : mine_m, by = a.scale * kLog2e;
   float z = 0.0f, s = 0.0f;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
@@ -193,21 +231,40 @@ __global__ __launch_bounds__(NT) void k_token_logprob(LpArgs a) {
     X::unpack(v[i], f);
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      const float d = f[j] * a.scale - from;
-      const float e = __builtin_amdgcn_exp2f(d * kLog2e);
+      // (the difference of the logits first: no product of a large one can overflow, and equal ones give 0)
+      const float d = f[j] - from;
+      const float e = __builtin_amdgcn_exp2f(d * by);
       z += e;
       s = __builtin_fmaf(e, fmaxf(d, -1e30f), s);   // (nothing of a logit of -infinity)
     }
   }
   z = wave_sum(z);
   s = wave_sum(s);
-  if (lane == 0) red[1][wave] = z, red[2][wave] = s;
+  if (lane == 0) red[0][wave] = mine_m, red[1][wave] = z, red[2][wave] = s;
   if (TOP) {
+    // the wave's k-th largest lane maximum, by the upper half of its order (a lower bound is as good)
+    const uint32_t mine = kth_largest<16>(order_of(top), a.top);
+    if (lane == 0) bound[wave] = mine;
+    if (t == 0) count = 0;
+    __syncthreads();
     uint32_t b = bound[0];
 #pragma unroll
     for (int w = 1; w < NW; ++w) b = max(b, bound[w]);
-    const float least = b <= 0x007FFFFFu ? -INFINITY : value_of((u64)b << 32);
-    if (top >= least) {
+    // (where the bound is -infinity, everything would be listed, the places behind the row's end too)
+    const bool nothing = b <= 0x007FFFFFu;
+    const float least = nothing ? INFINITY : value_of((u64)b << 32);
+    int above = nothing ? (t == 0 ? CAP + 1 : 0) : 0;
+    if (top >= least && !nothing) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        float f[E];
+        X::unpack(v[i], f);
+#pragma unroll
+        for (int j = 0; j < E; ++j) above += f[j] >= least;
+      }
+    }
+    int at = places(above, &count);
+    if (above > 0 && at + above <= CAP) {
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         float f[E];
@@ -215,48 +272,98 @@ __global__ __launch_bounds__(NT) void k_token_logprob(LpArgs a) {
 #pragma unroll
         for (int j = 0; j < E; ++j) {
           const int col = col0 + i * NT * E + j;
-          if (f[j] >= least && col < a.vocab) {
-            const int n = atomicAdd(&count, 1);
-            if (n < CAP) list[n] = entry_of(f[j], col);
-          }
+          if (f[j] >= least) list[at++] = entry_of(f[j], col);
         }
       }
     }
   }
   __syncthreads();
-  z = red[1][0], s = red[2][0];
+  float m = red[0][0];
 #pragma unroll
-  for (int w = 1; w < NW; ++w) z += red[1][w], s += red[2][w];
-  const bool whole = a.segs == 1;
+  for (int w = 1; w < NW; ++w) m = fmaxf(m, red[0][w]);
+  z = s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const float mw = red[0][w], d = mw == -INFINITY ? 0.0f : mw - m, e = __builtin_amdgcn_exp2f(d * by);
+    z += e * red[1][w];
+    s += e * __builtin_fmaf(red[1][w], fmaxf(d, -1e30f), red[2][w]);
+  }
   RowEnd end{};
   if (whole) {
-    end = finish_row<F32>(a, row, m, z, s, t == 0);
+    end = finish_row<F32>(a, row, given, m, z, s, t == 0);
   } else if (t == 0) {
     a.part[row * a.segs + seg] = LpPart{m, z, s, 0};
   }
   if (!TOP) return;
   u64* const cand = whole ? nullptr : a.cand + (row * a.segs + seg) * a.top;
-  const int n = count;
-  if (n <= CAP && z == z) {
-    for (int i = t; i < n; i += NT) {
-      const u64 e = list[i];
-      int rank = 0;
-      for (int j = 0; j < n; ++j) rank += list[j] > e;
-      if (rank >= a.top) continue;
-      if (whole) write_top(a, row, rank, e, end);
-      else cand[rank] = e;
+  const auto put = [&](int rank, u64 e) {
+    if (whole) write_top(a, row, rank, e, end);
+    else cand[rank] = e;
+  };
+  int n = count;
+  if (n > CAP && z == z) {
+    // Many equal logits (or nearly so): the bound in full, all elements above it, and of those that equal it the first k
+    // of each wave.
+    const uint32_t mine = order_of(top), b = kth_largest<0>(mine, a.top);
+    __syncthreads();
+    if (lane == 0) bound[wave] = b;
+    if (t == 0) count = 0;
+    __syncthreads();
+    uint32_t order = bound[0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) order = max(order, bound[w]);
+    const float least = value_of((u64)order << 32);
+    // (read again, in loops that are not unrolled: these paths are to cost the common one no registers)
+    int above = 0;
+#pragma unroll 1
+    for (int i = 0; i < C; ++i) {
+      float f[E];
+      X::unpack(load_piece<F32>(x, col0 + i * NT * E, a.vocab), f);
+#pragma unroll
+      for (int j = 0; j < E; ++j) above += f[j] > least;
     }
+    int at = places(above, &count), have = 0;   // have: equal ones of this wave
+#pragma unroll 1
+    for (int i = 0; i < C; ++i) {
+      float f[E];
+      X::unpack(load_piece<F32>(x, col0 + i * NT * E, a.vocab), f);
+      const int col = col0 + i * NT * E;
+      uint32_t equal = 0;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        if (f[j] == least && col + j < a.vocab) equal |= 1u << j;
+        if (f[j] > least) {
+          if (at < CAP) list[at] = entry_of(f[j], col + j);
+          ++at;
+        }
+      }
+      if (have < a.top && __ballot(equal != 0)) {
+        const int incl = wave_prefix(__popc(equal)), total = __builtin_amdgcn_readlane(incl, 63);
+        const int before = have + incl - __popc(equal), mine = min(max(a.top - before, 0), __popc(equal));
+        int to = places(mine, &count);
+#pragma unroll
+        for (int j = 0, k = 0; j < E; ++j)
+          if (equal >> j & 1 && k++ < mine && to < CAP) list[to++] = (u64)order << 32 | (0xFFFFFFFFu - (uint32_t)(col + j));
+        have += total;
+      }
+    }
+    __syncthreads();
+    n = count;
+  }
+  if (n <= CAP && z == z) {
+    rank_list<NT>(list, n, a.top, put);
     if (!whole)
       for (int i = n + t; i < a.top; i += NT) cand[i] = 0;
     return;
   }
+  // k rounds of a maximum
   u64 last = ~0ull;
   for (int k = 0; k < a.top; ++k) {
     u64 best = 0;
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < C; ++i) {
       float f[E];
-      X::unpack(v[i], f);
+      X::unpack(load_piece<F32>(x, col0 + i * NT * E, a.vocab), f);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const int col = col0 + i * NT * E + j;
@@ -274,47 +381,55 @@ __global__ __launch_bounds__(NT) void k_token_logprob(LpArgs a) {
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < NW; ++w) best = list[w] > best ? list[w] : best;
-    if (t == 0) {
-      if (!whole) cand[k] = best;
-      else write_top(a, row, k, best, end);   // (a whole row has k elements)
-    }
-    last = best;   // 0 where the part has no more: then nothing is below it
+    if (t == 0) put(k, best);   // 0 where the part has no more (a whole row has k elements); then nothing is below it
+    last = best;
   }
 }
 
-// The parts of a row joined: one workgroup per row.
-constexpr int JT = 256;
+// The parts of a row joined by a wave, a part to a lane.  The parts' candidates are in descending order each, so the
+// largest of all is the largest of their first ones; parts ascend with the tokens, so of equal ones it is the first
+// lane's.  JW waves to a workgroup, which share nothing.
+constexpr int JW = 4;
 template <bool F32, bool TOP>
-__global__ __launch_bounds__(JT) void k_logprob_join(LpArgs a) {
-  __shared__ u64 list[TOP ? kLpMaxSegs * kLpMaxTop : 1];
-  const int64_t row = blockIdx.x;
-  const int t = threadIdx.x, lane = t & 63;
-  // every wave joins the sums (a part to a lane)
+__global__ __launch_bounds__(64 * JW) void k_logprob_join(LpArgs a) {
+  extern __shared__ u64 lists[];   // [JW][segs][top]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row = (int64_t)blockIdx.x * JW + wave;
+  if (row >= a.rows) return;
+  const Given<F32> given(a, row, a.logprob ? a.token[row] : -1);
+  const int n = a.segs * a.top;
+  u64* const list = lists + wave * n;
+  if (TOP)
+    for (int i = lane; i < n; i += 64) list[i] = a.cand[row * n + i];
   float m = -INFINITY, z = 0.0f, s = 0.0f;
   if (lane < a.segs) {
     const LpPart p = a.part[row * a.segs + lane];
     m = p.m, z = p.z, s = p.s;
   }
-  const int n = a.segs * a.top;
-  if (TOP)
-    for (int i = t; i < n; i += JT) list[i] = a.cand[row * n + i];
   const float mm = wave_max(m);
   const float d = m == -INFINITY ? 0.0f : m - mm;
-  const float e = __builtin_amdgcn_exp2f(d * kLog2e);
-  s = e * __builtin_fmaf(z, d, s);
-  z = e * z;
-  z = wave_sum(z);
+  const float e = __builtin_amdgcn_exp2f(d * (a.scale * kLog2e));
+  s = e * __builtin_fmaf(z, fmaxf(d, -1e30f), s);
+  z = wave_sum(e * z);
   s = wave_sum(s);
-  const RowEnd end = finish_row<F32>(a, row, mm, z, s, t == 0);
+  const RowEnd end = finish_row<F32>(a, row, given, mm, z, s, lane == 0);
   if (!TOP) return;
-  __syncthreads();
-  for (int i = t; i < n; i += JT) {
-    const u64 x = list[i];
-    if (x == 0) continue;
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += list[j] > x;
-    if (rank < a.top) write_top(a, row, rank, x, end);
+  // (written and read by one wave, whose LDS accesses keep their order) a lane's first candidate, and its next one loaded ahead; 0 where there are none
+  const int stop = lane < a.segs ? (lane + 1) * a.top : 0;
+  int at = lane * a.top;
+  u64 head = at < stop ? list[at] : 0, next = at + 1 < stop ? list[at + 1] : 0, kept = 0;
+  for (int k = 0; k < a.top; ++k) {
+    const uint32_t mine = (uint32_t)(head >> 32), best = wave_max(mine);
+    const int from = __ffsll(__ballot(mine == best)) - 1;
+    const uint32_t low = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)head, from);
+    if (lane == k) kept = (u64)best << 32 | low;
+    if (lane == from) {
+      ++at;
+      head = next;
+      next = at + 1 < stop ? list[at + 1] : 0;
+    }
   }
+  if (lane < a.top) write_top(a, row, lane, kept, end);
 }
 
 // Gradient: BC 16-byte pieces of a row to a thread.
@@ -329,8 +444,7 @@ __global__ __launch_bounds__(BT) void k_token_logprob_bwd(LpBwdArgs a, unsigned 
   auto* const dx = static_cast<typename X::T*>(a.dx) + row * a.dx_stride;
   const int col0 = (seg * BC * BT + (int)threadIdx.x) * E;
   uint4 v[BC];
-#pragma unroll
-  for (int i = 0; i < BC; ++i) v[i] = load_chunk<F32>(x, min(col0 + i * BT * E, a.vocab), a.vocab);
+  load_pieces<F32, BC>(v, x, col0, BT * E, a.vocab);
   const int64_t token = a.token ? a.token[row] : -1;
   const float m = a.stats[2 * row], z = a.stats[2 * row + 1];
   const bool empty = z == 0.0f;
@@ -366,46 +480,73 @@ __global__ __launch_bounds__(BT) void k_token_logprob_bwd(LpBwdArgs a, unsigned 
 
 int64_t pieces(int64_t vocab, bool fp32) { return (vocab + (fp32 ? 3 : 7)) / (fp32 ? 4 : 8); }
 
-// 16-byte loads of a thread: the fewest that hold a row in one part, or 32 K elements (64 registers of fp32); fewer where
-// the rows alone would leave CUs without work.
-int loads_for(int64_t rows, int64_t vocab, bool fp32) {
+// Threads of a part and 16-byte loads of each.
+struct Part {
+  int t, c;
+};
+// By what the rows alone say, not by the outputs that a call asks for, so that the sums do not depend on these.
+//   A row of up to 32 K logits is one part, held by as few threads as its length allows (1000 logits by a wave: 4096 rows 6 us, by
+// 512 threads 12).
+//   Of bf16 and 128 rows or more, parts have 16 K logits at most: 4096 rows of 32000 take 46 + 5 us with the join and 70 + 9 with 20
+// alternatives, whole ones 51 and 111; 8 rows are faster whole (12 us against 10 + 5).  (fp32, as many: 86 and 105 whole, 87 + 5 and
+// 96 + 10.)
+//   Longer rows have parts of that size, and smaller ones while all rows together have fewer than 128.
+Part part_for(int64_t rows, int64_t vocab, bool fp32) {
   const int64_t n = pieces(vocab, fp32);
-  const int most = fp32 ? 16 : 8;
-  int c = 1;
-  while (c < most && (int64_t)c * NT < n) c *= 2;
-  while (c > 1 && rows * ((n + c * NT - 1) / (c * NT)) < 128 && (n + c / 2 * NT - 1) / (c / 2 * NT) <= kLpMaxSegs) c /= 2;
-  return c;
+  if (n <= 64) return {64, 1};
+  if (n <= 256) return {64, 4};
+  if (n <= 512) return {256, 2};
+  if (n <= 1024) return {256, 4};
+  if (n <= 2048) return {256, 8};
+  const auto parts = [&](int64_t per) { return (n + per - 1) / per; };
+  const Part most = fp32 ? Part{512, 16} : Part{512, 8};
+  int64_t per = (int64_t)most.t * most.c;
+  if (!fp32 && rows >= 128 && parts(2048) <= kLpMaxSegs) return {256, 8};
+  if (n <= 4096) return {512, 8};
+  if (per >= n) return most;
+  while (per > 512 && rows * parts(per) < 128 && parts(per / 2) <= kLpMaxSegs) per /= 2;
+  return per == 512 ? Part{512, 1} : per == 1024 ? Part{512, 2} : per == 2048 ? Part{512, 4} : per == 4096 ? Part{512, 8} : most;
 }
 
 template <bool F32, bool TOP>
-hipError_t launch_parts(const LpArgs& a, int c, hipStream_t s) {
-  const dim3 g((unsigned)(a.rows * a.segs)), b(NT);
+hipError_t launch_parts(const LpArgs& a, Part p, hipStream_t s) {
+  const int64_t items = a.rows * a.segs;
+  const dim3 g((unsigned)items), b(p.t);
   {
     ProfScope ps("k_token_logprob", s);
-    if (c == 1) hipLaunchKernelGGL((k_token_logprob<F32, 1, TOP>), g, b, 0, s, a);
-    else if (c == 2) hipLaunchKernelGGL((k_token_logprob<F32, 2, TOP>), g, b, 0, s, a);
-    else if (c == 4) hipLaunchKernelGGL((k_token_logprob<F32, 4, TOP>), g, b, 0, s, a);
-    else if (c == 8 || !F32) hipLaunchKernelGGL((k_token_logprob<F32, 8, TOP>), g, b, 0, s, a);
-    else hipLaunchKernelGGL((k_token_logprob<F32, F32 ? 16 : 8, TOP>), g, b, 0, s, a);
+#define LP_LAUNCH(T, C) hipLaunchKernelGGL((k_token_logprob<F32, C, TOP, T>), g, b, 0, s, a)
+    if (p.t == 64 && p.c == 1) LP_LAUNCH(64, 1);
+    else if (p.t == 64) LP_LAUNCH(64, 4);
+    else if (p.t == 256 && p.c == 2) LP_LAUNCH(256, 2);
+    else if (p.t == 256 && p.c == 4) LP_LAUNCH(256, 4);
+    else if (p.t == 256) LP_LAUNCH(256, 8);
+    else if (p.c == 1) LP_LAUNCH(512, 1);
+    else if (p.c == 2) LP_LAUNCH(512, 2);
+    else if (p.c == 4) LP_LAUNCH(512, 4);
+    else if (p.c == 8) LP_LAUNCH(512, 8);
+    else if constexpr (F32) LP_LAUNCH(512, 16);   // (of fp32 alone)
+#undef LP_LAUNCH
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.segs == 1) return e;
   }
   ProfScope ps("k_logprob_join", s);
-  hipLaunchKernelGGL((k_logprob_join<F32, TOP>), dim3((unsigned)a.rows), dim3(JT), 0, s, a);
+  const size_t lds = (size_t)JW * a.segs * a.top * sizeof(u64);   // at most 32 KB
+  hipLaunchKernelGGL((k_logprob_join<F32, TOP>), dim3((unsigned)((a.rows + JW - 1) / JW)), dim3(64 * JW), lds, s, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 int lp_segments(int64_t rows, int64_t vocab, bool fp32) {
-  const int64_t per = (int64_t)loads_for(rows, vocab, fp32) * NT;
+  const Part p = part_for(rows, vocab, fp32);
+  const int64_t per = (int64_t)p.t * p.c;
   return (int)((pieces(vocab, fp32) + per - 1) / per);
 }
 
 hipError_t launch_logprob(const LpArgs& a, hipStream_t s) {
-  const int c = loads_for(a.rows, a.vocab, a.fp32);
-  if (a.fp32) return a.top ? launch_parts<true, true>(a, c, s) : launch_parts<true, false>(a, c, s);
-  return a.top ? launch_parts<false, true>(a, c, s) : launch_parts<false, false>(a, c, s);
+  const Part p = part_for(a.rows, a.vocab, a.fp32);
+  if (a.fp32) return a.top ? launch_parts<true, true>(a, p, s) : launch_parts<true, false>(a, p, s);
+  return a.top ? launch_parts<false, true>(a, p, s) : launch_parts<false, false>(a, p, s);
 }
 
 hipError_t launch_logprob_bwd(const LpBwdArgs& a, hipStream_t s) {

@@ -36,12 +36,6 @@ __device__ __forceinline__ uint4* out_row(const RowsView& v, int64_t row) {
   return reinterpret_cast<uint4*>(v.data + row * v.stride);
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
-}
-
 // Sums of N values over the T threads of a row, the same in all of them.  `buf`: [T / 64][N] floats, free again
 // after the barrier of the next call but one (two buffers).
 template <int T, int N>

@@ -16,6 +16,42 @@ struct RowsView {
   int64_t stride;
 };
 
+#ifdef __HIPCC__
+// Sums, maxima and prefix sums of a wave by data-parallel moves (shifts by 1, 2, 4, 8 within rows of 16 lanes, then the last
+// lane of a row to the next one, and of the first half to the second): a few cycles a step where an exchange through LDS takes
+// over a hundred.  The order is fixed.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_or(uint32_t none, uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xF, false);
+}
+#define QL_WAVE_SCAN(STEP) STEP(0x111, 0xF) STEP(0x112, 0xF) STEP(0x114, 0xF) STEP(0x118, 0xF) STEP(0x142, 0xA) STEP(0x143, 0xC)
+__device__ __forceinline__ float wave_sum(float v) {
+#define QL_STEP(C, R) v += __uint_as_float(dpp_or<C, R>(0u, __float_as_uint(v)));
+  QL_WAVE_SCAN(QL_STEP)
+#undef QL_STEP
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+__device__ __forceinline__ float wave_max(float v) {   // (NaN are passed over)
+#define QL_STEP(C, R) v = fmaxf(v, __uint_as_float(dpp_or<C, R>(0xFF800000u, __float_as_uint(v))));
+  QL_WAVE_SCAN(QL_STEP)
+#undef QL_STEP
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#define QL_STEP(C, R) v = max(v, dpp_or<C, R>(0u, v));
+  QL_WAVE_SCAN(QL_STEP)
+#undef QL_STEP
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ int wave_prefix(int v) {   // the sum up to and with this lane
+#define QL_STEP(C, R) v += (int)dpp_or<C, R>(0u, (uint32_t)v);
+  QL_WAVE_SCAN(QL_STEP)
+#undef QL_STEP
+  return v;
+}
+#undef QL_WAVE_SCAN
+#endif
+
 // ---- residual addition and norm (rms_norm.hip) ------------------------------------------------
 struct NormArgs {
   RowsView x, res;    // forward: input and residual (or none); backward: dy and the forward's sum

@@ -65,10 +65,10 @@ LpWs lp_layout(void* base, int64_t rows, int64_t segs, int32_t top) {
   w.bytes = round_up(c.off, 256);
   return w;
 }
-// Parts of a call with at most these rows and logits: a row is cut into pieces of 32768 logits, or smaller ones while all
-// rows together have fewer than 128, so into no more than 256 in all then.
+// Parts of a call with at most these rows and logits: a row is cut into pieces of 16384 logits at least, or smaller ones while
+// all rows together have fewer than 128, so into no more than 256 in all then.
 int64_t lp_most_parts(int64_t rows, int64_t vocab) {
-  const int64_t per_row = (vocab + 32767) / 32768;
+  const int64_t per_row = (vocab + 16383) / 16384;
   return std::max<int64_t>(256, per_row > 1 ? rows * per_row : 0);
 }
 int64_t lp_parts(int64_t rows, int64_t vocab, int32_t dtype) { return lp_segments(rows, vocab, dtype == QLORA_FP32); }
