@@ -605,12 +605,12 @@ def _rows(t: torch.Tensor, name: str, device=None, shape=None):
     return t.data_ptr(), strides[0]
 
 
-def _new_rows(given, name: str, device, shape):
-    """An output and its (address, row stride): the caller's, checked, or a new contiguous one."""
+def _new_rows(given, name: str, device, like):
+    """An output like the tensor `like` and its (address, row stride): the caller's, checked, or a new contiguous one."""
     if given is not None:
-        return given, _rows(given, name, device, shape)
-    t = torch.empty(shape, dtype=torch.bfloat16, device=device)
-    return t, (t.data_ptr(), shape[1])
+        return given, _rows(given, name, device, like.shape)
+    t = torch.empty_like(like, memory_format=torch.contiguous_format)   # (less than half the cost of torch.empty's arguments)
+    return t, (t.data_ptr(), like.size(1))
 
 
 def qlora_rms_norm(x: torch.Tensor, weight: torch.Tensor | None, residual: torch.Tensor | None = None,
@@ -628,8 +628,8 @@ def qlora_rms_norm(x: torch.Tensor, weight: torch.Tensor | None, residual: torch
         raise QLoRAError("sum_out needs a residual")
 
     def run(stream):
-        y, (py, sy) = _new_rows(out, "out", dev, shape)
-        h, (ph, sh) = (x, (None, 0)) if residual is None else _new_rows(sum_out, "sum_out", dev, shape)
+        y, (py, sy) = _new_rows(out, "out", dev, x)
+        h, (ph, sh) = (x, (None, 0)) if residual is None else _new_rows(sum_out, "sum_out", dev, x)
         _check(lib().qlora_rms_norm(px, sx, pr, sr, shape[0], shape[1], _at(weight), eps, py, sy, ph, sh, stream),
                "qlora_rms_norm")
         return y, h
@@ -662,7 +662,7 @@ def qlora_rms_norm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor |
         _need(dweight, torch.float32, dev, "dweight", (shape[1],))
 
     def run(stream):
-        out, (px, sx) = _new_rows(dx, "dx", dev, shape)
+        out, (px, sx) = _new_rows(dx, "dx", dev, dy)
         gw, ws = None, None
         if weight_grad:
             gw = torch.empty(shape[1], dtype=torch.float32, device=dev) if dweight is None else dweight
@@ -739,7 +739,7 @@ def qlora_gated_bwd(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, activati
             _need(t, torch.bfloat16, dev, name, shape)
 
     def run(stream):
-        new = lambda: torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        new = lambda: torch.empty_like(dH)
         g = new() if dG is None else dG
         u = new() if dU is None else dU
         h = new() if H is True else H if isinstance(H, torch.Tensor) else None
@@ -819,7 +819,7 @@ def qlora_token_logprob_bwd(logits: torch.Tensor, token: torch.Tensor | None, st
             _need(t, torch.float32, dev, name, (rows,))
 
     def run(stream):
-        d = torch.empty((rows, vocab), dtype=logits.dtype, device=dev) if out is None else out
+        d = torch.empty_like(logits, memory_format=torch.contiguous_format) if out is None else out
         pd, sd, _ = _logits(d, "out", dev, logits)
         _check(lib().qlora_token_logprob_bwd(px, sx, rows, vocab, kind, _at(token), scale, stats.data_ptr(), _at(dlogprob),
                                              _at(entropy), _at(dentropy), pd, sd, stream), "qlora_token_logprob_bwd")

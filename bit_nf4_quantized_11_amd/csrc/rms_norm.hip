@@ -3,10 +3,12 @@
 //   h = bf16(x + residual),  y = bf16(h w r),  r = 1 / sqrt(mean(h^2) + eps)
 //   dx = bf16(dh + r (w dy - h r^2 mean(w dy h))),  dw = sum over rows of dy h r
 //
-// Bound by HBM: 4 to 8 B per element in either direction.  A row stays in the registers of the T threads that
+// Bound by HBM: 4 to 8 B per element in either direction: forward of 4096 x 4096 with a residual 22 us = 6.1 TB/s, backward with dh
+// 24 us = 5.6 TB/s and 4.6 for the weight's gradient, whose 512 partials are 8 MB more (2048 x 8192: 28 + 4.8 us).  For a few rows by a
+// launch and two dependent round trips (16 x 8192: 3.8 us).  A row stays in the registers of the T threads that
 // hold it (a wave for short rows, a workgroup for long ones), 8 elements to a load, so each tensor is read or written once.
-// The backward walks over rows with the weight's gradient in registers, one partial per group of T threads,
-// summed by a second kernel in a fixed order.
+// The backward walks over rows with the weight's gradient in registers, one partial per workgroup, summed by a second
+// kernel in a fixed order.
 #include "kernels.h"
 #include "rows.h"
 
@@ -16,24 +18,23 @@ namespace {
 
 constexpr int NT = 256;   // threads of a workgroup of several rows
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    f[2 * i] = __uint_as_float(v[i] << 16);
+    f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
   }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
+  return u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
 }
 
-__device__ __forceinline__ const uint4* row_of(const RowsView& v, int64_t row) {
-  return reinterpret_cast<const uint4*>(v.data + row * v.stride);
+__device__ __forceinline__ const u32x4* row_of(const RowsView& v, int64_t row) {
+  return reinterpret_cast<const u32x4*>(v.data + row * v.stride);
 }
-__device__ __forceinline__ uint4* out_row(const RowsView& v, int64_t row) {
-  return reinterpret_cast<uint4*>(v.data + row * v.stride);
+__device__ __forceinline__ u32x4* out_row(const RowsView& v, int64_t row) {
+  return reinterpret_cast<u32x4*>(v.data + row * v.stride);
 }
 
 // Sums of N values over the T threads of a row, the same in all of them.  `buf`: [T / 64][N] floats, free again
@@ -64,8 +65,8 @@ __global__ __launch_bounds__(T < NT ? NT : T) void k_rms_norm(NormArgs a) {
   const int t = threadIdx.x % T, chunks = a.dim >> 3;
   const int64_t row = (int64_t)blockIdx.x * (T < NT ? NT / T : 1) + threadIdx.x / T;
   if (row >= a.rows) return;   // (a whole wave, and never one of several that wait for each other)
-  const uint4 zero = make_uint4(0, 0, 0, 0), one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-  uint4 xv[C], rv[C], wv[C];
+  const u32x4 zero = u32x4{0, 0, 0, 0}, one = u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+  u32x4 xv[C], rv[C], wv[C];
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int c = t + i * T;
@@ -77,7 +78,7 @@ __global__ __launch_bounds__(T < NT ? NT : T) void k_rms_norm(NormArgs a) {
   for (int i = 0; i < C; ++i) {
     const int c = t + i * T;
     wv[i] = one;
-    if (a.w && c < chunks) wv[i] = reinterpret_cast<const uint4*>(a.w)[c];
+    if (a.w && c < chunks) wv[i] = reinterpret_cast<const u32x4*>(a.w)[c];
   }
   float ss[1] = {0.0f};
 #pragma unroll
@@ -110,42 +111,61 @@ __global__ __launch_bounds__(T < NT ? NT : T) void k_rms_norm(NormArgs a) {
   }
 }
 
+// The loads of a row in the backward.
 template <int T, int C, bool DH>
+struct BwdRow {
+  u32x4 g[C], h[C], d[DH ? C : 1];
+  __device__ __forceinline__ void load(const NormArgs& a, int64_t row, int t, int chunks) {
+    const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int c = t + i * T;
+      const bool in = c < chunks;
+      g[i] = in ? row_of(a.x, row)[c] : zero;
+      h[i] = in ? row_of(a.res, row)[c] : zero;
+      if constexpr (DH) d[i] = in ? row_of(a.dh, row)[c] : zero;
+    }
+  }
+};
+
+// AHEAD: the next row's loads are issued before this row's sums are waited for (4096 x 4096 with dh 25.4 -> 24 us, without 20.3 ->
+// 18.7), where the registers leave two workgroups to a CU all the same (2048 x 8192 with dh: 28 us without, 29 with).
+template <int T, int C, bool DH, bool AHEAD = C <= 2 || !DH>
 __global__ __launch_bounds__(T < NT ? NT : T) void k_rms_norm_bwd(NormArgs a) {
   constexpr int G = T < NT ? NT / T : 1;   // rows of a workgroup at a time
   __shared__ float buf[2][T / 64 * 2];
+  __shared__ float sum[G > 1 ? (G - 1) * T * C * 8 : 1];
   const int t = threadIdx.x % T, chunks = a.dim >> 3;
-  const uint4 zero = make_uint4(0, 0, 0, 0), one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+  const u32x4 one = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
   float acc[C][8];
 #pragma unroll
   for (int i = 0; i < C; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
-  uint4 wv[C];
+  u32x4 wv[C];
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int c = t + i * T;
     wv[i] = one;
-    if (a.w && c < chunks) wv[i] = reinterpret_cast<const uint4*>(a.w)[c];
+    if (a.w && c < chunks) wv[i] = reinterpret_cast<const u32x4*>(a.w)[c];
   }
-  const int64_t group = (int64_t)blockIdx.x * G + threadIdx.x / T, step = (int64_t)gridDim.x * G;
+  const int64_t first = (int64_t)blockIdx.x * G + threadIdx.x / T, step = (int64_t)gridDim.x * G;
+  BwdRow<T, C, DH> now, next;
+  if (AHEAD && first < a.rows) next.load(a, first, t, chunks);
   int turn = 0;
-  for (int64_t row = group; row < a.rows; row += step, turn ^= 1) {
-    uint4 gv[C], hv[C], dv[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int c = t + i * T;
-      const bool in = c < chunks;
-      gv[i] = in ? row_of(a.x, row)[c] : zero;
-      hv[i] = in ? row_of(a.res, row)[c] : zero;
-      if (DH) dv[i] = in ? row_of(a.dh, row)[c] : zero;
+  for (int64_t row = first; row < a.rows; row += step, turn ^= 1) {
+    if constexpr (AHEAD) {
+      now = next;
+      if (row + step < a.rows) next.load(a, row + step, t, chunks);
+    } else {
+      now.load(a, row, t, chunks);
     }
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float g[8], h[8], w[8];
-      unpack8(gv[i], g);
-      unpack8(hv[i], h);
+      unpack8(now.g[i], g);
+      unpack8(now.h[i], h);
       unpack8(wv[i], w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -159,10 +179,10 @@ __global__ __launch_bounds__(T < NT ? NT : T) void k_rms_norm_bwd(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float g[8], h[8], w[8], d[8];
-      unpack8(gv[i], g);
-      unpack8(hv[i], h);
+      unpack8(now.g[i], g);
+      unpack8(now.h[i], h);
       unpack8(wv[i], w);
-      if (DH) unpack8(dv[i], d);
+      if constexpr (DH) unpack8(now.d[i], d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         acc[i][j] = __builtin_fmaf(g[j] * h[j], r, acc[i][j]);
@@ -173,18 +193,92 @@ __global__ __launch_bounds__(T < NT ? NT : T) void k_rms_norm_bwd(NormArgs a) {
     }
   }
   if (!a.part) return;
+  if constexpr (G > 1) {   // the workgroup's waves, in their order
+    const int w = threadIdx.x / T;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (w > 0) sum[((w - 1) * C * 8 + i * 8 + j) * T + t] = acc[i][j];
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int k = 0; k < G - 1; ++k) acc[i][j] += sum[(k * C * 8 + i * 8 + j) * T + t];
+  }
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int c = t + i * T;
     if (c >= chunks) continue;
-    float* const p = a.part + group * a.dim + c * 8;
+    float* const p = a.part + (int64_t)blockIdx.x * a.dim + c * 8;
+    *reinterpret_cast<f32x4*>(p) = f32x4{acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{acc[i][4], acc[i][5], acc[i][6], acc[i][7]};
+  }
+}
+
+// Rows too long for the registers of a workgroup: dy and h are read a second time (from the caches) after the sums
+// (500 x 32768: 38 us; held in registers, most of which spill, 102).
+template <bool DH>
+__global__ __launch_bounds__(1024) void k_rms_norm_bwd_long(NormArgs a) {
+  constexpr int T = 1024, C = 4;
+  __shared__ float buf[2][T / 64 * 2];
+  const int t = threadIdx.x, chunks = a.dim >> 3;
+  const u32x4* const wp = reinterpret_cast<const u32x4*>(a.w);
+  float acc[C][8] = {};
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int c = t + i * T;
+      if (c >= chunks) continue;
+      float g[8], h[8], w[8];
+      unpack8(row_of(a.x, row)[c], g);
+      unpack8(row_of(a.res, row)[c], h);
+      if (a.w) unpack8(wp[c], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[0] = __builtin_fmaf(h[j], h[j], s[0]);
+        s[1] = __builtin_fmaf(g[j] * h[j], a.w ? w[j] : 1.0f, s[1]);
+      }
+    }
+    row_sum<T, 2>(s, buf[turn]);
+    const float r = 1.0f / sqrtf(s[0] * a.inv_dim + a.eps);
+    const float m = s[1] * a.inv_dim * r * r;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int c = t + i * T;
+      if (c >= chunks) continue;
+      float g[8], h[8], w[8], d[8];
+      unpack8(row_of(a.x, row)[c], g);
+      unpack8(row_of(a.res, row)[c], h);
+      if (a.w) unpack8(wp[c], w);
+      if (DH) unpack8(row_of(a.dh, row)[c], d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        acc[i][j] = __builtin_fmaf(g[j] * h[j], r, acc[i][j]);
+        const float v = __builtin_fmaf(-h[j], m, g[j] * (a.w ? w[j] : 1.0f));
+        g[j] = DH ? __builtin_fmaf(r, v, d[j]) : r * v;
+      }
+      out_row(a.y, row)[c] = pack8(g);
+    }
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int c = t + i * T;
+    if (c >= chunks) continue;
+    float* const p = a.part + (int64_t)blockIdx.x * a.dim + c * 8;
     *reinterpret_cast<f32x4*>(p) = f32x4{acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
     *reinterpret_cast<f32x4*>(p + 4) = f32x4{acc[i][4], acc[i][5], acc[i][6], acc[i][7]};
   }
 }
 
 // dw[c] = sum over n partials [n][dim]: 32 columns per workgroup (128 B of a partial), 32 threads per column.
-constexpr int WT = 1024, WC = 32, WR = WT / WC, WL = 8;
+constexpr int WT = 1024, WC = 32, WR = WT / WC, WL = 16;
 __global__ __launch_bounds__(WT) void k_norm_weight_grad(const float* __restrict__ part, int n, int dim, float* __restrict__ dw) {
   __shared__ float sum[WR][WC + 1];
   const int c = threadIdx.x % WC, r = threadIdx.x / WC, col = blockIdx.x * WC + c;
@@ -224,60 +318,66 @@ Shape shape_of(int32_t dim) {
   return {1024, 4};
 }
 
-int64_t bwd_groups(int64_t rows, const Shape& s) {
+// of the backward
+Shape bwd_shape_of(int32_t dim) {
+  const Shape sh = shape_of(dim);
+  return sh.t == 1024 && sh.c == 2 ? Shape{512, 4} : sh;
+}
+int64_t bwd_wgs(int64_t rows, const Shape& s) {
   const int per = s.t < NT ? NT / s.t : 1;
-  const int64_t wgs = (rows + per - 1) / per, most = s.t == 1024 ? 256 : 512;
-  return (wgs < most ? wgs : most) * per;
+  const int64_t wgs = (rows + per - 1) / per, most = s.t >= 512 ? 256 : 512;
+  return wgs < most ? wgs : most;
 }
 
 }  // namespace
 
-// K<threads, loads, flag> launched for the run-time shape
-#define NORM_LAUNCH(K, sh, flag, grid, ...)                                                             \
-  do {                                                                                                   \
-    const dim3 g_((unsigned)(grid)), b_((unsigned)(sh.t < NT ? NT : sh.t));                              \
-    if (flag) {                                                                                          \
-      if (sh.t == 64 && sh.c == 1) hipLaunchKernelGGL((K<64, 1, true>), g_, b_, 0, s, __VA_ARGS__);      \
-      else if (sh.t == 64 && sh.c == 2) hipLaunchKernelGGL((K<64, 2, true>), g_, b_, 0, s, __VA_ARGS__); \
-      else if (sh.t == 64) hipLaunchKernelGGL((K<64, 4, true>), g_, b_, 0, s, __VA_ARGS__);              \
-      else if (sh.t == 256 && sh.c == 2) hipLaunchKernelGGL((K<256, 2, true>), g_, b_, 0, s, __VA_ARGS__); \
-      else if (sh.t == 256) hipLaunchKernelGGL((K<256, 4, true>), g_, b_, 0, s, __VA_ARGS__);            \
-      else if (sh.c == 2) hipLaunchKernelGGL((K<1024, 2, true>), g_, b_, 0, s, __VA_ARGS__);             \
-      else hipLaunchKernelGGL((K<1024, 4, true>), g_, b_, 0, s, __VA_ARGS__);                            \
-    } else {                                                                                             \
-      if (sh.t == 64 && sh.c == 1) hipLaunchKernelGGL((K<64, 1, false>), g_, b_, 0, s, __VA_ARGS__);     \
-      else if (sh.t == 64 && sh.c == 2) hipLaunchKernelGGL((K<64, 2, false>), g_, b_, 0, s, __VA_ARGS__); \
-      else if (sh.t == 64) hipLaunchKernelGGL((K<64, 4, false>), g_, b_, 0, s, __VA_ARGS__);             \
-      else if (sh.t == 256 && sh.c == 2) hipLaunchKernelGGL((K<256, 2, false>), g_, b_, 0, s, __VA_ARGS__); \
-      else if (sh.t == 256) hipLaunchKernelGGL((K<256, 4, false>), g_, b_, 0, s, __VA_ARGS__);           \
-      else if (sh.c == 2) hipLaunchKernelGGL((K<1024, 2, false>), g_, b_, 0, s, __VA_ARGS__);            \
-      else hipLaunchKernelGGL((K<1024, 4, false>), g_, b_, 0, s, __VA_ARGS__);                           \
-    }                                                                                                    \
-  } while (0)
+// a launch with the flag where the run-time shape is T x C
+#define NORM_CASE(T, C, KT, KF)                                                              \
+  if (sh.t == T && sh.c == C) {                                                              \
+    if (flag) hipLaunchKernelGGL(KT, g, dim3(T < NT ? NT : T), 0, s, a);                     \
+    else hipLaunchKernelGGL(KF, g, dim3(T < NT ? NT : T), 0, s, a);                          \
+  }
+#define FWD_CASE(T, C) NORM_CASE(T, C, (k_rms_norm<T, C, true>), (k_rms_norm<T, C, false>))
+#define BWD_CASE(T, C) NORM_CASE(T, C, (k_rms_norm_bwd<T, C, true>), (k_rms_norm_bwd<T, C, false>))
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
   const Shape sh = shape_of(a.dim);
   const int per = sh.t < NT ? NT / sh.t : 1;
+  const dim3 g((unsigned)((a.rows + per - 1) / per));
+  const bool flag = a.res.data != nullptr;
   ProfScope ps("k_rms_norm", s);
-  NORM_LAUNCH(k_rms_norm, sh, a.res.data != nullptr, (a.rows + per - 1) / per, a);
+  FWD_CASE(64, 1)
+  FWD_CASE(64, 2)
+  FWD_CASE(64, 4)
+  FWD_CASE(256, 2)
+  FWD_CASE(256, 4)
+  FWD_CASE(1024, 2)
+  FWD_CASE(1024, 4)
   return hipGetLastError();
 }
 
-size_t norm_part_floats(int64_t rows, int32_t dim) { return (size_t)bwd_groups(rows, shape_of(dim)) * dim; }
+size_t norm_part_floats(int64_t rows, int32_t dim) { return (size_t)bwd_wgs(rows, bwd_shape_of(dim)) * dim; }
 
 hipError_t launch_rms_norm_bwd(const NormArgs& a, float* dw, hipStream_t s) {
-  const Shape sh = shape_of(a.dim);
-  const int per = sh.t < NT ? NT / sh.t : 1;
-  const int64_t groups = bwd_groups(a.rows, sh);
+  const Shape sh = bwd_shape_of(a.dim);
+  const int64_t wgs = bwd_wgs(a.rows, sh);
   {
+    const dim3 g((unsigned)wgs);
+    const bool flag = a.dh.data != nullptr;
     ProfScope ps("k_rms_norm_bwd", s);
-    NORM_LAUNCH(k_rms_norm_bwd, sh, a.dh.data != nullptr, groups / per, a);
+    BWD_CASE(64, 1)
+    BWD_CASE(64, 2)
+    BWD_CASE(64, 4)
+    BWD_CASE(256, 2)
+    BWD_CASE(256, 4)
+    BWD_CASE(512, 4)
+    NORM_CASE(1024, 4, (k_rms_norm_bwd_long<true>), (k_rms_norm_bwd_long<false>))
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (!a.part) return hipSuccess;
   ProfScope ps("k_norm_weight_grad", s);
-  hipLaunchKernelGGL(k_norm_weight_grad, dim3((unsigned)((a.dim + WC - 1) / WC)), dim3(WT), 0, s, a.part, (int)groups, a.dim, dw);
+  hipLaunchKernelGGL(k_norm_weight_grad, dim3((unsigned)((a.dim + WC - 1) / WC)), dim3(WT), 0, s, a.part, (int)wgs, a.dim, dw);
   return hipGetLastError();
 }
 
