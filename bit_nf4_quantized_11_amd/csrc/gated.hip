@@ -10,6 +10,7 @@ namespace qlora {
 
 namespace {
 
+using gemm::i16x4;
 using gemm::ld16;
 using gemm::make_rsrc;
 using gemm::rsrc_t;
@@ -24,36 +25,42 @@ struct EpiArgs {
   uint16_t* H;
 };
 
-// Both sides' sums as k_gemv_epilogue forms them (partial sums in slice order, T = its partials in slice order, Ts = bf16(s T),
-// plus Ts B), then the activation and the product.  64 columns of one 16-token group per workgroup; thread t takes
-// column t % 64 for tokens t / 64 + 4 q.  The first 4 slices' loads of both sides are issued before any is used.  The ranks
-// go through LDS 128 at a time: [2][16][ranks] floats of Ts, [2][ranks][64] bf16 of B.
-constexpr int RANKS = 128;
+// Natural [ranks][64] tile of B: row j = 128 bytes of eight 16-byte chunks, chunk q at q ^ 2 f(j), which keeps the
+// transposing reads (4 rows x 32 bytes per 16 lanes, two such row quads 8 apart per 32 lanes) free of conflicts.
+__device__ __forceinline__ int bpos(int j, int q) {
+  const int f = ((j >> 1) & 1) | ((j >> 2) & 2);
+  return j * 64 + ((q ^ (f << 1)) << 3);
+}
+
+// Both sides' sums (partial sums in slice order, T = its partials in slice order, Ts = bf16(s T), plus Ts B by matrix
+// instructions), then the activation and the product.  64 features of one 16-token group per workgroup, 16 to a wave; lane l
+// holds features 4 (l / 16) .. + 3 of token l % 16, as the matrix instruction leaves them.  Bound by latency: the first 4
+// slices' loads and B's are issued before any is used.  The ranks go through LDS 128 at a time.
+// (16 tokens, 22016 features, rank 64, 4 slices: 5.x us; with Ts B by fp32 multiply-adds out of LDS 11.2, and 200 tokens 14.)
+constexpr int RANKS = 128, TPAD = 8, S0 = 4;
 __global__ __launch_bounds__(256) void k_gated_epilogue(EpiArgs a) {
-  extern __shared__ __attribute__((aligned(16))) float lds[];
-  const int t = threadIdx.x, rp = (int)a.rp, rl = min(rp, RANKS);
-  float* const sTs = lds;
-  uint16_t* const sB = reinterpret_cast<uint16_t*>(lds + 2 * 16 * rl);
+  extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int rp = (int)a.rp, rl = min(rp, RANKS), ts_ld = rl + TPAD;
+  uint16_t* const sT = lds;                          // [2][16][ts_ld] of Ts
+  uint16_t* const sB = lds + 2 * 16 * ts_ld;         // [2][rl][64]
   const int64_t n0 = (int64_t)blockIdx.x * 64, m0 = (int64_t)blockIdx.y * 16;
-  const int c = t & 63, mq = t >> 6;
-  const int64_t n = n0 + c, nc = n < a.N ? n : a.N - 1;   // clamped column: every load stays inside the partials
-  const int Mg = (int)min<int64_t>(16, a.M - m0), mcap = Mg - 1;
-  constexpr int S0 = 4;
-  float v[2][S0][4];
+  const int tok = lane & 15, g = lane >> 4;
+  const int Mg = (int)min<int64_t>(16, a.M - m0);
+  const int64_t n = n0 + wave * 16 + 4 * g;          // this lane's features
+  const int64_t at = (m0 + min(tok, Mg - 1)) * a.npad + min(n, a.npad - 4), slice = a.M * a.npad;
+  f32x4 v[2][S0];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float* const part = a.side[k].partial + m0 * a.npad;
+  for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int u = 0; u < S0; ++u)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[k][u][q] = part[((int64_t)min(u, a.splits - 1) * a.M + min(mq + 4 * q, mcap)) * a.npad + nc];
-  }
+      v[k][u] = *reinterpret_cast<const f32x4*>(a.side[k].partial + min(u, a.splits - 1) * slice + at);
   const uint32_t bend = (uint32_t)(a.r * a.N * 2);
   const rsrc_t rB[2] = {make_rsrc(a.side[0].B, bend), make_rsrc(a.side[1].B, bend)};
-  float lora[2][4] = {};
+  f32x4 lora[2] = {};
   for (int j0 = 0; j0 < rp; j0 += RANKS) {
     const int jn = min(rp - j0, RANKS);   // 64 or 128
-    // rows j0 .. of B for the 64 columns: jn * 8 chunks of 16 bytes a side (outside B: past its end, zero)
+    // rows j0 .. of B for the 64 features: jn * 8 chunks of 16 bytes a side (outside B: past its end, zero)
     uint4 bv[2][4];
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -68,90 +75,86 @@ __global__ __launch_bounds__(256) void k_gated_epilogue(EpiArgs a) {
     for (int k = 0; k < 2; ++k) {
       const float* const tp = a.side[k].partial + a.tpart + m0 * a.rp;
       uint16_t* const save = a.side[k].T_save && blockIdx.x == 0 ? a.side[k].T_save + m0 * a.r : nullptr;
-      for (int e0 = t; e0 < Mg * jn; e0 += 4 * 256) {
-        float ts[4] = {0.f, 0.f, 0.f, 0.f};
-        int at[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int idx = min(e0 + e * 256, Mg * jn - 1), m = idx / jn;
-          at[e] = m * rp + j0 + idx - m * jn;
-        }
+      for (int e = t; e < Mg * (jn >> 2); e += 256) {
+        const int m = e / (jn >> 2), jl = (e - m * (jn >> 2)) * 4, jj = j0 + jl;
+        const float* const p = tp + m * rp + jj;
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
         for (int s0 = 0; s0 < a.asplits; s0 += 4) {
-          float tv[4][4];
+          f32x4 tv[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) tv[u] = *reinterpret_cast<const f32x4*>(p + (int64_t)min(s0 + u, a.asplits - 1) * a.M * a.rp);
 #pragma unroll
           for (int u = 0; u < 4; ++u)
+            if (s0 + u < a.asplits)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) tv[u][e] = tp[(int64_t)min(s0 + u, a.asplits - 1) * a.M * a.rp + at[e]];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (s0 + u < a.asplits) ts[e] = __fadd_rn(ts[e], tv[u][e]);
+              for (int i = 0; i < 4; ++i) sum[i] = __fadd_rn(sum[i], tv[u][i]);
         }
+        uint32_t ts[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int idx = e0 + e * 256;
-          if (idx >= Mg * jn) continue;
-          const int m = idx / jn, jl = idx - m * jn, jj = j0 + jl;
-          sTs[(k * 16 + m) * rl + jl] = jj < a.r ? bf16_to_f32(f32_to_bf16_bits(__fmul_rn(a.scale, ts[e]))) : 0.0f;
-          if (save && jj < a.r) save[m * a.r + jj] = (uint16_t)f32_to_bf16_bits(ts[e]);
+        for (int i = 0; i < 4; ++i) {
+          // (r is a multiple of 8: the four ranks are all below it or none)
+          ts[i] = jj < a.r ? f32_to_bf16_bits(__fmul_rn(a.scale, sum[i])) : 0u;
+          if (save && jj < a.r) save[m * a.r + jj + i] = (uint16_t)f32_to_bf16_bits(sum[i]);
         }
+        *reinterpret_cast<uint2*>(sT + (k * 16 + m) * ts_ld + jl) = make_uint2(ts[0] | ts[1] << 16, ts[2] | ts[3] << 16);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int idx = t + 256 * u;
-        if (idx < jn * 8) *reinterpret_cast<uint4*>(sB + k * rl * 64 + idx * 8) = bv[k][u];
+        if (idx < jn * 8) *reinterpret_cast<uint4*>(sB + k * rl * 64 + bpos(idx >> 3, idx & 7)) = bv[k][u];
       }
     }
     __syncthreads();
+    const int j = lane & 15, jc = wave * 16 + (j & 3) * 4;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-      for (int jj = 0; jj < jn; jj += 4) {
-        float b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = bf16_to_f32(sB[k * rl * 64 + (jj + i) * 64 + c]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          // (tokens past the group read what the LDS holds; their sums are not stored)
-          const float4 tq = *reinterpret_cast<const float4*>(sTs + (k * 16 + mq + 4 * q) * rl + jj);
-          lora[k][q] = __builtin_fmaf(tq.x, b[0], lora[k][q]);
-          lora[k][q] = __builtin_fmaf(tq.y, b[1], lora[k][q]);
-          lora[k][q] = __builtin_fmaf(tq.z, b[2], lora[k][q]);
-          lora[k][q] = __builtin_fmaf(tq.w, b[3], lora[k][q]);
-        }
+      for (int ks = 0; ks < jn; ks += 32) {
+        const uint16_t* const b = sB + k * rl * 64;
+        const int kr = ks + g * 8 + (j >> 2);
+        const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) i16x4*)(b + bpos(kr, jc >> 3) + (jc & 7)));
+        const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) i16x4*)(b + bpos(kr + 4, jc >> 3) + (jc & 7)));
+        const uint2 x = __builtin_bit_cast(uint2, lo), y = __builtin_bit_cast(uint2, hi);
+        const u32x4 wa = {x.x, x.y, y.x, y.y};
+        // (rows of tokens past the group hold whatever the LDS does; their sums are not stored)
+        const u32x4 tb = *reinterpret_cast<const u32x4*>(sT + (k * 16 + tok) * ts_ld + ks + g * 8);
+        lora[k] = mfma16(wa, tb, lora[k]);
       }
   }
-  if (n >= a.N) return;
-  float out[2][4];
+  if (n >= a.N || tok >= Mg) return;
+  f32x4 out[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const float* const part = a.side[k].partial + m0 * a.npad;
-    float acc[4];
+    f32x4 acc = v[k][0];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      acc[q] = v[k][0][q];
+    for (int u = 1; u < S0; ++u)
+      if (u < a.splits)
 #pragma unroll
-      for (int u = 1; u < S0; ++u)
-        if (u < a.splits) acc[q] = __fadd_rn(acc[q], v[k][u][q]);
+        for (int i = 0; i < 4; ++i) acc[i] = __fadd_rn(acc[i], v[k][u][i]);
+    for (int s0 = S0; s0 < a.splits; s0 += S0) {
+      f32x4 w[S0];
+#pragma unroll
+      for (int u = 0; u < S0; ++u) w[u] = *reinterpret_cast<const f32x4*>(a.side[k].partial + min(s0 + u, a.splits - 1) * slice + at);
+#pragma unroll
+      for (int u = 0; u < S0; ++u)
+        if (s0 + u < a.splits)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i] = __fadd_rn(acc[i], w[u][i]);
     }
-    for (int sp = S0; sp < a.splits; ++sp) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        acc[q] = __fadd_rn(acc[q], part[((int64_t)sp * a.M + min(mq + 4 * q, mcap)) * a.npad + n]);
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) out[k][q] = __fadd_rn(acc[q], lora[k][q]);
+    for (int i = 0; i < 4; ++i) out[k][i] = __fadd_rn(acc[i], lora[k][i]);
   }
+  float h[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int m = mq + 4 * q;
-    if (m >= Mg) continue;
-    const int64_t at = (m0 + m) * a.N + n;
-    a.H[at] = (uint16_t)f32_to_bf16_bits(activate(out[0][q], a.act) * out[1][q]);
-    if (a.side[0].out) {
-      a.side[0].out[at] = (uint16_t)f32_to_bf16_bits(out[0][q]);
-      a.side[1].out[at] = (uint16_t)f32_to_bf16_bits(out[1][q]);
-    }
+  for (int i = 0; i < 4; ++i) h[i] = activate(out[0][i], a.act) * out[1][i];
+  const auto put = [&](uint16_t* p, float a0, float a1, float a2, float a3) {
+    *reinterpret_cast<uint2*>(p + (m0 + tok) * a.N + n) = make_uint2(pack_bf16x2(a0, a1), pack_bf16x2(a2, a3));
+  };
+  put(a.H, h[0], h[1], h[2], h[3]);
+  if (a.side[0].out) {
+    put(a.side[0].out, out[0][0], out[0][1], out[0][2], out[0][3]);
+    put(a.side[1].out, out[1][0], out[1][1], out[1][2], out[1][3]);
   }
 }
 
@@ -193,7 +196,8 @@ hipError_t launch_gated_epilogue(const GatedSide& gate, const GatedSide& up, con
                                  int64_t r, float scale, int act, uint16_t* H, hipStream_t s) {
   const int64_t rp = (r + 63) / 64 * 64;
   const EpiArgs a{{gate, up}, pl.splits, pl.asplits, pl.tpart, M, N, pl.npad, rp, r, scale, act, H};
-  const size_t lds = (size_t)(rp < RANKS ? rp : RANKS) * (2 * 16 * 4 + 2 * 64 * 2);
+  const int64_t rl = rp < RANKS ? rp : RANKS;
+  const size_t lds = (size_t)(2 * 16 * (rl + TPAD) + 2 * rl * 64) * 2;   // at most 41 KB
   ProfScope ps("k_gated_epilogue", s);
   hipLaunchKernelGGL(k_gated_epilogue, dim3((unsigned)((N + 63) / 64), (unsigned)pl.ngr), dim3(256), lds, s, a);
   return hipGetLastError();

@@ -313,6 +313,7 @@ Shape shape_of(int32_t dim) {
   if (chunks <= 128) return {64, 2};
   if (chunks <= 256) return {64, 4};
   if (chunks <= 512) return {256, 2};
+  if (chunks <= 768) return {256, 3};
   if (chunks <= 1024) return {256, 4};
   if (chunks <= 2048) return {1024, 2};
   return {1024, 4};
@@ -350,6 +351,7 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
   FWD_CASE(64, 2)
   FWD_CASE(64, 4)
   FWD_CASE(256, 2)
+  FWD_CASE(256, 3)
   FWD_CASE(256, 4)
   FWD_CASE(1024, 2)
   FWD_CASE(1024, 4)
@@ -369,6 +371,7 @@ hipError_t launch_rms_norm_bwd(const NormArgs& a, float* dw, hipStream_t s) {
     BWD_CASE(64, 2)
     BWD_CASE(64, 4)
     BWD_CASE(256, 2)
+    BWD_CASE(256, 3)
     BWD_CASE(256, 4)
     BWD_CASE(512, 4)
     NORM_CASE(1024, 4, (k_rms_norm_bwd_long<true>), (k_rms_norm_bwd_long<false>))
