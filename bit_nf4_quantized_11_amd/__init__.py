@@ -724,30 +724,33 @@ def qlora_gated_fwd(X: torch.Tensor, gate: NF4Weight, up: NF4Weight, A_gate: tor
     return _launch(X, stream, run)
 
 
-def qlora_gated_bwd(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, activation: str = "silu",
+def qlora_gated_bwd(dH: torch.Tensor | None, G: torch.Tensor, U: torch.Tensor, activation: str = "silu",
                     H: torch.Tensor | bool = False, dG: torch.Tensor | None = None, dU: torch.Tensor | None = None,
                     stream=None):
     """Gradients of the gated block's G and U from that of H = act(G) U and the saved G, U [M][out]; qlora_linear_bwd of each
-    projection goes on from them.  H: True for H itself again in a new tensor, or a tensor to fill.  Outputs may be the
-    inputs, one each.  Returns (dG, dU, H or None)."""
-    dev, kind = dH.device, _activation(activation)
-    if dH.dim() != 2 or not dH.is_cuda:
-        raise QLoRAError("dH must be [M][out] on the GPU")
-    shape = dH.shape
+    projection goes on from them.  H: True for H itself in a new tensor, or a tensor to fill.  dH None: H alone (which the
+    last projection's backward needs), in place of a kept one.  Outputs may be the inputs, one each.  Returns (dG, dU,
+    H or None)."""
+    dev, kind = G.device, _activation(activation)
+    if G.dim() != 2 or not G.is_cuda:
+        raise QLoRAError("G must be [M][out] on the GPU")
+    shape = G.shape
+    if dH is None and (H is False or dG is not None or dU is not None):
+        raise QLoRAError("without dH there is H alone")
     for t, name in ((dH, "dH"), (G, "G"), (U, "U"), (dG, "dG"), (dU, "dU"), (H, "H")):
         if isinstance(t, torch.Tensor):
             _need(t, torch.bfloat16, dev, name, shape)
 
     def run(stream):
-        new = lambda: torch.empty_like(dH)
-        g = new() if dG is None else dG
-        u = new() if dU is None else dU
+        new = lambda: torch.empty_like(G)
+        g = new() if dG is None and dH is not None else dG
+        u = new() if dU is None and dH is not None else dU
         h = new() if H is True else H if isinstance(H, torch.Tensor) else None
-        _check(lib().qlora_gated_bwd(dH.data_ptr(), G.data_ptr(), U.data_ptr(), shape[0], shape[1], kind, g.data_ptr(),
-                                     u.data_ptr(), _at(h), stream), "qlora_gated_bwd")
+        _check(lib().qlora_gated_bwd(_at(dH), G.data_ptr(), U.data_ptr(), shape[0], shape[1], kind, _at(g), _at(u), _at(h),
+                                     stream), "qlora_gated_bwd")
         return g, u, h
 
-    return _launch(dH, stream, run)
+    return _launch(G, stream, run)
 
 
 _LOGIT_TYPES = {torch.bfloat16: 0, torch.float32: 1}   # qlora_dtype values

@@ -579,10 +579,12 @@ qlora_status qlora_gated_bwd(const uint16_t* dH, const uint16_t* G, const uint16
     return QLORA_ERR_SHAPE;
   if (activation != QLORA_ACT_SILU && activation != QLORA_ACT_GELU) return QLORA_ERR_UNSUPPORTED;
   if (M == 0) return QLORA_OK;
-  if (!dH || !G || !U || !dG || !dU) return QLORA_ERR_NULL;
+  // without a gradient H alone is formed
+  if (!G || !U || (dH == nullptr) != (dG == nullptr) || (dH == nullptr) != (dU == nullptr) || (!dH && !H))
+    return QLORA_ERR_NULL;
   if (!aligned16(dH) || !aligned16(G) || !aligned16(U) || !aligned16(dG) || !aligned16(dU) || !aligned16(H))
     return QLORA_ERR_ALIGN;
-  if (dG == dU || H == dG || H == dU) return QLORA_ERR_SHAPE;
+  if (dH && (dG == dU || H == dG || H == dU)) return QLORA_ERR_SHAPE;
   QL_HIP(launch_gated_bwd(dH, G, U, M * out_features, activation, dG, dU, H, stream));
   return QLORA_OK;
 }

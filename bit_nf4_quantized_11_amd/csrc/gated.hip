@@ -159,12 +159,13 @@ __global__ __launch_bounds__(256) void k_gated_epilogue(EpiArgs a) {
 }
 
 // Bound by HBM: 6 B read and 4 or 6 B written per element.  8 elements a thread.
-template <bool H_OUT>
+// GRAD: dG and dU (else H alone, from 4 B read).
+template <bool GRAD, bool H_OUT>
 __global__ __launch_bounds__(256) void k_gated_bwd(const uint4* dH, const uint4* G, const uint4* U, int64_t n8, int act,
                                                    uint4* dG, uint4* dU, uint4* H) {
   const int64_t step = (int64_t)gridDim.x * 256;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += step) {
-    const uint4 dv = dH[i], gv = G[i], uv = U[i];
+    const uint4 dv = GRAD ? dH[i] : make_uint4(0, 0, 0, 0), gv = G[i], uv = U[i];
     const uint32_t d4[4] = {dv.x, dv.y, dv.z, dv.w}, g4[4] = {gv.x, gv.y, gv.z, gv.w}, u4[4] = {uv.x, uv.y, uv.z, uv.w};
     uint32_t og[4], ou[4], oh[4];
 #pragma unroll
@@ -184,8 +185,10 @@ __global__ __launch_bounds__(256) void k_gated_bwd(const uint4* dH, const uint4*
       ou[j] = pack_bf16x2(u[0], u[1]);
       oh[j] = pack_bf16x2(h[0], h[1]);
     }
-    dG[i] = make_uint4(og[0], og[1], og[2], og[3]);
-    dU[i] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+    if (GRAD) {
+      dG[i] = make_uint4(og[0], og[1], og[2], og[3]);
+      dU[i] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+    }
     if (H_OUT) H[i] = make_uint4(oh[0], oh[1], oh[2], oh[3]);
   }
 }
@@ -210,8 +213,9 @@ hipError_t launch_gated_bwd(const uint16_t* dH, const uint16_t* G, const uint16_
   ProfScope ps("k_gated_bwd", s);
   const auto in = [](const uint16_t* p) { return reinterpret_cast<const uint4*>(p); };
   const auto out = [](uint16_t* p) { return reinterpret_cast<uint4*>(p); };
-  if (H) hipLaunchKernelGGL((k_gated_bwd<true>), g, b, 0, s, in(dH), in(G), in(U), n8, act, out(dG), out(dU), out(H));
-  else hipLaunchKernelGGL((k_gated_bwd<false>), g, b, 0, s, in(dH), in(G), in(U), n8, act, out(dG), out(dU), out(H));
+  if (!dH) hipLaunchKernelGGL((k_gated_bwd<false, true>), g, b, 0, s, in(dH), in(G), in(U), n8, act, out(dG), out(dU), out(H));
+  else if (H) hipLaunchKernelGGL((k_gated_bwd<true, true>), g, b, 0, s, in(dH), in(G), in(U), n8, act, out(dG), out(dU), out(H));
+  else hipLaunchKernelGGL((k_gated_bwd<true, false>), g, b, 0, s, in(dH), in(G), in(U), n8, act, out(dG), out(dU), out(H));
   return hipGetLastError();
 }
 

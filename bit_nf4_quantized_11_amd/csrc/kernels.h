@@ -145,7 +145,7 @@ struct GatedSide {
 };
 hipError_t launch_gated_epilogue(const GatedSide& gate, const GatedSide& up, const GemvPlan& pl, int64_t M, int64_t N,
                                  int64_t r, float scale, int act, uint16_t* H, hipStream_t s);
-// dG = bf16(dH U act'(G)), dU = bf16(dH act(G)), H = bf16(act(G) U) or NULL; n elements, a multiple of 8
+// dG = bf16(dH U act'(G)), dU = bf16(dH act(G)), H = bf16(act(G) U) or NULL; n elements, a multiple of 8.  dH NULL: H alone.
 hipError_t launch_gated_bwd(const uint16_t* dH, const uint16_t* G, const uint16_t* U, int64_t n, int act, uint16_t* dG,
                             uint16_t* dU, uint16_t* H, hipStream_t s);
 

@@ -443,9 +443,10 @@ qlora_status qlora_gated_fwd(const uint16_t* X, int64_t M, const qlora_nf4* gate
                              uint16_t* T_gate, uint16_t* T_up, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* Backward of its activation and product, from the gradient of H and the saved G, U [M][out] (finite):
- *   dG = bf16(dH U act'(G)),   dU = bf16(dH act(G)),   H = bf16(act(G) U) again where H is not NULL
- * (so that the forward's H, the input of the next projection, need not be kept).  qlora_linear_bwd of each projection
- * goes on from dG and dU.  Outputs may be the inputs, one each; no other overlap.
+ *   dG = bf16(dH U act'(G)),   dU = bf16(dH act(G)),   H = bf16(act(G) U) where H is not NULL
+ * qlora_linear_bwd of each projection goes on from dG and dU, and the gradients of X are added.  With dH, dG and dU NULL
+ * H alone is formed: the last projection's backward needs it, so that the forward's H need not be kept (it is that of the rounded G and U,
+ * two bf16 roundings from the forward's).  Outputs may be the inputs, one each; no other overlap.
  * Requires: out_features % 8 == 0, 8 .. 2^22; 0 <= M < 2^26; pointers 16-byte aligned.  M = 0 is a no-op.      */
 qlora_status qlora_gated_bwd(const uint16_t* dH, const uint16_t* G, const uint16_t* U, int64_t M, int64_t out_features,
                              int32_t activation, uint16_t* dG, uint16_t* dU, uint16_t* H, hipStream_t stream);

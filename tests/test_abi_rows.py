@@ -95,6 +95,7 @@ def test_gated_bwd_validation(lib):
     assert f(M=0) == OK and f(M=0, dH=None, G=None, U=None, dG=None, dU=None) == OK
     for name in ("dH", "G", "U", "dG", "dU"):
         assert f(**{name: None}) == NULL
+    assert f(dH=None, dG=None, dU=None) == NULL and f(dH=None, dU=None, H=S) == NULL      # H alone, or all
     assert f(M=-1) == SHAPE and f(M=1 << 26) == SHAPE and f(n=0) == SHAPE and f(n=12) == SHAPE and f(n=(1 << 22) + 8) == SHAPE
     assert f(dG=P, dU=P) == SHAPE and f(H=S) == SHAPE and f(H=P) == SHAPE            # one output twice
     for name in ("dH", "G", "U", "dG", "dU", "H"):

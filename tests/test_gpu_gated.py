@@ -20,8 +20,7 @@ pytestmark = pytest.mark.gpu
 BF16, ACT, E24 = 2.0 ** -8, 2.0 ** -15, 2.0 ** -24
 TINY = 2.0 ** -126   # (values below it are zeros)
 
-# M, in, out, r, activation, codebook, block, double quantization: the three forms (up to 64 tokens; K-slices; whole
-# tiles) with partial tiles, several token groups, odd feature counts and ranks
+# M, in, out, r, activation, codebook, block, double quantization: the forms (up to 64 tokens; K-slices; whole tiles) with partial tiles, several token groups, odd feature counts and ranks
 CASES = [
     (1, 64, 8, 8, "silu", "nf4", 64, True),
     (1, 4096, 136, 16, "silu", "nf4", 64, True),
@@ -38,6 +37,9 @@ CASES = [
     (513, 4096, 72, 64, "silu", "nf4", 256, True),
     (1025, 128, 328, 264 - 8, "gelu", "nf4", 32, False),
     (1100, 320, 1288, 40, "silu", "nf4", 64, True),
+    # more tiles than CUs
+    (2000, 1024, 2296, 72, "silu", "nf4", 64, True),
+    (700, 1088, 7464, 16, "gelu", "fp4", 32, False),
 ]
 
 
@@ -133,6 +135,10 @@ def test_backward(act, shape):
     low = 2.0 ** -120 * np.abs(d)   # (an activation below the smallest normal number)
     assert np.all(np.abs(f64(dU) - d * a) <= (BF16 * 1.01 + ACT) * np.abs(d * a) + low + TINY)
     assert np.all(np.abs(f64(H) - a * u) <= (BF16 * 1.01 + ACT) * np.abs(a * u) + 2.0 ** -120 * np.abs(u) + TINY)
+    again = Q.qlora_gated_bwd(None, G, U, act, H=True)
+    assert again[0] is None and again[1] is None and torch.equal(again[2], H)
+    over = G.clone()
+    assert Q.qlora_gated_bwd(None, over, U, act, H=over)[2] is over and torch.equal(over, H)
     none = Q.qlora_gated_bwd(dH, G, U, act)
     assert none[2] is None and torch.equal(none[0], dG) and torch.equal(none[1], dU)
     # written over the inputs
@@ -201,6 +207,9 @@ def test_binding_refusals():
     for args in ((d.float(), d, d), (d, d[:3], d), (d, d, d.cpu()), (d[0], d[0], d[0]), (d[:, :60], d[:, :60], d[:, :60])):
         with pytest.raises(Q.QLoRAError):
             Q.qlora_gated_bwd(*args)
+    for kw in ({}, {"H": True, "dG": d}, {"H": True, "dU": d}):
+        with pytest.raises(Q.QLoRAError):
+            Q.qlora_gated_bwd(None, d.clone(), d.clone(), **kw)
     for kw in ({"activation": "tanh"}, {"dG": d, "dU": d}, {"H": d, "dU": d}, {"dG": d.float()}):
         with pytest.raises(Q.QLoRAError):
             Q.qlora_gated_bwd(d, d.clone(), d.clone(), **kw)
