@@ -713,7 +713,10 @@ def qlora_gated_fwd(X: torch.Tensor, gate: NF4Weight, up: NF4Weight, A_gate: tor
     def run(stream):
         new = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device=dev)
         out = new(M, d_out) if H is None else H
-        saved = (new(M, d_out), new(M, d_out), new(M, r), new(M, r)) if save else (None,) * 4
+        saved = (None,) * 4
+        if save:
+            T = new(M, r)
+            saved = (torch.empty_like(out), torch.empty_like(out), T, torch.empty_like(T))
         ws = _bytes(workspace, dev, lambda: qlora_gated_workspace(M, d_in, d_out, r))
         g, u = gate.desc(), up.desc()
         _check(lib().qlora_gated_fwd(X.data_ptr(), M, C.byref(g), C.byref(u), A_gate.data_ptr(), B_gate.data_ptr(),

@@ -262,7 +262,8 @@ GatedWs gated_layout(void* base, int64_t M, int64_t in, int64_t out, int32_t r) 
     ws.gv.splits = (int)split_count(in, st);
     ws.gv.tpart = (size_t)ws.gv.splits * Mm * ws.gv.npad;
   }
-  const size_t pf = use_gemv(M) || st ? gemv_partial_floats(ws.gv, Mm) : lora_partial_floats(ws.t);
+  const size_t pf = use_gemv(M) || st ? gemv_partial_floats(ws.gv, Mm)
+                                      : std::max(lora_partial_floats(ws.t), gated_tail(Mm, in, out).part_floats);
   ws.Tg = c.take<uint16_t>((size_t)Mm * rp);
   ws.Tu = c.take<uint16_t>((size_t)Mm * rp);
   ws.gate = c.take<float>(std::max<size_t>(pf, 1));
@@ -569,7 +570,8 @@ qlora_status qlora_gated_fwd(const uint16_t* X, int64_t M, const qlora_nf4* gate
   pu.partial = L.up;
   QL_HIP(launch_lora(pg, &pu, "k_lora_xa", stream));
   if (pg.splits > 1) QL_HIP(launch_lora_reduce(pg, &pu, "k_lora_xa_reduce", stream));
-  QL_HIP(launch_gated_gemm(X, M, in, out, vg, vu, L.Tg, L.Tu, rp, B_gate, B_up, r, activation, H, G, U, stream));
+  QL_HIP(launch_gated_gemm(X, M, in, out, vg, vu, L.Tg, L.Tu, rp, B_gate, B_up, r, activation, H, G, U, L.gate, L.up,
+                           stream));
   return QLORA_OK;
 }
 

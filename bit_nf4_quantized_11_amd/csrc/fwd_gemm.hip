@@ -16,6 +16,8 @@
 // features of a tile are 64 of the gate's weight and the same 64 of the up projection's, so the waves of one feature half
 // hold G and those of the other U, and meet in LDS after the reduction.  X is read once for both, and G and U
 // reach memory only where the backward wants them.
+#include <algorithm>
+
 #include "common.h"
 #include "gated.h"
 #include "gemm_core.h"
@@ -50,6 +52,9 @@ struct FwdParams {
   uint16_t* G;   // or NULL, with U
   uint16_t* U;
   int act;
+  // gated: tiles from `whole` on are cut into `slices` of the reduction, fp32 sums to partial, partial2
+  // [slice][256][npad] (GatedTail in kernels.h)
+  uint32_t whole, slices;
 };
 
 struct WRegs {
@@ -70,7 +75,8 @@ struct Stage {
 // fp32 partial sums (few tokens: the K-slices give the GPU enough workgroups); the adapter
 // term and the final sum come from the weight-streaming path's epilogue.
 // GATED: a tile has 64 features of each of two weights (p.w, p.w2); see above.
-template <bool DQ, int BM, bool SPLIT, bool GATED>
+// TAIL: the last tiles are cut into slices (GatedTail).
+template <bool DQ, int BM, bool SPLIT, bool GATED, bool TAIL>
 __global__ __launch_bounds__(NT) void k_fwd_nf4_gemm(FwdParams p) {
   __shared__ __attribute__((aligned(16))) uint16_t smem[SMEM_ELEMS];
   uint16_t* const sT[2] = {smem, smem + TILE_T};
@@ -80,11 +86,29 @@ __global__ __launch_bounds__(NT) void k_fwd_nf4_gemm(FwdParams p) {
   constexpr int FT = GATED ? BF / 2 : BF;   // features of a tile
   const int64_t tiles_t = (p.M + BT - 1) / BT, tiles_f = (p.N + FT - 1) / FT;
   const uint32_t split = SPLIT ? (uint32_t)(blockIdx.x / (tiles_t * tiles_f)) : 0u;
-  tile_of(tiles_t, tiles_f, tt, tf, SPLIT ? (int64_t)blockIdx.x - (int64_t)split * tiles_t * tiles_f : -1);
+  uint32_t part = 0;   // slice of a tile at the end of the launch
+  bool tail = false;
+  if constexpr (TAIL) {
+    tail = blockIdx.x >= p.whole;
+    if (tail) {
+      const uint32_t n = (uint32_t)(tiles_t * tiles_f) - p.whole, i = blockIdx.x - p.whole;
+      part = i / n;
+      tt = tiles_t - 1;
+      tf = tiles_f - n + (i - part * n);
+    } else {
+      // the tiles before them, a multiple of 256, in runs of one XCD each (see tile_of)
+      const uint32_t L = (blockIdx.x & 7) * (p.whole >> 3) + (blockIdx.x >> 3);
+      tt = L / tiles_f;
+      tf = L - tt * tiles_f;
+    }
+  } else {
+    tile_of(tiles_t, tiles_f, tt, tf, SPLIT ? (int64_t)blockIdx.x - (int64_t)split * tiles_t * tiles_f : -1);
+  }
   const uint32_t m0 = (uint32_t)(tt * BT), n0 = (uint32_t)(tf * FT);
   const uint32_t nkb_all = (uint32_t)(p.K / 64);
-  const uint32_t it0 = SPLIT ? split * p.spl : 0u;                       // first stage
-  const uint32_t nkb = SPLIT ? min(nkb_all, it0 + p.spl) - it0 : nkb_all;   // stages of this workgroup
+  const uint32_t it0 = SPLIT ? split * p.spl : tail ? part * nkb_all / p.slices : 0u;   // first stage
+  const uint32_t nkb = SPLIT ? min(nkb_all, it0 + p.spl) - it0                           // stages of this workgroup
+                             : (tail ? (part + 1) * nkb_all / p.slices : nkb_all) - it0;
   const int t = threadIdx.x;
   // weight row t/4 of the tile, quarter t%4 of its block (groups 2q and 2q+1 -> chunks
   // 2q, 2q+1 of the LDS row); rows past N read as zero (their outputs are not stored)
@@ -217,7 +241,7 @@ __global__ __launch_bounds__(NT) void k_fwd_nf4_gemm(FwdParams p) {
   const uint64_t bbytes = (uint64_t)p.r * p.N * 2;
   const rsrc_t rB = make_rsrc(p.B, bbytes);
   const int bj = t >> 3, be = t & 7;
-  for (uint32_t j0 = 0; j0 < (uint32_t)p.rp; j0 += 64) {
+  for (uint32_t j0 = part ? (uint32_t)p.rp : 0u; j0 < (uint32_t)p.rp; j0 += 64) {   // (a tile's first slice takes them)
     TokenRegs T;
     load_tokens(T, ts, j0);
     uint4 b0, b1;
@@ -249,6 +273,15 @@ __global__ __launch_bounds__(NT) void k_fwd_nf4_gemm(FwdParams p) {
     if (combine_halves(acc, smem)) store_out(acc, p.Y, p.N, m0, p.M, n0, p.N);
   } else {
     const bool holds = combine_halves(acc, smem);
+    if (tail) {
+      if (holds) {
+        const int64_t rows = min<int64_t>(BT, p.M - m0), left = p.N - n0;
+        const int64_t c0 = n0 - (tiles_f - (tiles_t * tiles_f - p.whole)) * FT;   // column of the tail
+        float* const out = (wave_f() ? p.partial2 : p.partial) + (int64_t)part * BT * p.npad;
+        store_out_f32(acc, out, p.npad, 0, rows, c0 - wave_f() * 64, c0 + min<int64_t>(left, FT));
+      }
+      return;
+    }
     // the wave of G keeps features 0 .. 31 of the tile and takes U's from the wave of U, which keeps 32 .. 63
     const int lane = t & 63, q = wave_id() & 3, wf = wave_f();
     float4* const x = reinterpret_cast<float4*>(smem);
@@ -293,18 +326,18 @@ __global__ __launch_bounds__(NT) void k_fwd_nf4_gemm(FwdParams p) {
   }
 }
 
-template <bool SPLIT, bool GATED>
+template <bool SPLIT, bool GATED, bool TAIL = false>
 void launch_variant(const FwdParams& p, unsigned wgs, hipStream_t s) {
   const dim3 grid(wgs), block(NT);
   const int bm = p.w.bshift == 6 ? 0 : p.w.bshift > 6 ? 1 : 2;
   if (p.w.dq) {
-    if (bm == 0) hipLaunchKernelGGL((k_fwd_nf4_gemm<true, 0, SPLIT, GATED>), grid, block, 0, s, p);
-    else if (bm == 1) hipLaunchKernelGGL((k_fwd_nf4_gemm<true, 1, SPLIT, GATED>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((k_fwd_nf4_gemm<true, 2, SPLIT, GATED>), grid, block, 0, s, p);
+    if (bm == 0) hipLaunchKernelGGL((k_fwd_nf4_gemm<true, 0, SPLIT, GATED, TAIL>), grid, block, 0, s, p);
+    else if (bm == 1) hipLaunchKernelGGL((k_fwd_nf4_gemm<true, 1, SPLIT, GATED, TAIL>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((k_fwd_nf4_gemm<true, 2, SPLIT, GATED, TAIL>), grid, block, 0, s, p);
   } else {
-    if (bm == 0) hipLaunchKernelGGL((k_fwd_nf4_gemm<false, 0, SPLIT, GATED>), grid, block, 0, s, p);
-    else if (bm == 1) hipLaunchKernelGGL((k_fwd_nf4_gemm<false, 1, SPLIT, GATED>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((k_fwd_nf4_gemm<false, 2, SPLIT, GATED>), grid, block, 0, s, p);
+    if (bm == 0) hipLaunchKernelGGL((k_fwd_nf4_gemm<false, 0, SPLIT, GATED, TAIL>), grid, block, 0, s, p);
+    else if (bm == 1) hipLaunchKernelGGL((k_fwd_nf4_gemm<false, 1, SPLIT, GATED, TAIL>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((k_fwd_nf4_gemm<false, 2, SPLIT, GATED, TAIL>), grid, block, 0, s, p);
   }
 }
 
@@ -353,9 +386,21 @@ hipError_t launch_fwd_gemm_split(const uint16_t* X, int64_t M, int64_t K, int64_
   return hipGetLastError();
 }
 
+GatedTail gated_tail(int64_t M, int64_t K, int64_t N) {
+  GatedTail t{0, 0, 0, 0};
+  const int64_t tiles_f = (N + BF / 2 - 1) / (BF / 2), tiles = (M + BT - 1) / BT * tiles_f, rest = tiles % 256;
+  if (tiles < 256 || rest == 0 || rest > 128 || rest > tiles_f || K / 64 < 16) return t;
+  t.tiles = (int)rest;
+  t.slices = (int)std::min<int64_t>(256 / rest, 4);
+  t.npad = rest * (BF / 2);
+  t.part_floats = (size_t)t.slices * BT * t.npad;
+  return t;
+}
+
 hipError_t launch_gated_gemm(const uint16_t* X, int64_t M, int64_t K, int64_t N, const NF4View& gate, const NF4View& up,
                              const uint16_t* Tg, const uint16_t* Tu, int64_t rp, const uint16_t* Bg, const uint16_t* Bu,
-                             int64_t r, int act, uint16_t* H, uint16_t* G, uint16_t* U, hipStream_t s) {
+                             int64_t r, int act, uint16_t* H, uint16_t* G, uint16_t* U, float* gate_partial, float* up_partial,
+                             hipStream_t s) {
   FwdParams p = params_of(X, M, K, N, gate);
   p.w2 = up;
   p.Ts = Tg;
@@ -368,9 +413,22 @@ hipError_t launch_gated_gemm(const uint16_t* X, int64_t M, int64_t K, int64_t N,
   p.Y = H;
   p.G = G;
   p.U = U;
-  ProfScope ps("k_gated_nf4_gemm", s);
-  launch_variant<false, true>(p, (unsigned)(((M + BT - 1) / BT) * ((N + BF / 2 - 1) / (BF / 2))), s);
-  return hipGetLastError();
+  const GatedTail tail = gated_tail(M, K, N);
+  const int64_t tiles_f = (N + BF / 2 - 1) / (BF / 2), tiles = (M + BT - 1) / BT * tiles_f;
+  p.whole = (uint32_t)(tiles - tail.tiles);
+  p.slices = (uint32_t)std::max(tail.slices, 1);
+  p.partial = gate_partial;
+  p.partial2 = up_partial;
+  p.npad = tail.npad;
+  {
+    ProfScope ps("k_gated_nf4_gemm", s);
+    if (tail.tiles) launch_variant<false, true, true>(p, p.whole + (unsigned)(tail.tiles * tail.slices), s);
+    else launch_variant<false, true>(p, p.whole, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || tail.tiles == 0) return e;
+  }
+  return launch_gated_finish(gate_partial, up_partial, tail, M, N, (M - 1) / BT * BT, (tiles_f - tail.tiles) * (BF / 2), act, H,
+                             G, U, s);
 }
 
 hipError_t launch_gated_gemm_split(const uint16_t* X, int64_t M, int64_t K, int64_t N, const NF4View& gate, const NF4View& up,

@@ -158,6 +158,39 @@ __global__ __launch_bounds__(256) void k_gated_epilogue(EpiArgs a) {
   }
 }
 
+// The tiles that the large forward left in slices: their sums in slice order, then activation and product.  4 features a
+// thread; bound by memory (8 B read per slice and output, mostly from the caches, where they have just been written).
+__global__ __launch_bounds__(256) void k_gated_finish(const float* gate, const float* up, int slices, int64_t npad, int64_t rows,
+                                                      int64_t N, int64_t m0, int64_t n0, int act, uint16_t* H, uint16_t* G,
+                                                      uint16_t* U) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per_row = npad / 4;
+  const int64_t m = i / per_row, c = (i - m * per_row) * 4, n = n0 + c;
+  if (m >= rows || n >= N) return;
+  const int64_t slice = 256 * npad, at = m * npad + c;
+  f32x4 v[2][4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int64_t o = min(u, slices - 1) * slice + at;
+    v[0][u] = *reinterpret_cast<const f32x4*>(gate + o);
+    v[1][u] = *reinterpret_cast<const f32x4*>(up + o);
+  }
+#pragma unroll
+  for (int u = 1; u < 4; ++u)
+    if (u < slices) {
+      v[0][0] += v[0][u];
+      v[1][0] += v[1][u];
+    }
+  float h[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) h[j] = activate(v[0][0][j], act) * v[1][0][j];
+  const int64_t o = (m0 + m) * N + n;
+  *reinterpret_cast<uint2*>(H + o) = make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
+  if (G) {
+    *reinterpret_cast<uint2*>(G + o) = make_uint2(pack_bf16x2(v[0][0][0], v[0][0][1]), pack_bf16x2(v[0][0][2], v[0][0][3]));
+    *reinterpret_cast<uint2*>(U + o) = make_uint2(pack_bf16x2(v[1][0][0], v[1][0][1]), pack_bf16x2(v[1][0][2], v[1][0][3]));
+  }
+}
+
 // Bound by HBM: 6 B read and 4 or 6 B written per element.  8 elements a thread.
 // GRAD: dG and dU (else H alone, from 4 B read).
 template <bool GRAD, bool H_OUT>
@@ -203,6 +236,15 @@ hipError_t launch_gated_epilogue(const GatedSide& gate, const GatedSide& up, con
   const size_t lds = (size_t)(2 * 16 * (rl + TPAD) + 2 * rl * 64) * 2;   // at most 41 KB
   ProfScope ps("k_gated_epilogue", s);
   hipLaunchKernelGGL(k_gated_epilogue, dim3((unsigned)((N + 63) / 64), (unsigned)pl.ngr), dim3(256), lds, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_finish(const float* gate_partial, const float* up_partial, const GatedTail& tail, int64_t M, int64_t N,
+                               int64_t m0, int64_t n0, int act, uint16_t* H, uint16_t* G, uint16_t* U, hipStream_t s) {
+  const int64_t rows = M - m0, wgs = (rows * (tail.npad / 4) + 255) / 256;
+  ProfScope ps("k_gated_finish", s);
+  hipLaunchKernelGGL(k_gated_finish, dim3((unsigned)wgs), dim3(256), 0, s, gate_partial, up_partial, tail.slices, tail.npad, rows,
+                     N, m0, n0, act, H, G, U);
   return hipGetLastError();
 }
 

@@ -131,9 +131,22 @@ hipError_t launch_gemv_epilogue(const float* partial, const GemvPlan& pl, int64_
 
 // ---- gated block (fwd_gemm.hip, gated.hip): H = bf16(act(G) U), G and U two products as above of one X and two weights of
 // one format.  act: qlora_activation.  G, U in bf16 where wanted (both or neither).
+// A tile takes a CU for the whole reduction, so the tiles past a multiple of 256 would leave most CUs idle for as long as
+// 256 take: up to 128 of them, at the end of the last token panel, are cut into slices instead, fp32 sums
+// [slice][256][npad] per side, which a last launch joins.
+struct GatedTail {
+  int tiles, slices;    // 0: none
+  int64_t npad;
+  size_t part_floats;   // of each side
+};
+GatedTail gated_tail(int64_t M, int64_t K, int64_t N);
 hipError_t launch_gated_gemm(const uint16_t* X, int64_t M, int64_t K, int64_t N, const NF4View& gate, const NF4View& up,
                              const uint16_t* Tg, const uint16_t* Tu, int64_t rp, const uint16_t* Bg, const uint16_t* Bu,
-                             int64_t r, int act, uint16_t* H, uint16_t* G, uint16_t* U, hipStream_t s);
+                             int64_t r, int act, uint16_t* H, uint16_t* G, uint16_t* U, float* gate_partial, float* up_partial,
+                             hipStream_t s);
+// H, G, U of rows m0 .. and features n0 .. from a tail's sums
+hipError_t launch_gated_finish(const float* gate_partial, const float* up_partial, const GatedTail& tail, int64_t M, int64_t N,
+                               int64_t m0, int64_t n0, int act, uint16_t* H, uint16_t* G, uint16_t* U, hipStream_t s);
 hipError_t launch_gated_gemm_split(const uint16_t* X, int64_t M, int64_t K, int64_t N, const NF4View& gate, const NF4View& up,
                                    int stages, float* gate_partial, float* up_partial, int64_t npad, hipStream_t s);
 // the epilogue of both few-token forms: partials of the two sides as launch_gemv and launch_gated_gemm_split leave them

@@ -190,6 +190,51 @@ def test_nan_infinity_and_wrong_tokens():
             assert g[[1, 3, 4]].isnan().all() and torch.all(g[5] == 0) and g[0].isfinite().all() and g[2, 9].isnan()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+def test_masks_of_the_lowest_value_and_infinite_products(dtype):
+    """A mask of the type's lowest number: beside other logits it has probability 0; a whole row of it is uniform, and with
+    a scale that makes it -infinity in fp32 a row of nothing.  A logit whose product is +infinity makes its row NaN."""
+    require_gpu()
+    low = torch.finfo(dtype).min
+    for n, v in ((4, 100), (4, 40000), (200, 20000)):
+        x = torch.randn(n, v, generator=torch.Generator().manual_seed(v)).to(dtype)
+        x[0] = low
+        x[1, ::2] = low
+        x[2, 7] = -low
+        x = x.cuda()
+        token = torch.full((n,), 1, device="cuda")
+        lp, stats, ent, tlp, tix = Q.qlora_token_logprob(x, token, entropy=True, top=3)
+        assert abs(lp[0].item() + math.log(v)) < 1e-4 and abs(ent[0].item() - math.log(v)) < 1e-4 and stats[0, 1] == v
+        assert tix[0].tolist() == [0, 1, 2] and tix[2, 0] == 7
+        want = oracle.token_logprob(_f64(x[1:2])[:, 1::2], np.array([0]), 1.0, 0)
+        assert abs(lp[1].item() - want[0][0]) < 1e-4 and abs(ent[1].item() - want[3][0]) < 1e-3
+        assert lp[2] == -math.inf or lp[2].item() < -1e38       # (the given token beside one that is everything)
+        g = Q.qlora_token_logprob_bwd(x, token, stats, torch.ones(n, device="cuda"), ent, torch.ones(n, device="cuda"))
+        assert g[[0, 1]].isfinite().all() and torch.all(g[1, ::2] == 0)
+        lp, stats, ent, tlp, tix = Q.qlora_token_logprob(x, token, 2.0, entropy=True, top=3)
+        assert lp[0] == -math.inf and ent[0] == 0 and stats[0, 0] == -math.inf and stats[0, 1] == 0 and torch.all(tlp[0] == -math.inf)
+        assert lp[1].isfinite() and lp[2].isnan() and ent[2].isnan()
+        g = Q.qlora_token_logprob_bwd(x, token, stats, torch.ones(n, device="cuda"), ent, torch.ones(n, device="cuda"), 2.0)
+        assert torch.all(g[0] == 0) and g[1].isfinite().all() and g[2].isnan().any()
+
+
+def test_rows_past_32_bit_offsets():
+    """Rows 2^31 + 40 elements apart: the last one lies 8.6 GB behind the first."""
+    require_gpu()
+    v, stride = 3000, (1 << 31) + 40
+    buf = torch.zeros(2 * stride + v, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((3, v), (stride, 1))
+    small = torch.randn(3, v, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    x.copy_(small)
+    token = torch.tensor([0, 5, v - 1], device="cuda")
+    a, b = Q.qlora_token_logprob(x, token, entropy=True, top=4), Q.qlora_token_logprob(small, token, entropy=True, top=4)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    d = torch.randn(3, device="cuda")
+    want = Q.qlora_token_logprob_bwd(small, token, b[1], d)
+    assert Q.qlora_token_logprob_bwd(x, token, b[1], d, out=x) is x and torch.equal(x, want)
+    assert buf[v:stride].abs().max() == 0 and buf[stride + v:2 * stride].abs().max() == 0
+
+
 def test_difference():
     """The gradient against differences of the forward: float32 logits, a step of 2^-7 along a random direction; the values
     are exact to 2^-16 (module's head), so the quotient to 2^-8 per row, and the curvature adds 2^-13."""

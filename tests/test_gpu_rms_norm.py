@@ -120,6 +120,25 @@ def test_strides_in_place_and_repeated():
     assert torch.all(wide[:, :8] == 7) and torch.all(wide[:, 8 + dim:] == 7)
 
 
+def test_rows_past_32_bit_offsets():
+    """Rows 2^31 + 40 elements apart: the last one lies 8.6 GB behind the first."""
+    require_gpu()
+    dim, stride = 1000, (1 << 31) + 40
+    buf = torch.zeros(2 * stride + dim, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((3, dim), (stride, 1))
+    small, r, dy = (_t(i, (3, dim)) for i in (1, 2, 3))
+    w = _weight(4, dim)
+    x.copy_(small)
+    want, h = Q.qlora_rms_norm(small, w, r)
+    assert torch.equal(Q.qlora_rms_norm(x, w, r)[0], want)
+    Q.qlora_rms_norm(small, w, r, sum_out=x)
+    assert torch.equal(x, h)
+    dx, dw = Q.qlora_rms_norm_bwd(dy, h, w)
+    got = Q.qlora_rms_norm_bwd(dy, x, w, dx=x)
+    assert torch.equal(x, dx) and torch.equal(got[1], dw)
+    assert buf[dim:stride].abs().max() == 0 and buf[stride + dim:2 * stride].abs().max() == 0
+
+
 def test_no_rows_and_special_values():
     require_gpu()
     dim = 256
