@@ -711,11 +711,11 @@ def qlora_gated_fwd(X: torch.Tensor, gate: NF4Weight, up: NF4Weight, A_gate: tor
         _need(H, torch.bfloat16, dev, "H", (M, d_out))
 
     def run(stream):
-        new = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        out = new(M, d_out) if H is None else H
+        new = X.new_empty
+        out = new((M, d_out)) if H is None else H
         saved = (None,) * 4
         if save:
-            T = new(M, r)
+            T = new((M, r))
             saved = (torch.empty_like(out), torch.empty_like(out), T, torch.empty_like(T))
         ws = _bytes(workspace, dev, lambda: qlora_gated_workspace(M, d_in, d_out, r))
         g, u = gate.desc(), up.desc()
@@ -787,12 +787,12 @@ def qlora_token_logprob(logits: torch.Tensor, token: torch.Tensor | None, scale:
         _need(token, torch.int64, dev, "token", (rows,))
 
     def run(stream):
-        new = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)
-        lp = None if token is None else new(rows)
-        stats = new(rows, 2)
-        ent = new(rows) if entropy else None
-        tlp = new(rows, top) if top else None
-        tix = torch.empty((rows, top), dtype=torch.int64, device=dev) if top else None
+        new, f32 = logits.new_empty, torch.float32
+        lp = None if token is None else new((rows,), dtype=f32)
+        stats = new((rows, 2), dtype=f32)
+        ent = new((rows,), dtype=f32) if entropy else None
+        tlp = new((rows, top), dtype=f32) if top else None
+        tix = new((rows, top), dtype=torch.int64) if top else None
         ws = _bytes(workspace, dev, lambda: qlora_token_logprob_workspace(rows, vocab, top))
         _check(lib().qlora_token_logprob(px, sx, rows, vocab, kind, _at(token), scale, top, _at(lp), stats.data_ptr(),
                                          _at(ent), _at(tlp), _at(tix), ws.data_ptr(), ws.nbytes, stream),

@@ -257,7 +257,10 @@ GatedWs gated_layout(void* base, int64_t M, int64_t in, int64_t out, int32_t r) 
   GatedWs ws;
   ws.t = lora_problem(gemm_T(nullptr, nullptr, Mm, in, r), epi_none(), kMaxSplits);
   const int64_t st = gated_split_stages(M, in, out);
-  ws.gv = gemv_plan(Mm, in, out, rp, st != 0, true);
+  // X A beside the K-slices: on the CUs that these leave (200 tokens of 1024 -> 2816: 15.9 us against 18.1), or, where these are
+  // few, in pieces so short that every CU takes one first (100 tokens of 4096 -> 4096: 36 us a call against 47)
+  const int64_t left = 256 - (Mm + 255) / 256 * ((out + 63) / 64) * split_count(in, std::max<int64_t>(st, 1));
+  ws.gv = gemv_plan(Mm, in, out, rp, st != 0, true, left >= 64 ? left : 256);
   if (st) {
     ws.gv.splits = (int)split_count(in, st);
     ws.gv.tpart = (size_t)ws.gv.splits * Mm * ws.gv.npad;
@@ -555,11 +558,13 @@ qlora_status qlora_gated_fwd(const uint16_t* X, int64_t M, const qlora_nf4* gate
   const NF4View vg = view_of(gate), vu = view_of(up);
   const int64_t stages = gated_split_stages(M, in, out);
   if (use_gemv(M) || stages) {
-    // few tokens: one pass over both packed weights that also forms the partials of X A; or, where the tiles are few, X A's
-    // partials alone and the products in K-slices; then the epilogue
+    // few tokens: one pass over both packed weights, or, where the tiles are few, the products in K-slices; either forms the
+    // partials of X A too; then the epilogue
     const GemvUp side{vu, A_up, L.up};
-    QL_HIP(launch_gemv(X, M, in, out, vg, A_gate, r, L.gv, L.gate, stream, stages != 0, &side));
-    if (stages) QL_HIP(launch_gated_gemm_split(X, M, in, out, vg, vu, (int)stages, L.gate, L.up, L.gv.npad, stream));
+    if (stages)
+      QL_HIP(launch_gated_gemm_split(X, M, in, out, vg, vu, A_gate, A_up, r, L.gv, (int)stages, L.gate, L.up, stream));
+    else
+      QL_HIP(launch_gemv(X, M, in, out, vg, A_gate, r, L.gv, L.gate, stream, false, &side));
     QL_HIP(launch_gated_epilogue(GatedSide{L.gate, B_gate, G, T_gate}, GatedSide{L.up, B_up, U, T_up}, L.gv, M, out, r, scale,
                                  activation, H, stream));
     return QLORA_OK;

@@ -20,6 +20,7 @@
 
 #include "common.h"
 #include "gated.h"
+#include "gemv.h"
 #include "gemm_core.h"
 #include "kernels.h"
 
@@ -77,32 +78,31 @@ struct Stage {
 // GATED: a tile has 64 features of each of two weights (p.w, p.w2); see above.
 // TAIL: the last tiles are cut into slices (GatedTail).
 template <bool DQ, int BM, bool SPLIT, bool GATED, bool TAIL>
-__global__ __launch_bounds__(NT) void k_fwd_nf4_gemm(FwdParams p) {
-  __shared__ __attribute__((aligned(16))) uint16_t smem[SMEM_ELEMS];
+__device__ __forceinline__ void gemm_workgroup(const FwdParams& p, uint32_t bid, uint16_t* smem) {
   uint16_t* const sT[2] = {smem, smem + TILE_T};
   uint16_t* const sF[2] = {smem + 2 * TILE_T, smem + 2 * TILE_T + TILE_F};
 
   int64_t tt, tf;
   constexpr int FT = GATED ? BF / 2 : BF;   // features of a tile
   const int64_t tiles_t = (p.M + BT - 1) / BT, tiles_f = (p.N + FT - 1) / FT;
-  const uint32_t split = SPLIT ? (uint32_t)(blockIdx.x / (tiles_t * tiles_f)) : 0u;
+  const uint32_t split = SPLIT ? (uint32_t)(bid / (tiles_t * tiles_f)) : 0u;
   uint32_t part = 0;   // slice of a tile at the end of the launch
   bool tail = false;
   if constexpr (TAIL) {
-    tail = blockIdx.x >= p.whole;
+    tail = bid >= p.whole;
     if (tail) {
-      const uint32_t n = (uint32_t)(tiles_t * tiles_f) - p.whole, i = blockIdx.x - p.whole;
+      const uint32_t n = (uint32_t)(tiles_t * tiles_f) - p.whole, i = bid - p.whole;
       part = i / n;
       tt = tiles_t - 1;
       tf = tiles_f - n + (i - part * n);
     } else {
       // the tiles before them, a multiple of 256, in runs of one XCD each (see tile_of)
-      const uint32_t L = (blockIdx.x & 7) * (p.whole >> 3) + (blockIdx.x >> 3);
+      const uint32_t L = (bid & 7) * (p.whole >> 3) + (bid >> 3);
       tt = L / tiles_f;
       tf = L - tt * tiles_f;
     }
   } else {
-    tile_of(tiles_t, tiles_f, tt, tf, SPLIT ? (int64_t)blockIdx.x - (int64_t)split * tiles_t * tiles_f : -1);
+    tile_of(tiles_t, tiles_f, tt, tf, (int64_t)bid - (int64_t)split * tiles_t * tiles_f);
   }
   const uint32_t m0 = (uint32_t)(tt * BT), n0 = (uint32_t)(tf * FT);
   const uint32_t nkb_all = (uint32_t)(p.K / 64);
@@ -326,6 +326,31 @@ __global__ __launch_bounds__(NT) void k_fwd_nf4_gemm(FwdParams p) {
   }
 }
 
+template <bool DQ, int BM, bool SPLIT, bool GATED, bool TAIL>
+__global__ __launch_bounds__(NT) void k_fwd_nf4_gemm(FwdParams p) {
+  __shared__ __attribute__((aligned(16))) uint16_t smem[SMEM_ELEMS];
+  gemm_workgroup<DQ, BM, SPLIT, GATED, TAIL>(p, blockIdx.x, smem);
+}
+
+// The gated block's products in K-slices, and in front of them the workgroups that form the partial sums of X A for both
+// sides (a launch of their own takes 4.6 us of a call of 27).
+static_assert(gemv::kLdsAdapter <= SMEM_ELEMS * 2 && gemv::GT == NT, "both kinds of workgroups in one launch");
+template <bool DQ, int BM>
+__global__ __launch_bounds__(NT) void k_gated_nf4_split(FwdParams p, gemv::GemvParams a, gemv::GemvSide up, uint32_t adapters) {
+  __shared__ __attribute__((aligned(16))) uint16_t smem[SMEM_ELEMS];
+  if (blockIdx.x >= 2 * adapters) {
+    gemm_workgroup<DQ, BM, true, true, false>(p, blockIdx.x - 2 * adapters, smem);
+    return;
+  }
+  uint32_t bid = blockIdx.x;
+  if (bid >= adapters) {
+    bid -= adapters;
+    a.A = up.A;
+    a.tpartial = up.tpartial;
+  }
+  gemv::adapter_group(a, (int)bid, reinterpret_cast<uint8_t*>(smem));
+}
+
 template <bool SPLIT, bool GATED, bool TAIL = false>
 void launch_variant(const FwdParams& p, unsigned wgs, hipStream_t s) {
   const dim3 grid(wgs), block(NT);
@@ -432,16 +457,32 @@ hipError_t launch_gated_gemm(const uint16_t* X, int64_t M, int64_t K, int64_t N,
 }
 
 hipError_t launch_gated_gemm_split(const uint16_t* X, int64_t M, int64_t K, int64_t N, const NF4View& gate, const NF4View& up,
-                                   int stages, float* gate_partial, float* up_partial, int64_t npad, hipStream_t s) {
+                                   const uint16_t* A_gate, const uint16_t* A_up, int64_t r, const GemvPlan& pl, int stages,
+                                   float* gate_partial, float* up_partial, hipStream_t s) {
   FwdParams p = params_of(X, M, K, N, gate);
   p.w2 = up;
   p.partial = gate_partial;
   p.partial2 = up_partial;
-  p.npad = npad;
+  p.npad = pl.npad;
   p.spl = (uint32_t)stages;
-  const int64_t used = (K / 64 + stages - 1) / stages;
-  ProfScope ps("k_gated_nf4_gemm", s);
-  launch_variant<true, true>(p, (unsigned)(((M + BT - 1) / BT) * ((N + BF / 2 - 1) / (BF / 2)) * used), s);
+  const gemv::GemvParams a = gemv::gemv_params(X, M, K, N, gate, A_gate, r, pl, gate_partial);
+  gemv::GemvSide side{};
+  side.A = A_up;
+  side.tpartial = up_partial + pl.tpart;
+  const int64_t used = (K / 64 + stages - 1) / stages, tiles = ((M + BT - 1) / BT) * ((N + BF / 2 - 1) / (BF / 2));
+  const uint32_t adapters = (uint32_t)(pl.agroups * pl.asplits * pl.ngr);
+  const int bm = gate.bshift == 6 ? 0 : gate.bshift > 6 ? 1 : 2;
+  const dim3 g((unsigned)(tiles * used) + 2 * adapters), b(NT);
+  ProfScope ps("k_gated_nf4_split", s);
+  if (gate.dq) {
+    if (bm == 0) hipLaunchKernelGGL((k_gated_nf4_split<true, 0>), g, b, 0, s, p, a, side, adapters);
+    else if (bm == 1) hipLaunchKernelGGL((k_gated_nf4_split<true, 1>), g, b, 0, s, p, a, side, adapters);
+    else hipLaunchKernelGGL((k_gated_nf4_split<true, 2>), g, b, 0, s, p, a, side, adapters);
+  } else {
+    if (bm == 0) hipLaunchKernelGGL((k_gated_nf4_split<false, 0>), g, b, 0, s, p, a, side, adapters);
+    else if (bm == 1) hipLaunchKernelGGL((k_gated_nf4_split<false, 1>), g, b, 0, s, p, a, side, adapters);
+    else hipLaunchKernelGGL((k_gated_nf4_split<false, 2>), g, b, 0, s, p, a, side, adapters);
+  }
   return hipGetLastError();
 }
 

@@ -113,7 +113,8 @@ struct GemvPlan {
   int tg;                     // token groups each weight lane feeds (1, 2 or 4 >= ngr)
   size_t tpart;               // float offset of the adapter partials
 };
-GemvPlan gemv_plan(int64_t M, int64_t K, int64_t N, int64_t rp, bool adapters_only = false, bool gated = false);
+GemvPlan gemv_plan(int64_t M, int64_t K, int64_t N, int64_t rp, bool adapters_only = false, bool gated = false,
+                   int64_t room = 0);
 size_t gemv_partial_floats(const GemvPlan& pl, int64_t M);
 // adapters_only: launch only the X A workgroups (their partials feed the epilogue after the
 // split large-M forward)
@@ -147,8 +148,10 @@ hipError_t launch_gated_gemm(const uint16_t* X, int64_t M, int64_t K, int64_t N,
 // H, G, U of rows m0 .. and features n0 .. from a tail's sums
 hipError_t launch_gated_finish(const float* gate_partial, const float* up_partial, const GatedTail& tail, int64_t M, int64_t N,
                                int64_t m0, int64_t n0, int act, uint16_t* H, uint16_t* G, uint16_t* U, hipStream_t s);
+// K-slices of `stages` 64-deep stages, and the partial sums of X A for both sides, in one launch
 hipError_t launch_gated_gemm_split(const uint16_t* X, int64_t M, int64_t K, int64_t N, const NF4View& gate, const NF4View& up,
-                                   int stages, float* gate_partial, float* up_partial, int64_t npad, hipStream_t s);
+                                   const uint16_t* A_gate, const uint16_t* A_up, int64_t r, const GemvPlan& pl, int stages,
+                                   float* gate_partial, float* up_partial, hipStream_t s);
 // the epilogue of both few-token forms: partials of the two sides as launch_gemv and launch_gated_gemm_split leave them
 struct GatedSide {
   const float* partial;
