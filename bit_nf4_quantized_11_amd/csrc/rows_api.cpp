@@ -36,6 +36,11 @@ qlora_status check_rows(const uint16_t* p, int64_t stride, int64_t rows, int32_t
   return stride % 8 == 0 ? QLORA_OK : QLORA_ERR_ALIGN;
 }
 
+// Output rows that begin where input rows do are those rows: with another stride they would overlap others.
+bool in_place_ok(const void* out, int64_t out_stride, const void* in, int64_t in_stride, int64_t rows) {
+  return out != in || out_stride == in_stride || rows <= 1;
+}
+
 RowsView view(const uint16_t* p, int64_t stride) { return RowsView{const_cast<uint16_t*>(p), stride}; }
 
 bool dtype_ok(int32_t d) { return d == QLORA_BF16 || d == QLORA_FP32; }
@@ -89,7 +94,11 @@ qlora_status qlora_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t*
     if ((st = check_rows(residual, residual_stride, rows, dim, false)) != QLORA_OK) return st;
     if ((st = check_rows(sum, sum_stride, rows, dim, true)) != QLORA_OK) return st;
     if (rows > 0 && y == sum) return QLORA_ERR_SHAPE;
+    if (!in_place_ok(y, y_stride, residual, residual_stride, rows) || !in_place_ok(sum, sum_stride, x, x_stride, rows) ||
+        !in_place_ok(sum, sum_stride, residual, residual_stride, rows))
+      return QLORA_ERR_SHAPE;
   }
+  if (!in_place_ok(y, y_stride, x, x_stride, rows)) return QLORA_ERR_SHAPE;
   if (rows == 0) return QLORA_OK;
   NormArgs a{};
   a.x = view(x, x_stride);
@@ -122,6 +131,9 @@ qlora_status qlora_rms_norm_bwd(const uint16_t* dy, int64_t dy_stride, const uin
   if ((st = check_rows(h, h_stride, rows, dim, false)) != QLORA_OK) return st;
   if (dh && (st = check_rows(dh, dh_stride, rows, dim, false)) != QLORA_OK) return st;
   if ((st = check_rows(dx, dx_stride, rows, dim, true)) != QLORA_OK) return st;
+  if (!in_place_ok(dx, dx_stride, dy, dy_stride, rows) || !in_place_ok(dx, dx_stride, h, h_stride, rows) ||
+      !in_place_ok(dx, dx_stride, dh, dh_stride, rows))
+    return QLORA_ERR_SHAPE;
   if (dweight) {
     if (!ws || ws_bytes < qlora_rms_norm_bwd_workspace(rows, dim)) return QLORA_ERR_WORKSPACE;
     if (!aligned16(ws)) return QLORA_ERR_ALIGN;
@@ -196,6 +208,7 @@ qlora_status qlora_token_logprob_bwd(const void* logits, int64_t stride, int64_t
   qlora_status st = check_logits(logits, stride, rows, vocab, dtype, scale, false);
   if (st != QLORA_OK) return st;
   if ((st = check_logits(dlogits, dlogits_stride, rows, vocab, dtype, scale, true)) != QLORA_OK) return st;
+  if (!in_place_ok(dlogits, dlogits_stride, logits, stride, rows)) return QLORA_ERR_SHAPE;
   if (rows == 0) return QLORA_OK;
   if (!stats || (dlogprob && !token) || (dentropy && !entropy) || (!dlogprob && !dentropy)) return QLORA_ERR_NULL;
   if (!aligned8(token) || !aligned4(stats) || !aligned4(dlogprob) || !aligned4(entropy) || !aligned4(dentropy))

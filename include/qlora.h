@@ -435,7 +435,9 @@ typedef enum { QLORA_ACT_SILU = 0, QLORA_ACT_GELU = 1 } qlora_activation;
  * bf16 of G and U [M][out] (both or neither) and of T = X A of each [M][r] (both or neither) are written where their pointers
  * are not NULL.  M = 0 is a no-op.
  * Requires: what qlora_linear_fwd does of X, H, each weight and its adapters; both weights of one shape and format
- * (UNSUPPORTED otherwise); adapters of one rank; ws of qlora_gated_workspace(M, in, out, r) bytes.           */
+ * (UNSUPPORTED otherwise; they may be the same one); adapters of one rank; outputs that overlap nothing; ws of
+ * qlora_gated_workspace(M, in, out, r) bytes, 16-byte aligned (some smaller M take more than larger ones: a workspace for several
+ * sizes is the largest of theirs).                                                                         */
 size_t qlora_gated_workspace(int64_t M, int64_t in_features, int64_t out_features, int32_t r);
 qlora_status qlora_gated_fwd(const uint16_t* X, int64_t M, const qlora_nf4* gate, const qlora_nf4* up,
                              const uint16_t* A_gate, const uint16_t* B_gate, const uint16_t* A_up, const uint16_t* B_up,
@@ -464,7 +466,7 @@ typedef enum { QLORA_BF16 = 0, QLORA_FP32 = 1 } qlora_dtype;
  *   logits by the lower index, NaN before all.
  * logprob may be NULL (then token may be too).  Logits of -infinity have probability 0.  A row of nothing else has
  * m = -infinity, z = 0, logprob and top_logprob -infinity, entropy 0.  A NaN or +infinity makes its row's logprob and
- * entropy NaN.  fp32 throughout; the same call gives the same bits.
+ * entropy NaN.  A finite logit whose product with the scale overflows counts as the infinity of its sign.  fp32 throughout; the same call gives the same bits.
  * Requires: 1 <= vocab <= 2^20, 0 <= rows < 2^22, rows * vocab < 2^35; any stride from 0 to 2^36 - 1 and pointers aligned to their elements (rows may
  * start anywhere); 0 <= top <= 32, top <= vocab; scale finite and > 0; ws of qlora_token_logprob_workspace bytes, 16-byte
  * aligned (it grows with rows, vocab and top, so that of the largest call serves smaller ones; 0 for sizes that are

@@ -154,3 +154,23 @@ def test_token_logprob_bwd_validation(lib):
     assert f(sd=99) == SHAPE and f(vocab=0) == SHAPE and f(rows=1 << 22) == SHAPE and f(sd=-100) == SHAPE
     assert f(dx=R + 2) == ALIGN and f(tok=P + 4) == ALIGN and f(dlp=Q + 2) == ALIGN and f(ent=Q, dent=Q + 2) == ALIGN
     assert f(scale=0.0) == UNSUPPORTED and f(dt=3) == UNSUPPORTED
+
+
+def test_outputs_that_would_overlap(lib):
+    """Rows written where inputs begin, at another stride, and one tensor for two outputs."""
+    n = lib.qlora_rms_norm_bwd_workspace(3, 64)
+
+    def norm(y=R, sy=64, h=S, sh=64):
+        return lib.qlora_rms_norm(P, 64, Q, 72, 3, 64, None, 0.0, y, sy, h, sh, None)
+
+    assert norm(y=P, sy=72) == SHAPE and norm(y=Q, sy=64) == SHAPE and norm(h=P, sh=72) == SHAPE and norm(h=Q, sh=64) == SHAPE
+    assert lib.qlora_rms_norm(P, 64, None, 0, 3, 64, None, 0.0, P, 128, None, 0, None) == SHAPE
+    for src in (P, Q, R):
+        st = lib.qlora_rms_norm_bwd(P, 64, Q, 64, R, 64, 3, 64, None, 0.0, src, 128, None, None, n, None)
+        assert st == SHAPE
+    assert lib.qlora_token_logprob_bwd(P, 100, 3, 100, 1, Q, 1.0, Q, Q, None, None, P, 101, None) == SHAPE
+    w = _w()
+    need = lib.qlora_gated_workspace(3, 64, 128, 8)
+    for H, G, U, Tg, Tu in ((R, R, S, None, None), (R, S, R, None, None), (R, S, S, None, None), (R, None, None, S, S)):
+        st = lib.qlora_gated_fwd(P, 3, C.byref(w), C.byref(w), P, P, P, P, 8, 0.5, 0, H, G, U, Tg, Tu, S, need, None)
+        assert st == SHAPE
