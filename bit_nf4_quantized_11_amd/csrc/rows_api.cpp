@@ -71,8 +71,9 @@ LpWs lp_layout(void* base, int64_t rows, int64_t segs, int32_t top) {
   return w;
 }
 // Parts of a call with at most these rows and logits: a row is cut into pieces of 16384 logits at least, or smaller ones while
-// all rows together have fewer than 128, so into no more than 256 in all then.
+// all rows together have fewer than 128, so into no more than 256 in all then.  0 where every row is whole.
 int64_t lp_most_parts(int64_t rows, int64_t vocab) {
+  if (vocab <= (rows < 128 ? 32768 : 16384)) return 0;
   const int64_t per_row = (vocab + 16383) / 16384;
   return std::max<int64_t>(256, per_row > 1 ? rows * per_row : 0);
 }

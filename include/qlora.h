@@ -469,8 +469,8 @@ typedef enum { QLORA_BF16 = 0, QLORA_FP32 = 1 } qlora_dtype;
  * entropy NaN.  A finite logit whose product with the scale overflows counts as the infinity of its sign.  fp32 throughout; the same call gives the same bits.
  * Requires: 1 <= vocab <= 2^20, 0 <= rows < 2^22, rows * vocab < 2^35; any stride from 0 to 2^36 - 1 and pointers aligned to their elements (rows may
  * start anywhere); 0 <= top <= 32, top <= vocab; scale finite and > 0; ws of qlora_token_logprob_workspace bytes, 16-byte
- * aligned (it grows with rows, vocab and top, so that of the largest call serves smaller ones; 0 for sizes that are
- * refused).  rows = 0 is a no-op.                                                                        */
+ * aligned (it grows with rows, vocab and top, so that of the largest call serves smaller ones; 0, and ws may be NULL, up to 32768
+ * logits a row, or 16384 with 128 rows or more; 0 also for sizes that are refused).  rows = 0 is a no-op.   */
 size_t qlora_token_logprob_workspace(int64_t rows, int64_t vocab, int32_t top);
 qlora_status qlora_token_logprob(const void* logits, int64_t stride, int64_t rows, int64_t vocab, int32_t dtype,
                                  const int64_t* token, float scale, int32_t top, float* logprob, float* stats,

@@ -174,3 +174,14 @@ def test_outputs_that_would_overlap(lib):
     for H, G, U, Tg, Tu in ((R, R, S, None, None), (R, S, R, None, None), (R, S, S, None, None), (R, None, None, S, S)):
         st = lib.qlora_gated_fwd(P, 3, C.byref(w), C.byref(w), P, P, P, P, 8, 0.5, 0, H, G, U, Tg, Tu, S, need, None)
         assert st == SHAPE
+
+
+def test_token_logprob_without_workspace(lib):
+    """None up to 32768 logits a row, or 16384 from 128 rows on: then a call of 0 bytes passes the check of its size (and is
+    refused for its alignment behind that)."""
+    for rows, most in ((1, 32768), (127, 32768), (128, 16384), (5000, 16384)):
+        for dt in (0, 1):
+            for v in (1, 4097, 8192, 8193, 16384, most):
+                assert lib.qlora_token_logprob_workspace(rows, v, 1) == 0
+                assert lib.qlora_token_logprob(P, v, rows, v, dt, P, 1.0, 1, Q, Q, None, R, R, P + 8, 0, None) == ALIGN
+        assert lib.qlora_token_logprob_workspace(rows, most + 1, 0) > 0
