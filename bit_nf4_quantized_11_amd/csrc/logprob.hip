@@ -8,10 +8,11 @@
 // taken from its own maximum without a second look at memory), the backward reads and writes them once.
 // Rows of several parts, and few long ones, are joined by a second kernel.  4096 x 32000 logits of bf16: forward 45 us = 5.8
 // TB/s and 4.7 for the join, backward 95 us = 5.5 TB/s; of fp32 forward 86 us = 6.1 TB/s.  With the waves of a row waiting for one
-// maximum it was 65 us.  8 x 32000: 5.3 us, 12 with 20 alternatives (latency: 2 for the bound and the list, 3 for the ranks).
+// maximum it was 65 us.  8 x 32000: 5.3 us, 8.0 with 20 alternatives (latency).
 //
-// The k largest: a wave's k-th largest of its lanes' maxima is a bound that at least k of its elements reach; with the
-// largest bound of all waves few elements remain (about 1.5 k a wave).  They are listed in LDS as 64-bit numbers
+// The k largest: a wave's k-th largest of its lanes' maxima is a bound that at least k of its elements reach; so is the least of
+// all waves' ceil(k / waves)-th largest, which leaves fewer where the large ones are spread (k = 20 over 8 waves: about 46 of a
+// row of 32000, with the first kind alone 130; the higher of the two is taken).  What remains is listed in LDS as 64-bit numbers
 // (order of the value, then the lower index) and each counts those above it: its rank, whatever the order of the list.
 // With more candidates than the list holds (equal or masked logits) the bound is taken in full and only the first k of
 // each wave's elements that equal it are listed; rows with still more, or with a NaN, take k rounds of a maximum instead.
@@ -163,6 +164,18 @@ __device__ __forceinline__ uint32_t kth_largest(uint32_t mine, int k) {
   return b;
 }
 
+// Both of two such numbers at once: their rounds' chains of scalar instructions run beside each other.
+template <int LOW>
+__device__ __forceinline__ void kth_largest(uint32_t mine, int k0, int k1, uint32_t& b0, uint32_t& b1) {
+  b0 = b1 = 0;
+#pragma unroll
+  for (int bit = 31; bit >= LOW; --bit) {
+    const uint32_t next0 = b0 | 1u << bit, next1 = b1 | 1u << bit;
+    if (__popcll(__ballot(mine >= next0)) >= k0) b0 = next0;
+    if (__popcll(__ballot(mine >= next1)) >= k1) b1 = next1;
+  }
+}
+
 // Where this lane's `mine` places begin in a list that all waves share.
 __device__ __forceinline__ int places(int mine, int* count) {
   if (!__ballot(mine > 0)) return 0;
@@ -208,7 +221,7 @@ __global__ __launch_bounds__(NT) void k_token_logprob(LpArgs a) {
   constexpr int E = X::E, NW = NT / 64;
   __shared__ float red[3][NW];
   __shared__ u64 list[TOP ? CAP + kPad : 1];
-  __shared__ uint32_t bound[NW];
+  __shared__ uint32_t bound[2][NW];
   __shared__ int count;
   const bool whole = a.segs == 1;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -248,39 +261,48 @@ __global__ __launch_bounds__(NT) void k_token_logprob(LpArgs a) {
   s = wave_sum(s);
   if (lane == 0) red[0][wave] = mine_m, red[1][wave] = z, red[2][wave] = s;
   if (TOP) {
-    // the wave's k-th largest lane maximum, by the upper half of its order (a lower bound is as good)
-    const uint32_t mine = kth_largest<16>(order_of(top), a.top);
-    if (lane == 0) bound[wave] = mine;
+    // the wave's k-th largest lane maximum, and its share of k, by the upper halves of their orders (lower bounds are as good)
+    uint32_t own, share;
+    kth_largest<16>(order_of(top), a.top, (a.top + NW - 1) / NW, own, share);
+    if (lane == 0) bound[0][wave] = own, bound[1][wave] = share;
     if (t == 0) count = 0;
     __syncthreads();
-    uint32_t b = bound[0];
+    uint32_t b = bound[0][0], all = bound[1][0];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) b = max(b, bound[w]);
+    for (int w = 1; w < NW; ++w) b = max(b, bound[0][w]), all = min(all, bound[1][w]);
+    b = max(b, all);
     // (where the bound is -infinity, everything would be listed, the places behind the row's end too)
     const bool nothing = b <= 0x007FFFFFu;
     const float least = nothing ? INFINITY : value_of((u64)b << 32);
-    int above = nothing ? (t == 0 ? CAP + 1 : 0) : 0;
+    // A bit for each of the thread's elements, the first one highest; those that are listed are read again (the row is in the caches;
+    // a branch on each in its register is 5 KB of instructions to fetch: 8 x 32000 9.9 us against 8.0).
+    static_assert(C * E <= 64, "bits of a thread's elements");
+    constexpr int B = C * E < 32 ? C * E : 32;
+    uint32_t hit[C * E / B] = {};
     if (top >= least && !nothing) {
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         float f[E];
         X::unpack(v[i], f);
 #pragma unroll
-        for (int j = 0; j < E; ++j) above += f[j] >= least;
-      }
-    }
-    int at = places(above, &count);
-    if (above > 0 && at + above <= CAP) {
-#pragma unroll
-      for (int i = 0; i < C; ++i) {
-        float f[E];
-        X::unpack(v[i], f);
-#pragma unroll
         for (int j = 0; j < E; ++j) {
-          const int col = col0 + i * NT * E + j;
-          if (f[j] >= least) list[at++] = entry_of(f[j], col);
+          uint32_t& h = hit[(i * E + j) / B];
+          h = h + h + (f[j] >= least ? 1u : 0u);
         }
       }
+    }
+    int above = nothing && t == 0 ? CAP + 1 : 0;
+#pragma unroll
+    for (int k = 0; k < C * E / B; ++k) above += __popc(hit[k]);
+    int at = places(above, &count);
+    if (at + above <= CAP) {
+#pragma unroll
+      for (int k = 0; k < C * E / B; ++k)
+        for (uint32_t h = hit[k]; h; ++at) {
+          const int b = 31 - __clz(h), e = k * B + B - 1 - b, col = col0 + e / E * (NT * E) + e % E;
+          h ^= 1u << b;
+          list[at] = entry_of(X::value(x + col), col);
+        }
     }
   }
   __syncthreads();
@@ -312,12 +334,12 @@ __global__ __launch_bounds__(NT) void k_token_logprob(LpArgs a) {
     // of each wave.
     const uint32_t mine = order_of(top), b = kth_largest<0>(mine, a.top);
     __syncthreads();
-    if (lane == 0) bound[wave] = b;
+    if (lane == 0) bound[0][wave] = b;
     if (t == 0) count = 0;
     __syncthreads();
-    uint32_t order = bound[0];
+    uint32_t order = bound[0][0];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) order = max(order, bound[w]);
+    for (int w = 1; w < NW; ++w) order = max(order, bound[0][w]);
     const float least = value_of((u64)order << 32);
     // (read again, a few loads at a time: this path is to cost the common one no registers)
     const bool larger = __ballot(top > least) != 0;   // (in this wave)
@@ -402,14 +424,23 @@ __global__ __launch_bounds__(64 * JW) void k_logprob_join(LpArgs a) {
   const int64_t row = (int64_t)blockIdx.x * JW + wave;
   if (row >= a.rows) return;
   const Given<F32> given(a, row, a.logprob ? a.token[row] : -1);
-  const int n = a.segs * a.top;
-  u64* const list = lists + wave * n;
-  if (TOP)
-    for (int i = lane; i < n; i += 64) list[i] = a.cand[row * n + i];
   float m = -INFINITY, z = 0.0f, s = 0.0f;
   if (lane < a.segs) {
     const LpPart p = a.part[row * a.segs + lane];
     m = p.m, z = p.z, s = p.s;
+  }
+  const int n = a.segs * a.top;
+  u64* const list = lists + wave * n;
+  if (TOP) {
+    constexpr int U = 8;   // loads in flight
+    for (int i0 = lane; i0 < n; i0 += 64 * U) {
+      u64 c[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) c[u] = a.cand[row * n + min(i0 + 64 * u, n - 1)];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + 64 * u < n) list[i0 + 64 * u] = c[u];
+    }
   }
   const float mm = wave_max(m);
   const float d = m == -INFINITY ? 0.0f : m - mm;
@@ -492,9 +523,8 @@ struct Part {
 // By what the rows alone say, not by the outputs that a call asks for, so that the sums do not depend on these.
 //   A row of up to 32 K logits is one part, held by as few threads as its length allows (1000 logits by a wave: 4096 rows 6 us, by
 // 512 threads 12).
-//   Of bf16 and 128 rows or more, parts have 16 K logits at most: 4096 rows of 32000 take 46 + 5 us with the join and 70 + 9 with 20
-// alternatives, whole ones 51 and 111; 8 rows are faster whole (12 us against 10 + 5).  (fp32, as many: 86 and 105 whole, 87 + 5 and
-// 96 + 10.)
+//   Of bf16 and 128 rows or more, parts have 16 K logits at most: 4096 rows of 32000 take 46 + 5 us with the join (66 + 9 with 20
+// alternatives), whole ones 51 (fp32, as many: 86 whole, 87 + 5); 8 rows are faster whole (8 us with 20 alternatives).
 //   Longer rows have parts of that size, and smaller ones while all rows together have fewer than 128.
 Part part_for(int64_t rows, int64_t vocab, bool fp32) {
   const int64_t n = pieces(vocab, fp32);

@@ -317,3 +317,30 @@ def test_binding_refusals():
     for out in (x.bfloat16(), x[:3], x.cpu(), torch.zeros(4, 100, device="cuda")[:, ::2], torch.zeros(1, 50, device="cuda").expand(4, 50)):
         with pytest.raises(Q.QLoRAError):
             Q.qlora_token_logprob_bwd(x, t, s, d, out=out)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("n,v", [(6, 700), (6, 3000), (6, 9000), (6, 32001), (140, 20000), (6, 150000)])
+def test_top_wherever_the_large_ones_lie(dtype, n, v):
+    """Rows whose large logits lie together, in one thread's elements, spread over all waves, at the row's end, or fewer than the
+    alternatives above equal ones: the first of a stable sort in descending order."""
+    require_gpu()
+    gen = torch.Generator().manual_seed(v)
+    x = torch.randn(n, v, generator=gen)
+    k = 32
+    x[0, 8:8 + 100] += 10                                    # neighbouring threads of one wave
+    x[1, ::8192 if v > 8192 else 64] += 10                   # one thread, or one of each wave
+    x[2, v - 40:] = 5 + torch.arange(40) % 7 / 8             # the end, with equal ones
+    x[3, torch.randperm(v, generator=gen)[:k]] = 9.0         # k equal ones and no others
+    x[4] = x[4].clamp(max=0.0)                               # half of them equal
+    x[4, torch.randperm(v, generator=gen)[:5]] = 3.0
+    x[5] = -torch.arange(v) // 3 / 16.0
+    x = x.to(dtype)
+    want = torch.sort(x.double(), dim=1, descending=True, stable=True)[1][:, :k]
+    token = torch.zeros(n, dtype=torch.int64, device="cuda")
+    for top in (1, 7, k):
+        _, _, _, tlp, tix = Q.qlora_token_logprob(x.cuda(), token, top=top)
+        assert torch.equal(tix.cpu(), want[:, :top]), top
+        exact = torch.log_softmax(x.double(), 1).gather(1, want[:, :top])
+        # (the distance from the largest logit is exact to 2^-24 of it, the sum's logarithm to 2^-18)
+        assert torch.all((tlp.double().cpu() - exact).abs() <= 2.0 ** -18 + 2.0 ** -22 * (16 + exact.abs()))
