@@ -170,8 +170,8 @@ __device__ __forceinline__ void gemm_workgroup(const FwdParams& p, uint32_t bid,
   const int kh = wave_k();
   auto compute_store = [&](Acc& acc, int cb, const Stage& S, int sb) {
     Frags Fa, Fb;
-    read_frags(Fa, sT[cb], sF[cb], 2 * kh);
-    read_frags(Fb, sT[cb], sF[cb], 2 * kh + 1);
+    read_frags<GATED>(Fa, sT[cb], sF[cb], 2 * kh);
+    read_frags<GATED>(Fb, sT[cb], sF[cb], 2 * kh + 1);
     mma_group(acc, Fa, 0);
     store_tokens_part(S.T, sT[sb], 0);
     store_tokens_part(S.T, sT[sb], 1);
@@ -209,6 +209,20 @@ __device__ __forceinline__ void gemm_workgroup(const FwdParams& p, uint32_t bid,
   // two stages per trip (stage it in buffer 0 with it+1 in S1, then it+1 in buffer 1 with
   // it+2 in S0); a single exit keeps the accumulators in one register set
   uint32_t it = 0;
+  // (of the gated forms) a wave of tokens 128 .. 255 of a panel that has none of them stores its share of the stages alone,
+  // between as many barriers: 100 tokens of 4096 -> 11008 61 us, with its products of zeros 71
+  if (GATED && __builtin_amdgcn_readfirstlane(wave_t<GATED>()) && p.M - (int64_t)m0 <= 128) {
+    for (; it + 1 < nkb; it += 2) {
+      load(min(it0 + it + 2, last), S0);
+      store_all(S1, 1);
+      __syncthreads();
+      load(min(it0 + it + 3, last), S1);
+      store_all(S0, 0);
+      __syncthreads();
+    }
+    if (it < nkb) __syncthreads();
+    it = nkb;
+  }
   for (; it + 1 < nkb; it += 2) {
     load(min(it0 + it + 2, last), S0);
     compute_store(acc, 0, S1, 1);
@@ -218,14 +232,14 @@ __device__ __forceinline__ void gemm_workgroup(const FwdParams& p, uint32_t bid,
     __syncthreads();
   }
   if (it < nkb) {   // odd number of stages: the last one is in buffer 0
-    mma_stage<false>(acc, sT[0], sF[0]);
+    mma_stage<false, GATED>(acc, sT[0], sF[0]);
     __syncthreads();
   }
 
   if constexpr (SPLIT && GATED) {
     // this wave's 64 features of its weight start at n0 (store_out_f32 adds the feature half's offset)
-    if (combine_halves(acc, smem))
-      store_out_f32(acc, (wave_f() ? p.partial2 : p.partial) + (int64_t)split * p.M * p.npad, p.npad, m0, p.M,
+    if (combine_halves<true>(acc, smem))
+      store_out_f32<true>(acc, (wave_f() ? p.partial2 : p.partial) + (int64_t)split * p.M * p.npad, p.npad, m0, p.M,
                     (int64_t)n0 - wave_f() * 64, p.N);
     return;
   }
@@ -267,24 +281,24 @@ __device__ __forceinline__ void gemm_workgroup(const FwdParams& p, uint32_t bid,
     *reinterpret_cast<uint4*>(sF[0] + swzN(bj, 2 * be)) = b0;
     *reinterpret_cast<uint4*>(sF[0] + swzN(bj, 2 * be + 1)) = b1;
     __syncthreads();
-    mma_stage<true>(acc, GATED && wave_f() ? sT[1] : sT[0], sF[0]);
+    mma_stage<true, GATED>(acc, GATED && wave_f() ? sT[1] : sT[0], sF[0]);
     __syncthreads();
   }
   if constexpr (!GATED) {
     if (combine_halves(acc, smem)) store_out(acc, p.Y, p.N, m0, p.M, n0, p.N);
   } else {
-    const bool holds = combine_halves(acc, smem);
+    const bool holds = combine_halves<true>(acc, smem);
     if (tail) {
       if (holds) {
         const int64_t rows = min<int64_t>(BT, p.M - m0), left = p.N - n0;
         const int64_t c0 = n0 - (tiles_f - (tiles_t * tiles_f - p.whole)) * FT;   // column of the tail
         float* const out = (wave_f() ? p.partial2 : p.partial) + (int64_t)part * BT * p.npad;
-        store_out_f32(acc, out, p.npad, 0, rows, c0 - wave_f() * 64, c0 + min<int64_t>(left, FT));
+        store_out_f32<true>(acc, out, p.npad, 0, rows, c0 - wave_f() * 64, c0 + min<int64_t>(left, FT));
       }
       return;
     }
     // the wave of G keeps features 0 .. 31 of the tile and takes U's from the wave of U, which keeps 32 .. 63
-    const int lane = t & 63, q = wave_id() & 3, wf = wave_f();
+    const int lane = t & 63, q = wave_t<true>() | wave_f() << 1, wf = wave_f();
     float4* const x = reinterpret_cast<float4*>(smem);
     if (holds) {
 #pragma unroll
@@ -299,7 +313,7 @@ __device__ __forceinline__ void gemm_workgroup(const FwdParams& p, uint32_t bid,
     if (!holds) return;
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      const int64_t tok = (int64_t)m0 + wave_t() * 128 + m * 32 + (lane & 31);
+      const int64_t tok = (int64_t)m0 + wave_t<true>() * 128 + m * 32 + (lane & 31);
       const f32x16 own = wf ? acc.c[1][m] : acc.c[0][m];
       if (tok >= p.M) continue;
 #pragma unroll

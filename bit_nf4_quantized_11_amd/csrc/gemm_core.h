@@ -77,9 +77,13 @@ __device__ __forceinline__ uint2 ld8(rsrc_t r, uint32_t voff, uint32_t soff = 0)
   return make_uint2(v.x, v.y);
 }
 
-// wave roles
+// wave roles.  SPREAD: waves w and w + 4, which share a SIMD, take different token halves, so that every SIMD has work where a half
+// has no tokens (elsewhere it costs the linear layer's kernels registers).
 __device__ __forceinline__ int wave_id() { return threadIdx.x >> 6; }
-__device__ __forceinline__ int wave_t() { return wave_id() & 1; }          // token half of the tile
+template <bool SPREAD = false>
+__device__ __forceinline__ int wave_t() {   // token half of the tile
+  return SPREAD ? (wave_id() & 1) ^ (wave_id() >> 2) : wave_id() & 1;
+}
 __device__ __forceinline__ int wave_f() { return (wave_id() >> 1) & 1; }   // feature half of the tile
 __device__ __forceinline__ int wave_k() { return wave_id() >> 2; }         // reduction half of a stage
 
@@ -163,8 +167,9 @@ struct Frags {
 };
 
 // ks (0..3) selects 16 of the 64 reduction values of the stage
+template <bool SPREAD = false>
 __device__ __forceinline__ void read_tokens(Frags& F, const uint16_t* __restrict__ sT, int ks) {
-  const int lane = threadIdx.x & 63, wt = wave_t();
+  const int lane = threadIdx.x & 63, wt = wave_t<SPREAD>();
   const int chunk = ks * 2 + (lane >> 5);
 #pragma unroll
   for (int m = 0; m < 4; ++m)
@@ -172,6 +177,7 @@ __device__ __forceinline__ void read_tokens(Frags& F, const uint16_t* __restrict
 }
 
 // feature operand from a feature tile [128][64]
+template <bool SPREAD = false>
 __device__ __forceinline__ void read_frags(Frags& F, const uint16_t* __restrict__ sT,
                                            const uint16_t* __restrict__ sF, int ks) {
   const int lane = threadIdx.x & 63, wf = wave_f();
@@ -179,7 +185,7 @@ __device__ __forceinline__ void read_frags(Frags& F, const uint16_t* __restrict_
 #pragma unroll
   for (int f = 0; f < 2; ++f)
     F.fa[f] = *reinterpret_cast<const u32x4*>(sF + swzF(wf * 64 + f * 32 + (lane & 31), chunk));
-  read_tokens(F, sT, ks);
+  read_tokens<SPREAD>(F, sT, ks);
 }
 
 // feature operand from a natural tile [64][128] with transposing reads: 16-lane group
@@ -201,12 +207,13 @@ __device__ __forceinline__ u32x4 read_natural_a(const uint16_t* __restrict__ sN,
   return o;
 }
 
+template <bool SPREAD = false>
 __device__ __forceinline__ void read_frags_natural(Frags& F, const uint16_t* __restrict__ sT,
                                                    const uint16_t* __restrict__ sN, int ks) {
   const int wf = wave_f();
 #pragma unroll
   for (int f = 0; f < 2; ++f) F.fa[f] = read_natural_a(sN, wf * 64 + f * 32, ks);
-  read_tokens(F, sT, ks);
+  read_tokens<SPREAD>(F, sT, ks);
 }
 
 __device__ __forceinline__ void mma_group(Acc& a, const Frags& F, int f) {
@@ -228,16 +235,16 @@ __device__ __forceinline__ void interleave_mfma_valu() {
 }
 
 // This wave's half of one 64-deep stage, without interleaved work (tail and adapter stages).
-template <bool NATURAL>
+template <bool NATURAL, bool SPREAD = false>
 __device__ __forceinline__ void mma_stage(Acc& a, const uint16_t* __restrict__ sT, const uint16_t* __restrict__ sF) {
   Frags F;
   const int kh = wave_k();
 #pragma unroll
   for (int k2 = 0; k2 < 2; ++k2) {
     if constexpr (NATURAL)
-      read_frags_natural(F, sT, sF, 2 * kh + k2);
+      read_frags_natural<SPREAD>(F, sT, sF, 2 * kh + k2);
     else
-      read_frags(F, sT, sF, 2 * kh + k2);
+      read_frags<SPREAD>(F, sT, sF, 2 * kh + k2);
     mma_group(a, F, 0);
     mma_group(a, F, 1);
   }
@@ -246,8 +253,9 @@ __device__ __forceinline__ void mma_stage(Acc& a, const uint16_t* __restrict__ s
 // Add the accumulators of the two waves of each quarter: waves 4..7 hand theirs to waves
 // 0..3 through LDS (`smem`, free at this point), one feature tile at a time.  Returns true
 // in the waves that hold the sum.
+template <bool SPREAD = false>
 __device__ __forceinline__ bool combine_halves(Acc& a, uint16_t* __restrict__ smem) {
-  const int lane = threadIdx.x & 63, q = wave_id() & 3;
+  const int lane = threadIdx.x & 63, q = wave_t<SPREAD>() | wave_f() << 1;
   const bool upper = wave_k() != 0;
   float4* x = reinterpret_cast<float4*>(smem);
 #pragma unroll
@@ -305,10 +313,11 @@ __device__ __forceinline__ void store_out(const Acc& a, uint16_t* __restrict__ o
 
 // Store the fp32 accumulators of this wave's quarter into out [ntok][ld] (ld % 4 == 0, 16-byte
 // aligned rows), features below nfeat only.
+template <bool SPREAD = false>
 __device__ __forceinline__ void store_out_f32(const Acc& a, float* __restrict__ out, int64_t ld, int64_t m0,
                                               int64_t ntok, int64_t f0, int64_t nfeat) {
   const int lane = threadIdx.x & 63;
-  const int wt = wave_t(), wf = wave_f();
+  const int wt = wave_t<SPREAD>(), wf = wave_f();
 #pragma unroll
   for (int m = 0; m < 4; ++m) {
     const int64_t tok = m0 + wt * 128 + m * 32 + (lane & 31);
