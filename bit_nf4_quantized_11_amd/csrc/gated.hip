@@ -37,7 +37,8 @@ __device__ __forceinline__ int bpos(int j, int q) {
 // holds features 4 (l / 16) .. + 3 of token l % 16, as the matrix instruction leaves them.  Bound by latency: the first 4
 // slices' loads and B's are issued before any is used.  The ranks go through LDS 128 at a time.
 // (16 tokens, 22016 features, rank 64, 4 slices: 6.8 us, where the partial sums are 11.3 MB; with Ts B by fp32 multiply-adds out of
-// LDS 11.2.)
+// LDS 11.2.  256 tokens, 5504 features, 2 slices: 12.4 us; with loads of as many slices and ranks at all times 15.1, with two blocks
+// of features to a workgroup 16.9.)
 constexpr int RANKS = 128, TPAD = 8, S0 = 4;
 __global__ __launch_bounds__(256) void k_gated_epilogue(EpiArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
@@ -55,7 +56,7 @@ __global__ __launch_bounds__(256) void k_gated_epilogue(EpiArgs a) {
   for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int u = 0; u < S0; ++u)
-      v[k][u] = *reinterpret_cast<const f32x4*>(a.side[k].partial + min(u, a.splits - 1) * slice + at);
+      if (u < a.splits) v[k][u] = *reinterpret_cast<const f32x4*>(a.side[k].partial + u * slice + at);
   const uint32_t bend = (uint32_t)(a.r * a.N * 2);
   const rsrc_t rB[2] = {make_rsrc(a.side[0].B, bend), make_rsrc(a.side[1].B, bend)};
   f32x4 lora[2] = {};
@@ -68,8 +69,8 @@ __global__ __launch_bounds__(256) void k_gated_epilogue(EpiArgs a) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int idx = t + 256 * u, jj = j0 + (idx >> 3), q = idx & 7;
-        const bool ok = idx < jn * 8 && jj < a.r && n0 + q * 8 < a.N;
-        bv[k][u] = ld16(rB[k], ok ? (uint32_t)((jj * a.N + n0 + q * 8) * 2) : bend);
+        const bool ok = jj < a.r && n0 + q * 8 < a.N;
+        if (256 * u < jn * 8) bv[k][u] = ld16(rB[k], ok ? (uint32_t)((jj * a.N + n0 + q * 8) * 2) : bend);
       }
     if (j0) __syncthreads();   // (the last ranks are done with)
 #pragma unroll
