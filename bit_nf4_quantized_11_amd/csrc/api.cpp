@@ -240,19 +240,20 @@ BwdWs bwd_layout(void* base, int64_t M, int64_t in, int64_t out, int32_t r) {
   return ws;
 }
 
-// The gated block's tiles have 64 features of each projection.  K-slices as many as all CUs take at once, one fewer where
-// four or more would leave the workgroups of X A none (100 tokens of 4096 -> 4096, 64 tiles: 34 us in 3 slices, 36 in 4).  Two
-// pay as well as more here (256 tokens of 2048 -> 5504, 86 tiles: 42 us in 2, 58 in 3 that no longer run at once, 52
-// whole; 300 tokens of 4096 -> 4096 64 against 77), past one token panel where their stages outweigh the sums' way through memory (512
-// tokens: of 1024 -> 2816 38 us in 2, 36 whole).
+// The gated block's tiles have 64 features of each projection.  K-slices as many as all CUs take at once, where there are more than
+// three as many as leave a fifth of them to X A (256 tokens of 8192 -> 2048, 32 tiles: 41 us in 6 slices, 46 in 8; 100 tokens of
+// 4096 -> 4096, 64 tiles: 30 in 3, 33 in 4).  Two pay as well (256 tokens of 2048 -> 5504, 86 tiles: 39 us in 2, 57 in 3 that no longer
+// run at once, 48 whole; 300 tokens of 4096 -> 4096 62 against 74), but past one half panel not where nearly every CU writes
+// sums for few stages (256 tokens of 1024 -> 8192, 128 tiles: 38 us in 2, 35 whole).  With more panels a slice has 8 stages at
+// least (500 tokens of 2048 -> 512: 25 us in 4, 28 in 8), else 4.
 int64_t gated_split_stages(int64_t M, int64_t in, int64_t out) {
   if (M <= 64 || M > kSplitMaxTokens) return 0;
   const int64_t tiles = (M + 255) / 256 * ((out + 63) / 64), nkb = in / 64;
   if (tiles < 1) return 0;
   int64_t s = 256 / tiles;
-  if (s > 3 && tiles * s > 224) --s;
-  s = std::min(s, nkb / 4);
-  if (s < 2 || (s == 2 && M > 256 && nkb < 32)) return 0;
+  if (s > 3) s = std::max<int64_t>(3, 200 / tiles);
+  s = std::min(s, nkb / (M > 256 ? 8 : 4));
+  if (s < 2 || (s == 2 && M > 128 && nkb < 32 && tiles > 100)) return 0;
   return (nkb + s - 1) / s;
 }
 
@@ -270,9 +271,9 @@ GatedWs gated_layout(void* base, int64_t M, int64_t in, int64_t out, int32_t r) 
   GatedWs ws;
   ws.t = lora_problem(gemm_T(nullptr, nullptr, Mm, in, r), epi_none(), kMaxSplits);
   const int64_t st = gated_split_stages(M, in, out);
-  // X A beside the K-slices: on the CUs that these leave (200 tokens of 1024 -> 2816: 15.9 us against 18.1), or, where it would
-  // run longer there than they do, in pieces so short that every CU takes one first (100 tokens of 4096 -> 4096 in 4 slices: 36 us
-  // a call against 47).  A 64-deep piece of X A takes about a third of a stage.
+  // X A beside the K-slices: on the CUs that these leave (100 tokens of 4096 -> 4096: 30 us a call, cut for all CUs 35), or, where it
+  // would run longer there than they do, in pieces so short that every CU takes one first (100 tokens of 4096 -> 5440, 85 tiles in 3
+  // slices: 37 to 40 us against 48 on the one CU left).  A 64-deep piece of X A takes about a third of a stage.
   const int64_t left = 256 - (Mm + 255) / 256 * ((out + 63) / 64) * split_count(in, std::max<int64_t>(st, 1));
   const int64_t pieces = left / 2 / (rp / 64 * ((Mm + 15) / 16));   // slices of X A that the rest of the CUs takes at once
   ws.gv = gemv_plan(Mm, in, out, rp, st != 0, true, pieces > 0 && in / 64 <= 3 * st * pieces ? left : 256);
