@@ -40,6 +40,12 @@ CASES = [
     # more tiles than CUs
     (2000, 1024, 2296, 72, "silu", "nf4", 64, True),
     (700, 1088, 7464, 16, "gelu", "fp4", 32, False),
+    # fewer than 128 tokens in the last panel: in slices of odd numbers of stages, whole, and in a cut tile
+    (90, 832, 328, 8, "gelu", "int4", 32, True),
+    (128, 1920, 1096, 32, "silu", "nf4", 128, True),
+    (129, 960, 2056, 64, "silu", "fp4", 64, True),
+    (300, 1024, 2824, 16, "gelu", "nf4", 64, True),
+    (340, 1088, 8200, 8, "silu", "nf4", 64, False),
 ]
 
 
