@@ -14,8 +14,11 @@
 // all waves' ceil(k / waves)-th largest, which leaves fewer where the large ones are spread (k = 20 over 8 waves: about 46 of a
 // row of 32000, with the first kind alone 130; the higher of the two is taken).  What remains is listed in LDS as 64-bit numbers
 // (order of the value, then the lower index) and each counts those above it: its rank, whatever the order of the list.
-// With more candidates than the list holds (equal or masked logits) the bound is taken in full and only the first k of
+// Where a mask leaves no such bound, all above -infinity are, and of the others the first (8 x 32000, 3 of them allowed: 8 us).
+// With more candidates than the list holds (equal logits) the bound is taken in full and only the first k of
 // each wave's elements that equal it are listed; rows with still more, or with a NaN, take k rounds of a maximum instead.
+#include <cfloat>
+
 #include "kernels.h"
 #include "rows.h"
 
@@ -260,6 +263,7 @@ __global__ __launch_bounds__(NT) void k_token_logprob(LpArgs a) {
   z = wave_sum(z);
   s = wave_sum(s);
   if (lane == 0) red[0][wave] = mine_m, red[1][wave] = z, red[2][wave] = s;
+  bool nothing = false;
   if (TOP) {
     // the wave's k-th largest lane maximum, and its share of k, by the upper halves of their orders (lower bounds are as good)
     uint32_t own, share;
@@ -271,15 +275,15 @@ __global__ __launch_bounds__(NT) void k_token_logprob(LpArgs a) {
 #pragma unroll
     for (int w = 1; w < NW; ++w) b = max(b, bound[0][w]), all = min(all, bound[1][w]);
     b = max(b, all);
-    // (where the bound is -infinity, everything would be listed, the places behind the row's end too)
-    const bool nothing = b <= 0x007FFFFFu;
-    const float least = nothing ? INFINITY : value_of((u64)b << 32);
+    // (where the bound is -infinity, all above that)
+    nothing = b <= 0x007FFFFFu;
+    const float least = nothing ? -FLT_MAX : value_of((u64)b << 32);
     // A bit for each of the thread's elements, the first one highest; those that are listed are read again (the row is in the caches;
     // a branch on each in its register is 5 KB of instructions to fetch: 8 x 32000 9.9 us against 8.0).
     static_assert(C * E <= 64, "bits of a thread's elements");
     constexpr int B = C * E < 32 ? C * E : 32;
     uint32_t hit[C * E / B] = {};
-    if (top >= least && !nothing) {
+    if (top >= least) {
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         float f[E];
@@ -291,7 +295,7 @@ __global__ __launch_bounds__(NT) void k_token_logprob(LpArgs a) {
         }
       }
     }
-    int above = nothing && t == 0 ? CAP + 1 : 0;
+    int above = 0;
 #pragma unroll
     for (int k = 0; k < C * E / B; ++k) above += __popc(hit[k]);
     int at = places(above, &count);
@@ -374,6 +378,14 @@ __global__ __launch_bounds__(NT) void k_token_logprob(LpArgs a) {
         have += __builtin_amdgcn_readlane(incl, 63);
       }
     }
+    __syncthreads();
+    n = count;
+  }
+  if (nothing && n < a.top) {
+    // Masked rows: with fewer than k elements above -infinity there are enough of those that equal it among the part's first k.
+    __syncthreads();
+    const int col = seg * C * NT * E + t;
+    if (t < a.top && col < a.vocab && X::value(x + col) == -INFINITY) list[atomicAdd(&count, 1)] = entry_of(-INFINITY, col);
     __syncthreads();
     n = count;
   }

@@ -344,3 +344,30 @@ def test_top_wherever_the_large_ones_lie(dtype, n, v):
         exact = torch.log_softmax(x.double(), 1).gather(1, want[:, :top])
         # (the distance from the largest logit is exact to 2^-24 of it, the sum's logarithm to 2^-18)
         assert torch.all((tlp.double().cpu() - exact).abs() <= 2.0 ** -18 + 2.0 ** -22 * (16 + exact.abs()))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("v", [40, 300, 5000, 32001, 150000])
+def test_top_of_rows_with_few_tokens_left(dtype, v):
+    """Masks that leave fewer tokens than the alternatives, as many, a few more, or tokens in the first places of the row
+    only: the allowed ones by their logits, then those of -infinity by their index."""
+    require_gpu()
+    gen = torch.Generator().manual_seed(v)
+    counts = (0, 1, 3, 19, 20, 21, 31, 32, 33, 36)
+    for n in (len(counts), 130):
+        x = torch.full((n, v), -math.inf)
+        for i in range(n):
+            k = counts[i % len(counts)]
+            at = torch.randperm(v, generator=gen)[:k] if i % 3 else torch.randperm(min(v, 40), generator=gen)[:k]
+            x[i, at] = torch.randn(len(at), generator=gen)
+        x = x.to(dtype)
+        want = torch.sort(x.double(), dim=1, descending=True, stable=True)[1]
+        token = torch.zeros(n, dtype=torch.int64, device="cuda")
+        for top in (1, 20, 32):
+            _, _, _, tlp, tix = Q.qlora_token_logprob(x.cuda(), token, top=top)
+            assert torch.equal(tix.cpu(), want[:, :top]), (n, top)
+            exact = torch.log_softmax(x.double(), 1).gather(1, want[:, :top])
+            exact[torch.isinf(x).all(1)] = -math.inf
+            got = tlp.double().cpu()
+            assert torch.equal(torch.isinf(got), torch.isinf(exact))
+            assert torch.all(((got - exact).abs() <= 2.0 ** -18 + 2.0 ** -22 * (16 + exact.abs())) | torch.isinf(exact))
