@@ -4,7 +4,7 @@
 //   dx = bf16(dh + r (w dy - h r^2 mean(w dy h))),  dw = sum over rows of dy h r
 //
 // Bound by HBM: 4 to 8 B per element in either direction: forward of 4096 x 4096 with a residual 22 us = 6.1 TB/s, backward with dh
-// 24 us = 5.6 TB/s and 4.6 for the weight's gradient, whose 512 partials are 8 MB more (2048 x 8192: 28 + 4.8 us).  For a few rows by a
+// 22.3 us = 6.2 TB/s and 4.0 for the weight's gradient, whose 256 partials are 4 MB more (2048 x 8192, 512 partials: 28 + 4.7 us).  For a few rows by a
 // launch and two dependent round trips (16 x 8192: 3.8 us).  A row stays in the registers of the T threads that
 // hold it (a wave for short rows, a workgroup for long ones), 8 elements to a load, so each tensor is read or written once.
 // The backward walks over rows with the weight's gradient in registers, one partial per workgroup, summed by a second
@@ -50,6 +50,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* buf) {
       for (int i = 0; i < N; ++i) buf[w * N + i] = v[i];
     }
     __syncthreads();
+    buf += threadIdx.x / T * (T / 64 * N);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       v[i] = buf[i];
@@ -111,6 +112,14 @@ __global__ __launch_bounds__(T < NT ? NT : T) void k_rms_norm(NormArgs a) {
   }
 }
 
+// AHEAD: the next row's loads are issued before this row's sums are waited for (4096 x 4096 with dh 25.4 -> 24 us, without 20.3 ->
+// 18.7), where the registers leave eight waves to a CU all the same (2048 x 8192 with dh: 28 us without, 29 with).
+constexpr bool bwd_ahead(int c, bool dh) { return c <= 2 || !dh; }
+// Threads of a workgroup, rows of t threads.  Two rows of 256, which halves the partial weight gradients (2048 x 8192 27.0 -> 23.7 us
+// in all, 1531 x 5000 16.2 -> 15.1, 4096 x 4096 with dh 26.5 -> 25.5), where the next rows' loads bridge the wait for each other
+// (2048 x 8192 with dh: 31.1 us apart, 31.7 in pairs).
+constexpr int bwd_threads(int t, int c, bool dh) { return t < NT ? NT : t == 256 && bwd_ahead(c, dh) ? 512 : t; }
+
 // The loads of a row in the backward.
 template <int T, int C, bool DH>
 struct BwdRow {
@@ -128,12 +137,11 @@ struct BwdRow {
   }
 };
 
-// AHEAD: the next row's loads are issued before this row's sums are waited for (4096 x 4096 with dh 25.4 -> 24 us, without 20.3 ->
-// 18.7), where the registers leave two workgroups to a CU all the same (2048 x 8192 with dh: 28 us without, 29 with).
-template <int T, int C, bool DH, bool AHEAD = C <= 2 || !DH>
-__global__ __launch_bounds__(T < NT ? NT : T) void k_rms_norm_bwd(NormArgs a) {
-  constexpr int G = T < NT ? NT / T : 1;   // rows of a workgroup at a time
-  __shared__ float buf[2][T / 64 * 2];
+template <int T, int C, bool DH>
+__global__ __launch_bounds__(bwd_threads(T, C, DH)) void k_rms_norm_bwd(NormArgs a) {
+  constexpr bool AHEAD = bwd_ahead(C, DH);
+  constexpr int G = bwd_threads(T, C, DH) / T;   // rows of a workgroup at a time
+  __shared__ float buf[2][T / 64 * 2 * G];
   __shared__ float sum[G > 1 ? (G - 1) * T * C * 8 : 1];
   const int t = threadIdx.x % T, chunks = a.dim >> 3;
   const u32x4 one = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
@@ -153,11 +161,14 @@ __global__ __launch_bounds__(T < NT ? NT : T) void k_rms_norm_bwd(NormArgs a) {
   BwdRow<T, C, DH> now, next;
   if (AHEAD && first < a.rows) next.load(a, first, t, chunks);
   int turn = 0;
-  for (int64_t row = first; row < a.rows; row += step, turn ^= 1) {
+  // (rows of several waves wait for each other's: as many turns for all)
+  const int64_t lead = T > 64 ? threadIdx.x / T : 0;
+  for (int64_t row = first; row - lead < a.rows; row += step, turn ^= 1) {
+    const bool real = row < a.rows;
     if constexpr (AHEAD) {
       now = next;
       if (row + step < a.rows) next.load(a, row + step, t, chunks);
-    } else {
+    } else if (real) {
       now.load(a, row, t, chunks);
     }
     float s[2] = {0.0f, 0.0f};
@@ -174,6 +185,7 @@ __global__ __launch_bounds__(T < NT ? NT : T) void k_rms_norm_bwd(NormArgs a) {
       }
     }
     row_sum<T, 2>(s, buf[turn]);
+    if (!real) break;
     const float r = 1.0f / sqrtf(s[0] * a.inv_dim + a.eps);
     const float m = s[1] * a.inv_dim * r * r;
 #pragma unroll
@@ -324,22 +336,25 @@ Shape bwd_shape_of(int32_t dim) {
   const Shape sh = shape_of(dim);
   return sh.t == 1024 && sh.c == 2 ? Shape{512, 4} : sh;
 }
-int64_t bwd_wgs(int64_t rows, const Shape& s) {
-  const int per = s.t < NT ? NT / s.t : 1;
-  const int64_t wgs = (rows + per - 1) / per, most = s.t >= 512 ? 256 : 512;
+int64_t bwd_wgs(int64_t rows, const Shape& s, bool dh) {
+  const int threads = bwd_threads(s.t, s.c, dh), per = threads / s.t;
+  const int64_t wgs = (rows + per - 1) / per, most = threads >= 512 ? 256 : 512;
   return wgs < most ? wgs : most;
 }
 
 }  // namespace
 
-// a launch with the flag where the run-time shape is T x C
-#define NORM_CASE(T, C, KT, KF)                                                              \
-  if (sh.t == T && sh.c == C) {                                                              \
-    if (flag) hipLaunchKernelGGL(KT, g, dim3(T < NT ? NT : T), 0, s, a);                     \
-    else hipLaunchKernelGGL(KF, g, dim3(T < NT ? NT : T), 0, s, a);                          \
+// a launch with the flag, in workgroups of W1 and W0 threads with and without it, where the run-time shape is T x C
+#define NORM_CASE(T, C, W1, W0, KT, KF)                               \
+  if (sh.t == T && sh.c == C) {                                       \
+    if (flag) hipLaunchKernelGGL(KT, g, dim3(W1), 0, s, a);           \
+    else hipLaunchKernelGGL(KF, g, dim3(W0), 0, s, a);                \
   }
-#define FWD_CASE(T, C) NORM_CASE(T, C, (k_rms_norm<T, C, true>), (k_rms_norm<T, C, false>))
-#define BWD_CASE(T, C) NORM_CASE(T, C, (k_rms_norm_bwd<T, C, true>), (k_rms_norm_bwd<T, C, false>))
+#define FWD_CASE(T, C) \
+  NORM_CASE(T, C, T < NT ? NT : T, T < NT ? NT : T, (k_rms_norm<T, C, true>), (k_rms_norm<T, C, false>))
+#define BWD_CASE(T, C)                                                             \
+  NORM_CASE(T, C, bwd_threads(T, C, true), bwd_threads(T, C, false), (k_rms_norm_bwd<T, C, true>), \
+            (k_rms_norm_bwd<T, C, false>))
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
   const Shape sh = shape_of(a.dim);
@@ -358,11 +373,12 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-size_t norm_part_floats(int64_t rows, int32_t dim) { return (size_t)bwd_wgs(rows, bwd_shape_of(dim)) * dim; }
+// (with dh there are as many workgroups as without, or more)
+size_t norm_part_floats(int64_t rows, int32_t dim) { return (size_t)bwd_wgs(rows, bwd_shape_of(dim), true) * dim; }
 
 hipError_t launch_rms_norm_bwd(const NormArgs& a, float* dw, hipStream_t s) {
   const Shape sh = bwd_shape_of(a.dim);
-  const int64_t wgs = bwd_wgs(a.rows, sh);
+  const int64_t wgs = bwd_wgs(a.rows, sh, a.dh.data != nullptr);
   {
     const dim3 g((unsigned)wgs);
     const bool flag = a.dh.data != nullptr;
@@ -374,7 +390,7 @@ hipError_t launch_rms_norm_bwd(const NormArgs& a, float* dw, hipStream_t s) {
     BWD_CASE(256, 3)
     BWD_CASE(256, 4)
     BWD_CASE(512, 4)
-    NORM_CASE(1024, 4, (k_rms_norm_bwd_long<true>), (k_rms_norm_bwd_long<false>))
+    NORM_CASE(1024, 4, 1024, 1024, (k_rms_norm_bwd_long<true>), (k_rms_norm_bwd_long<false>))
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
