@@ -565,7 +565,8 @@ qlora_status qlora_gated_fwd(const uint16_t* X, int64_t M, const qlora_nf4* gate
   for (const void* p : {(const void*)X, (const void*)A_gate, (const void*)B_gate, (const void*)A_up, (const void*)B_up,
                         (const void*)H, (const void*)G, (const void*)U, (const void*)T_gate, (const void*)T_up})
     if (!aligned16(p)) return QLORA_ERR_ALIGN;
-  if (M > 0 && ((G && (G == U || G == H || U == H)) || (T_gate && T_gate == T_up))) return QLORA_ERR_SHAPE;
+  if (M > 0 && (H == X || (G && (G == U || G == H || U == H || G == X || U == X)) || (T_gate && T_gate == T_up)))
+    return QLORA_ERR_SHAPE;   // (no output in place)
   const int64_t in = gate->cols, out = gate->rows, rp = rank_pad(r);
   const GatedWs need = gated_layout(nullptr, M, in, out, r);
   if (!ws || ws_bytes < need.bytes) return QLORA_ERR_WORKSPACE;

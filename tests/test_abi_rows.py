@@ -171,7 +171,8 @@ def test_outputs_that_would_overlap(lib):
     assert lib.qlora_token_logprob_bwd(P, 100, 3, 100, 1, Q, 1.0, Q, Q, None, None, P, 101, None) == SHAPE
     w = _w()
     need = lib.qlora_gated_workspace(3, 64, 128, 8)
-    for H, G, U, Tg, Tu in ((R, R, S, None, None), (R, S, R, None, None), (R, S, S, None, None), (R, None, None, S, S)):
+    for H, G, U, Tg, Tu in ((P, None, None, None, None), (R, P, S, None, None), (R, S, P, None, None), (R, R, S, None, None),
+                            (R, S, R, None, None), (R, S, S, None, None), (R, None, None, S, S)):
         st = lib.qlora_gated_fwd(P, 3, C.byref(w), C.byref(w), P, P, P, P, 8, 0.5, 0, H, G, U, Tg, Tu, S, need, None)
         assert st == SHAPE
 
