@@ -137,8 +137,8 @@ __device__ __forceinline__ RowEnd finish_row(const LpArgs& a, int64_t row, const
                                              bool write) {
   RowEnd r;
   r.m = top * a.scale;
-  // (a finite logit whose product with the scale is infinite counts as that infinity)
-  if (r.m == -INFINITY) z = 0.0f;
+  // (a finite logit whose product with the scale is infinite counts as that infinity; a NaN, which the maximum passes over, stays in z)
+  if (r.m == -INFINITY && z == z) z = 0.0f;
   if (r.m == INFINITY) z = NAN;
   r.empty = z == 0.0f;
   r.logz = logf(z);

@@ -465,8 +465,8 @@ typedef enum { QLORA_BF16 = 0, QLORA_FP32 = 1 } qlora_dtype;
  *   top_logprob, top_index [row][top]: the `top` most likely tokens and their log probabilities, in descending order; equal
  *   logits by the lower index, NaN before all.
  * logprob may be NULL (then token may be too).  Logits of -infinity have probability 0.  A row of nothing else has
- * m = -infinity, z = 0, logprob and top_logprob -infinity, entropy 0.  A NaN or +infinity makes its row's logprob and
- * entropy NaN.  A finite logit whose product with the scale overflows counts as the infinity of its sign.  fp32 throughout; the same call gives the same bits.
+ * m = -infinity, z = 0, logprob and top_logprob -infinity, entropy 0.  A NaN or +infinity makes its row's z, logprob and
+ * entropy NaN, a NaN beside nothing but -infinity too.  A finite logit whose product with the scale overflows counts as the infinity of its sign.  fp32 throughout; the same call gives the same bits.
  * Requires: 1 <= vocab <= 2^20, 0 <= rows < 2^22, rows * vocab < 2^35; any stride from 0 to 2^36 - 1 and pointers aligned to their elements (rows may
  * start anywhere); 0 <= top <= 32, top <= vocab; scale finite and > 0; ws of qlora_token_logprob_workspace bytes, 16-byte
  * aligned (it grows with rows, vocab and top, so that of the largest call serves smaller ones; 0, and ws may be NULL, up to 32768

@@ -1,0 +1,56 @@
+"""Log probabilities and their gradient at the ends of their ranges: NaN in rows that have nothing else, NaN at the first
+token, gradients of the entropy of any size, rows without a token, scales of any size.  (The sums of ordinary rows are in
+test_gpu_logprob.py, whose tolerances are used here.)"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import bit_nf4_quantized_11_amd as Q
+from helpers import log, require_gpu
+from oracle import rows as oracle
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = math.nan, math.inf
+TYPES = [torch.bfloat16, torch.float32]
+# rows, vocab: a wave to a row, one part of several waves, several parts, parts of many rows
+SHAPES = [(8, 40), (8, 700), (8, 9000), (8, 50000), (136, 40000)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("n,v", SHAPES)
+def test_nan_without_a_logit(dtype, n, v):
+    """A NaN makes its row NaN also where nothing else of the row is above -infinity; without one such a row is empty."""
+    require_gpu()
+    log("logprob nan", dtype, n, v)
+    x = torch.full((n, v), -INF)
+    x[0] = NAN
+    x[1, v // 2] = NAN
+    x[2, v - 1] = NAN
+    x[3, 1:4] = -NAN
+    x[5] = torch.finfo(dtype).min            # (its products with the scale are -infinity)
+    x[6] = torch.finfo(dtype).min
+    x[6, v // 3] = NAN
+    x[7, 5] = 1.0
+    x = x.to(dtype).cuda()
+    token = torch.full((n,), 7, device="cuda")
+    token[2] = -1
+    for top in (0, 1, 20):
+        lp, stats, ent, tlp, tix = Q.qlora_token_logprob(x, token, 2.0, entropy=True, top=top)
+        bad, empty = [0, 1, 2, 3, 6], [4, 5]
+        assert ent[bad].isnan().all() and stats[bad, 1].isnan().all()
+        assert lp[[0, 1, 3, 6]].isnan().all() and lp[2] == 0
+        assert torch.all(ent[empty] == 0) and torch.all(lp[empty] == -INF)
+        assert torch.all(stats[empty, 0] == -INF) and torch.all(stats[empty, 1] == 0)
+        assert lp[7] == -INF and ent[7] == 0 and stats[7].tolist() == [2.0, 1.0]
+        if top:
+            assert tlp[bad].isnan().all() and torch.all(tlp[empty] == -INF) and tlp[7, 0] == 0
+            assert tix[[1, 2, 3, 6, 7], 0].tolist() == [v // 2, v - 1, 1, v // 3, 5]
+    one = torch.ones(n, device="cuda")
+    for args in ((one, None, None), (None, ent, one), (one, ent, one)):
+        g = Q.qlora_token_logprob_bwd(x, token, stats, *args, 2.0)
+        assert g[[0, 1, 3, 6]].isnan().all() and torch.all(g[empty] == 0) and g[7].isfinite().all()
+        if args[2] is not None:
+            assert g[2].isnan().all()
