@@ -102,16 +102,18 @@ __device__ __forceinline__ void load_pieces(uint4 (&v)[C], const typename Elem<F
     if (col + i * step + E > n) v[i] = load_edge<F32>(row, col + i * step, n);
 }
 
-// Larger numbers for larger values; NaN above all, both zeros the same.  Never 0.
+// Larger numbers for larger values; NaN above all (+infinity is 0xFF800000), both zeros the same.  Never 0, nor all ones, which
+// with the inverted index 0 would make an entry that none is below.
+constexpr uint32_t kNanOrder = 0xFFFFFFFEu;
 __device__ __forceinline__ uint32_t order_of(float x) {
-  if (x != x) return 0xFFFFFFFFu;
+  if (x != x) return kNanOrder;
   const uint32_t b = x == 0.0f ? 0u : __float_as_uint(x);
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ u64 entry_of(float x, int col) { return (u64)order_of(x) << 32 | (0xFFFFFFFFu - (uint32_t)col); }
 __device__ __forceinline__ float value_of(u64 e) {
   const uint32_t k = (uint32_t)(e >> 32);
-  if (k == 0xFFFFFFFFu) return NAN;
+  if (k == kNanOrder) return NAN;
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 __device__ __forceinline__ int col_of(u64 e) { return (int)(0xFFFFFFFFu - (uint32_t)e); }

@@ -54,3 +54,23 @@ def test_nan_without_a_logit(dtype, n, v):
         assert g[[0, 1, 3, 6]].isnan().all() and torch.all(g[empty] == 0) and g[7].isfinite().all()
         if args[2] is not None:
             assert g[2].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("n,v", [(4, 1), (4, 3), (4, 32), *SHAPES])
+def test_nan_at_the_first_token(dtype, n, v):
+    """NaN before all else, equal ones by the lower index, from token 0 on; as many alternatives as tokens."""
+    require_gpu()
+    log("logprob first nan", dtype, n, v)
+    x = torch.randn(n, v, generator=torch.Generator().manual_seed(v))
+    x[0] = NAN
+    x[1, 0] = NAN
+    x[2, 0] = -NAN
+    x[2, v - 1] = NAN
+    x = x.to(dtype)
+    key = torch.where(x.isnan(), INF, x.double())
+    want = torch.sort(key, dim=1, descending=True, stable=True)[1]
+    for top in {1, min(v, 3), min(v, 32)}:
+        _, _, _, tlp, tix = Q.qlora_token_logprob(x.cuda(), None, top=top)
+        assert torch.equal(tix.cpu(), want[:, :top]), top
+        assert tlp[:3].isnan().all() and tlp[3].isfinite().all()
