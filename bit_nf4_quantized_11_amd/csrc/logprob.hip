@@ -502,8 +502,7 @@ __global__ __launch_bounds__(BT) void k_token_logprob_bwd(LpBwdArgs a, unsigned 
   const float dent = a.dent ? a.dent[row] : 0.0f;
   const float rz = empty ? 0.0f : 1.0f / z, logz = empty ? 0.0f : logf(z);
   const float from = empty ? 0.0f : m;
-  // -p (dlp + dent (ln p + entropy)) = -p (c + dent d),  c = dlp + dent (entropy - ln z)
-  const float c = a.dent ? __builtin_fmaf(dent, a.entropy[row] - logz, dlp) : dlp;
+  const float rest = a.dent ? a.entropy[row] - logz : 0.0f;   // ln p + entropy = d + rest
 #pragma unroll
   for (int i = 0; i < BC; ++i) {
     const int col = col0 + i * BT * E;
@@ -514,7 +513,8 @@ __global__ __launch_bounds__(BT) void k_token_logprob_bwd(LpBwdArgs a, unsigned 
     for (int j = 0; j < E; ++j) {
       const float d = f[j] * a.scale - from;
       const float p = __builtin_amdgcn_exp2f(d * kLog2e) * rz;
-      float g = -p * __builtin_fmaf(dent, fmaxf(d, -1e30f), c);
+      // (p first: a gradient of the entropy times ln p alone can be infinite where p is 0.  Nothing of a logit of -infinity)
+      float g = -__builtin_fmaf(dent, p * (fmaxf(d, -1e30f) + rest), p * dlp);
       if (col + j == token && !empty) g += dlp;
       f[j] = g * a.scale;
     }

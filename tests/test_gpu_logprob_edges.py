@@ -74,3 +74,42 @@ def test_nan_at_the_first_token(dtype, n, v):
         _, _, _, tlp, tix = Q.qlora_token_logprob(x.cuda(), None, top=top)
         assert torch.equal(tix.cpu(), want[:, :top]), top
         assert tlp[:3].isnan().all() and tlp[3].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("size", [1e-30, 1.0, 3e8, 1e20, 1e30, 1e37])
+def test_entropy_gradients_of_any_size(dtype, size):
+    """-dent p (ln p + H) and dlp (1[v] - p) where p is 0 (masked and far tokens) and where it is not."""
+    require_gpu()
+    log("logprob dent", dtype, size)
+    n, v = 6, 3000
+    gen = torch.Generator().manual_seed(1)
+    x = torch.randn(n, v, generator=gen) * 2
+    x[:, ::3] = -INF
+    x[1, 1::3] = torch.finfo(dtype).min
+    x[2, 1::3] = -1e4
+    x[3] = -INF
+    x = x.to(dtype)
+    token = torch.tensor([1, 2, 5, 1, -1, 8])
+    d1, d2 = (torch.randn(n, generator=gen) * size for _ in range(2))
+    _, stats, ent, _, _ = Q.qlora_token_logprob(x.cuda(), token.cuda(), entropy=True)
+    x64, f64 = x.double().numpy(), lambda t: t.double().numpy()
+    lp = oracle.log_softmax(x64)[0]
+    live = np.isfinite(lp)
+    p, ll = np.where(live, np.exp(np.where(live, lp, 0)), 0), np.where(live, np.abs(lp), 0)
+    plp = p * np.minimum(ll, 1e6)
+    H = plp.sum(-1, keepdims=True)
+    for a1, a2 in ((d1, d2), (None, d2), (d1, None)):
+        got = Q.qlora_token_logprob_bwd(x.cuda(), token.cuda(), stats, None if a1 is None else a1.cuda(), ent,
+                                        None if a2 is None else a2.cuda())
+        want = oracle.token_logprob_bwd(x64, token.numpy(), 1.0, None if a1 is None else f64(a1), None if a2 is None else f64(a2))
+        # logits below 16 and ln p above -2^5 where p counts: z is 2^-16 off and the entropy 2^-14 (H and ln z below 2^3), so p, and
+        # what it is multiplied by, less than 2^-13 of p and of their terms; then one rounding of the type
+        b1 = np.zeros((n, 1)) if a1 is None else np.abs(f64(a1))[:, None]
+        b2 = np.zeros((n, 1)) if a2 is None else np.abs(f64(a2))[:, None]
+        tol = 2.0 ** -13 * (p * b1 + b2 * (plp + p * (H + 1)))
+        tol[np.arange(n), np.maximum(token.numpy(), 0)] += 2.0 ** -23 * b1[:, 0]
+        step = torch.finfo(dtype).eps / 2
+        got = got.double().cpu().numpy()
+        assert np.all(np.abs(got - want) <= tol * (1 + step) + step * np.abs(want) + 2.0 ** -126)
+        assert np.all(got[~live & (np.arange(v) != token.numpy()[:, None])] == 0)
