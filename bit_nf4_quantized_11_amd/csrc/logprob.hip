@@ -497,26 +497,28 @@ __global__ __launch_bounds__(BT) void k_token_logprob_bwd(LpBwdArgs a, unsigned 
   load_pieces<F32, BC>(v, x, col0, BT * E, a.vocab);
   const int64_t token = a.token ? a.token[row] : -1;
   const float m = a.stats[2 * row], z = a.stats[2 * row + 1];
-  const bool empty = z == 0.0f;
   const float dlp = token >= a.vocab ? NAN : token >= 0 && a.dlp ? a.dlp[row] : 0.0f;
   const float dent = a.dent ? a.dent[row] : 0.0f;
-  const float rz = empty ? 0.0f : 1.0f / z, logz = empty ? 0.0f : logf(z);
-  const float from = empty ? 0.0f : m;
+  // rows whose gradient is 0 whatever their logits (padding may hold NaN) and the gradients are: without a token, and empty ones
+  const bool none = (token < 0 && !a.dent) || (z == 0.0f && token < a.vocab);
+  const float rz = 1.0f / z, logz = logf(z);
   const float rest = a.dent ? a.entropy[row] - logz : 0.0f;   // ln p + entropy = d + rest
 #pragma unroll
   for (int i = 0; i < BC; ++i) {
     const int col = col0 + i * BT * E;
     if (col >= a.vocab) break;
-    float f[E];
-    X::unpack(v[i], f);
+    float f[E] = {};
+    if (!none) {
+      X::unpack(v[i], f);
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const float d = f[j] * a.scale - from;
-      const float p = __builtin_amdgcn_exp2f(d * kLog2e) * rz;
-      // (p first: a gradient of the entropy times ln p alone can be infinite where p is 0.  Nothing of a logit of -infinity)
-      float g = -__builtin_fmaf(dent, p * (fmaxf(d, -1e30f) + rest), p * dlp);
-      if (col + j == token && !empty) g += dlp;
-      f[j] = g * a.scale;
+      for (int j = 0; j < E; ++j) {
+        const float d = f[j] * a.scale - m;
+        const float p = __builtin_amdgcn_exp2f(d * kLog2e) * rz;
+        // (p first: a gradient of the entropy times ln p alone can be infinite where p is 0.  Nothing of a logit of -infinity)
+        float g = -__builtin_fmaf(dent, p * (fmaxf(d, -1e30f) + rest), p * dlp);
+        if (col + j == token) g += dlp;
+        f[j] = g * a.scale;
+      }
     }
     if (col + E <= a.vocab) {
       store_any(dx + col, X::pack(f));

@@ -480,8 +480,9 @@ qlora_status qlora_token_logprob(const void* logits, int64_t stride, int64_t row
 /* Its backward: from the gradients of logprob and of entropy (fp32 [rows], either may be NULL, not both), the forward's
  * stats and, with dentropy, its entropy:
  *   dlogits[row][v] = scale (dlogprob (1[v = token] - p_v) - dentropy p_v (ln p_v + entropy)),   p_v = e^(x_v - m) / z
- * in the logits' type.  A row with token < 0 has no gradient from dlogprob, one with token >= vocab is NaN; a row without a
- * logit above -infinity has gradient 0.  dlogits may be the logits (same data and stride); no other overlap.
+ * in the logits' type.  A row with token < 0 has no gradient from dlogprob, whatever its logits and its dlogprob are (with
+ * dentropy NULL it is 0); one with token >= vocab is NaN; a row without a logit above -infinity has gradient 0, whatever those of
+ * its logprob and entropy are.  dlogits may be the logits (same data and stride); no other overlap.
  * Requires: as the forward; dlogits_stride >= vocab.                                                     */
 qlora_status qlora_token_logprob_bwd(const void* logits, int64_t stride, int64_t rows, int64_t vocab, int32_t dtype,
                                      const int64_t* token, float scale, const float* stats, const float* dlogprob,

@@ -113,3 +113,51 @@ def test_entropy_gradients_of_any_size(dtype, size):
         got = got.double().cpu().numpy()
         assert np.all(np.abs(got - want) <= tol * (1 + step) + step * np.abs(want) + 2.0 ** -126)
         assert np.all(got[~live & (np.arange(v) != token.numpy()[:, None])] == 0)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("n,v", SHAPES)
+def test_rows_without_a_token(dtype, n, v):
+    """A row without a token has no gradient of its log probability, whatever its logits and its dlogprob are: the padding
+    of a batch may hold anything."""
+    require_gpu()
+    log("logprob no token", dtype, n, v)
+    gen = torch.Generator().manual_seed(v)
+    x = torch.randn(n, v, generator=gen)
+    x[1] = NAN
+    x[2, 5] = INF
+    x[3, v - 1] = NAN
+    x[4] = -INF
+    x = x.to(dtype).cuda()
+    token = torch.randint(0, v, (n,), generator=gen).cuda()
+    token[1:6] = -100
+    lp, stats, _, _, _ = Q.qlora_token_logprob(x, token)
+    assert torch.all(lp[1:6] == 0)
+    d = torch.randn(n, generator=gen).cuda()
+    d[2], d[5] = INF, NAN
+    g = Q.qlora_token_logprob_bwd(x, token, stats, d)
+    assert torch.all(g[1:6] == 0) and g[0].isfinite().all() and g[6:].isfinite().all()
+    y = x.clone()
+    assert torch.equal(Q.qlora_token_logprob_bwd(y, token, stats, d, out=y), g)
+    # beside the entropy's gradient: that one alone
+    ent = Q.qlora_token_logprob(x, token, entropy=True)[2]
+    e = torch.randn(n, generator=gen).cuda()
+    both, alone = (Q.qlora_token_logprob_bwd(x, token, stats, a, ent, e) for a in (d, None))
+    assert torch.equal(both[4:6], alone[4:6]) and both[5].isfinite().all() and both[[1, 2, 3]].isnan().any(1).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_empty_rows_have_no_gradient(dtype):
+    """Also where what comes back for their log probability of -infinity is infinite or NaN; a token past the vocabulary stays NaN."""
+    require_gpu()
+    n, v = 6, 3000
+    x = torch.full((n, v), -INF, dtype=dtype, device="cuda")
+    x[1] = torch.finfo(dtype).min            # (times the scale)
+    x[5, 3] = 0.0
+    token = torch.tensor([0, 1, 2, -1, v, 3], device="cuda")
+    _, stats, ent, _, _ = Q.qlora_token_logprob(x, token, 2.0, entropy=True)
+    d, e = torch.tensor([INF, NAN, -INF, 1.0, 1.0, 1.0], device="cuda"), torch.tensor([NAN, 1.0, INF, NAN, 0.0, 1.0], device="cuda")
+    for a, b in ((d, None), (None, e), (d, e)):
+        g = Q.qlora_token_logprob_bwd(x, token, stats, a, ent, b, 2.0)
+        assert torch.all(g[:4] == 0) and torch.all(g[5] == 0)
+        assert g[4].isnan().all() if a is not None else torch.all(g[4] == 0)
