@@ -129,7 +129,7 @@ struct Given {
   }
 };
 
-// What the forward leaves of a row, from its whole sums (the largest logit, and the others for scaled ones).
+// What the forward leaves of a row, from its whole sums (of `unit` times these).
 struct RowEnd {
   float m, logz;
   bool empty;   // no logit above -infinity
@@ -138,7 +138,7 @@ template <bool F32>
 __device__ __forceinline__ RowEnd finish_row(const LpArgs& a, int64_t row, const Given<F32>& g, float top, float z, float s,
                                              bool write) {
   RowEnd r;
-  r.m = top * a.scale;
+  r.m = top * a.unit;
   // (a finite logit whose product with the scale is infinite counts as that infinity; a NaN, which the maximum passes over, stays in z)
   if (r.m == -INFINITY && z == z) z = 0.0f;
   if (r.m == INFINITY) z = NAN;
@@ -147,7 +147,7 @@ __device__ __forceinline__ RowEnd finish_row(const LpArgs& a, int64_t row, const
   if (!write) return r;
   a.stats[2 * row] = r.m;
   a.stats[2 * row + 1] = z;
-  if (a.entropy) a.entropy[row] = r.empty ? 0.0f : r.logz - s * (a.scale / z);
+  if (a.entropy) a.entropy[row] = r.empty ? 0.0f : r.logz - s * (a.unit / z);
   if (a.logprob)
     a.logprob[row] = g.token >= a.vocab ? NAN : g.token < 0 ? 0.0f : r.empty ? -INFINITY : (g.x * a.scale - r.m) - r.logz;
   return r;
@@ -246,22 +246,27 @@ __global__ __launch_bounds__(NT) void k_token_logprob(LpArgs a) {
 #pragma unroll
     for (int j = 0; j < E; ++j) top = fmaxf(top, f[j]);
   }
-  const float mine_m = wave_max(top);
-  const float from = mine_m == -INFINITY ? 0.0f : mine_m, by = a.scale * kLog2e;
+  const bool far = a.unit != a.scale;
+  const float mine_m = wave_max(top) * (far ? a.scale : 1.0f);
+  const float from = mine_m == -INFINITY ? 0.0f : mine_m, by = a.unit * kLog2e;
   float z = 0.0f, s = 0.0f;
+  const auto sums = [&](float first) {
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    float f[E];
-    X::unpack(v[i], f);
+    for (int i = 0; i < C; ++i) {
+      float f[E];
+      X::unpack(v[i], f);
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      // (the difference of the logits first: no product of a large one can overflow, and equal ones give 0)
-      const float d = f[j] - from;
-      const float e = __builtin_amdgcn_exp2f(d * by);
-      z += e;
-      s = __builtin_fmaf(e, fmaxf(d, -1e30f), s);   // (nothing of a logit of -infinity)
+      for (int j = 0; j < E; ++j) {
+        // (the difference before the scale: equal ones give 0)
+        const float d = f[j] * first - from;
+        const float e = __builtin_amdgcn_exp2f(d * by);
+        z += e;
+        s = __builtin_fmaf(e, fmaxf(d, -1e30f), s);   // (nothing of a logit of -infinity)
+      }
     }
-  }
+  };
+  if (far) sums(a.scale);
+  else sums(1.0f);
   z = wave_sum(z);
   s = wave_sum(s);
   if (lane == 0) red[0][wave] = mine_m, red[1][wave] = z, red[2][wave] = s;
@@ -458,7 +463,7 @@ __global__ __launch_bounds__(64 * JW) void k_logprob_join(LpArgs a) {
   }
   const float mm = wave_max(m);
   const float d = m == -INFINITY ? 0.0f : m - mm;
-  const float e = __builtin_amdgcn_exp2f(d * (a.scale * kLog2e));
+  const float e = __builtin_amdgcn_exp2f(d * (a.unit * kLog2e));
   s = e * __builtin_fmaf(z, fmaxf(d, -1e30f), s);
   z = wave_sum(e * z);
   s = wave_sum(s);

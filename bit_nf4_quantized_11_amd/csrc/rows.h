@@ -72,7 +72,7 @@ hipError_t launch_rms_norm_bwd(const NormArgs& a, float* dw, hipStream_t s);
 constexpr int kLpMaxTop = 32;
 constexpr int kLpMaxSegs = 32;       // parts of a row at most
 constexpr int64_t kLpMaxVocab = int64_t(1) << 20;
-// One part of a row: largest scaled logit, sum of exponentials from it, sum of exponential times logit from it.
+// One part of a row, of x in units of LpArgs::unit: the largest, the sum of exponentials from it, and that of each times its distance.
 struct LpPart {
   float m, z, s;
   uint32_t pad_;
@@ -84,6 +84,7 @@ struct LpArgs {
   int32_t vocab;
   int32_t fp32;
   float scale;
+  float unit;                 // what the sums' logits are yet to be multiplied with: the scale, or 1 where it is applied first
   int32_t top;
   const int64_t* token;       // or NULL
   float* logprob;             // or NULL

@@ -161,3 +161,49 @@ def test_empty_rows_have_no_gradient(dtype):
         g = Q.qlora_token_logprob_bwd(x, token, stats, a, ent, b, 2.0)
         assert torch.all(g[:4] == 0) and torch.all(g[5] == 0)
         assert g[4].isnan().all() if a is not None else torch.all(g[4] == 0)
+
+
+# scale, logits of size: products of ordinary size from factors at the ends of fp32, sums of logits past it, products past it
+SCALES = [(1.5 * 2.0 ** 127, 2.0 ** -126), (2.4e38, 0.0), (3e30, 1e-30), (1e-28, 1e28), (1e-33, 2e33), (1e-38, 3e38), (2.0 ** -127, 2e38),
+          (1e-38, 1.0)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("n,v", [(3, 40), (3, 9000), (3, 50000), (130, 40000)])
+@pytest.mark.parametrize("scale,size", SCALES)
+def test_scales_of_any_size(scale, size, n, v, dtype):
+    """Everything is of x = fl32(scale logit): forward and backward agree on it however large or small the factors are."""
+    require_gpu()
+    log("logprob scale", scale, size, n, v, dtype)
+    gen = torch.Generator().manual_seed(v)
+    x = ((torch.rand(n, v, generator=gen) * 2 - 1) * size).to(dtype)
+    x[1, ::2] = -INF
+    x[2, 1] = 0.0
+    token = torch.full((n,), 1)
+    s32 = np.float32(scale)
+    xs = (x.float().numpy() * s32).astype(np.float64)   # rounded to fp32, as defined
+    k = min(v, 8)
+    lp, stats, ent, tlp, tix = Q.qlora_token_logprob(x.cuda(), token.cuda(), scale, entropy=True, top=k)
+    w_lp, m, z, w_ent, _, _ = oracle.token_logprob(xs, token.numpy(), 1.0, k)
+    order = torch.sort(x.double(), dim=1, descending=True, stable=True)[1][:, :k]
+    w_tlp = np.take_along_axis(oracle.log_softmax(xs)[0], order.numpy(), 1)
+    h = lambda t: t.double().cpu().numpy()
+    # |x| at most 3: sums 2^-16 off, so logarithms 2^-15, and the entropy by twice that of the mean of d (at most 6): below 2^-12
+    assert np.array_equal(h(stats[:, 0]), m) and np.all(np.abs(h(stats[:, 1]) - z) <= 2.0 ** -15 * z)
+    assert np.all(np.abs(h(ent) - w_ent) <= 2.0 ** -12) and torch.equal(tix.cpu(), order)
+    f = np.isfinite(w_lp)
+    assert np.all(np.abs(h(lp) - w_lp)[f] <= 2.0 ** -14) and np.all(h(lp)[~f] == w_lp[~f])
+    assert np.all(np.abs(h(tlp) - w_tlp) <= 2.0 ** -14)
+    d1, d2 = torch.randn(n, generator=gen), torch.randn(n, generator=gen)
+    g = Q.qlora_token_logprob_bwd(x.cuda(), token.cuda(), stats, d1.cuda(), ent, d2.cuda(), scale)
+    want = oracle.token_logprob_bwd(xs, token.numpy(), 1.0, d1.double().numpy(), d2.double().numpy())
+    p = np.exp(oracle.log_softmax(xs)[0])
+    # (before the product with the scale; the factors of p are below 2^5 in all, and 2^-12 off; results of less than the least
+    # normal number may be anything between 0 and it)
+    tol = 2.0 ** -10 * p * (np.abs(d1.numpy()) + np.abs(d2.numpy()))[:, None]
+    tol[:, 1] += 2.0 ** -22 * np.abs(d1.numpy())
+    step = torch.finfo(dtype).eps / 2
+    s64 = float(s32)
+    with np.errstate(over="ignore"):
+        big = np.abs(want) * s64 > 2.0 ** 127
+        assert np.all((np.abs(h(g) - want * s64) <= 1.01 * s64 * tol + 1.01 * step * s64 * np.abs(want) + 2.0 ** -126)[~big])
