@@ -465,10 +465,27 @@ GemvPlan gemv_plan(int64_t M, int64_t K, int64_t N, int64_t rp, bool adapters_on
     const int64_t want = std::max<int64_t>(1, (gated ? room / 2 : 256) / (pl.agroups * pl.ngr));
     ka = std::max<int64_t>(256, ((K + want - 1) / want + 255) / 256 * 256);
   }
-  pl.ka = (int)std::min<int64_t>(ka, (K + 63) / 64 * 64);
-  pl.asplits = (int)((K + pl.ka - 1) / pl.ka);
-  const int64_t aw = pl.agroups * pl.asplits * pl.ngr;
-  pl.rranges = std::max<int64_t>(1, std::min<int64_t>(pl.rgroups, (slots - aw) / pl.splits));
+  int64_t aw = 0;
+  const auto cut = [&](int64_t rows) {
+    pl.ka = (int)std::min<int64_t>(rows, (K + 63) / 64 * 64);
+    pl.asplits = (int)((K + pl.ka - 1) / pl.ka);
+    aw = pl.agroups * pl.asplits * pl.ngr;
+    pl.rranges = std::max<int64_t>(1, std::min<int64_t>(pl.rgroups, (slots - aw) / pl.splits));
+  };
+  cut(ka);
+  // Adapter slices of KA rows of both sides can take every slot (rank 256, 64 tokens, 16384 inputs: 128 a side), which leaves the weights'
+  // rows to a single range: where they take a quarter, twice as long slices, four times, ... are weighed, the longer of a slice's
+  // chunks and a range's row groups, each of which costs as much as 3 to 6 chunks.  64 tokens of 16384 -> 53248: rank 256 5205 -> 495 us
+  // (two linear calls 823), rank 64 510 -> 460; 16 of 22016 -> 8192, rank 256 103 -> 74.
+  if (gated && !adapters_only && aw >= slots / 4) {
+    const auto cost = [&] { return std::max<int64_t>(pl.ka / 64, (2 + pl.tg) * ((pl.rgroups + pl.rranges - 1) / pl.rranges)); };
+    int64_t best = cost();
+    for (int64_t rows = 2 * ka; rows < 2 * K && pl.asplits > 1; rows *= 2) {
+      cut(rows);
+      if (cost() < best) best = cost(), ka = rows;
+    }
+    cut(ka);
+  }
   pl.tpart = (size_t)pl.splits * Mm * pl.npad;
   return pl;
 }
