@@ -593,6 +593,14 @@ def qlora_kv_attn(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float 
 
 
 # ---- around the projections: the residual's norm, the gated block, log probabilities ---------------------------
+_I32 = 2 ** 31 - 1
+
+
+def _i32(n: int) -> int:
+    """n, or the end of 32 bits that it lies past: the library refuses these, where ctypes would drop n's upper bits."""
+    return max(-_I32, min(n, _I32))
+
+
 def _rows(t: torch.Tensor, name: str, device=None, shape=None):
     """(address, row stride) of a bf16 [rows][dim] tensor, any row stride with dense rows."""
     strides = t.stride()
@@ -630,7 +638,7 @@ def qlora_rms_norm(x: torch.Tensor, weight: torch.Tensor | None, residual: torch
     def run(stream):
         y, (py, sy) = _new_rows(out, "out", dev, x)
         h, (ph, sh) = (x, (None, 0)) if residual is None else _new_rows(sum_out, "sum_out", dev, x)
-        _check(lib().qlora_rms_norm(px, sx, pr, sr, shape[0], shape[1], _at(weight), eps, py, sy, ph, sh, stream),
+        _check(lib().qlora_rms_norm(px, sx, pr, sr, shape[0], min(shape[1], _I32), _at(weight), eps, py, sy, ph, sh, stream),
                "qlora_rms_norm")
         return y, h
 
@@ -638,7 +646,7 @@ def qlora_rms_norm(x: torch.Tensor, weight: torch.Tensor | None, residual: torch
 
 
 def qlora_rms_norm_bwd_workspace(rows: int, dim: int) -> int:
-    return lib().qlora_rms_norm_bwd_workspace(rows, dim)
+    return lib().qlora_rms_norm_bwd_workspace(rows, _i32(dim))
 
 
 def qlora_rms_norm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None, dh: torch.Tensor | None = None,
@@ -667,8 +675,8 @@ def qlora_rms_norm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor |
         if weight_grad:
             gw = torch.empty(shape[1], dtype=torch.float32, device=dev) if dweight is None else dweight
             ws = _bytes(workspace, dev, lambda: qlora_rms_norm_bwd_workspace(shape[0], shape[1]))
-        _check(lib().qlora_rms_norm_bwd(pg, sg, ph, sh, pd, sd, shape[0], shape[1], _at(weight), eps, px, sx, _at(gw),
-                                        _at(ws), 0 if ws is None else ws.nbytes, stream), "qlora_rms_norm_bwd")
+        _check(lib().qlora_rms_norm_bwd(pg, sg, ph, sh, pd, sd, shape[0], min(shape[1], _I32), _at(weight), eps, px, sx,
+                                        _at(gw), _at(ws), 0 if ws is None else ws.nbytes, stream), "qlora_rms_norm_bwd")
         return out, gw
 
     return _launch(dy, stream, run)
@@ -685,7 +693,7 @@ def _activation(name: str) -> int:
 
 
 def qlora_gated_workspace(M: int, d_in: int, d_out: int, r: int) -> int:
-    return lib().qlora_gated_workspace(M, d_in, d_out, r)
+    return lib().qlora_gated_workspace(M, d_in, d_out, _i32(r))
 
 
 def qlora_gated_fwd(X: torch.Tensor, gate: NF4Weight, up: NF4Weight, A_gate: torch.Tensor, B_gate: torch.Tensor,
@@ -771,7 +779,7 @@ def _logits(t: torch.Tensor, name: str, device=None, like=None):
 
 
 def qlora_token_logprob_workspace(rows: int, vocab: int, top: int = 0) -> int:
-    return lib().qlora_token_logprob_workspace(rows, vocab, top)
+    return lib().qlora_token_logprob_workspace(rows, vocab, _i32(top))
 
 
 def qlora_token_logprob(logits: torch.Tensor, token: torch.Tensor | None, scale: float = 1.0, entropy: bool = False,
@@ -800,8 +808,8 @@ def qlora_token_logprob(logits: torch.Tensor, token: torch.Tensor | None, scale:
                "qlora_token_logprob")
         return lp, stats, ent, tlp, tix
 
-    if top < 0:
-        raise QLoRAError("top must be 0 (none) or positive")
+    if not 0 <= top <= vocab:
+        raise QLoRAError(f"top must be 0 (none) to {vocab}, the number of logits")
     return _launch(logits, stream, run)
 
 
