@@ -1,5 +1,5 @@
-"""The gated block for few tokens where its adapters are large beside its weights: long reductions, rank 256, several
-token groups."""
+"""The gated block for few tokens where its adapters are large beside its weights (long reductions, rank 256, several token
+groups), and the ends of the largest one."""
 import numpy as np
 import pytest
 import torch
@@ -24,15 +24,12 @@ def _make(M, K, N, r):
     return X, w, A, B
 
 
-@pytest.mark.parametrize("case", CASES, ids=str)
-def test_large_adapters(case):
-    """Tolerances: products exact in fp32, K of them added in some order (K 2^-24 of the sum of magnitudes, in slices of which it is
-    far less), s T rounded to bf16 before its product with B, then one rounding; H: |act'| below 1.13, act within 2^-15."""
-    require_gpu()
-    log("gated few", case)
-    M, K, N, r = case
-    X, w, A, B = _make(*case)
-    H, G, U, Tg, Tu = Q.qlora_gated_fwd(X, w[0], w[1], A[0], B[0], A[1], B[1], 0.25, "silu")
+def _check(X, w, A, B, scale, outs):
+    """H, G, U and both X A against float64.  Tolerances: products exact in fp32, K of them added in some order (K 2^-24 of the sum
+    of magnitudes, in slices of which it is far less), s T rounded to bf16 before its product with B, then one rounding; H:
+    |act'| below 1.13, act within 2^-15."""
+    H, G, U, Tg, Tu = outs
+    K, r = A[0].shape
     f64 = lambda t: host(t.float()).astype(np.float64)
     x = f64(X)
     sums, tols = [], []
@@ -40,9 +37,9 @@ def test_large_adapters(case):
         W, a, b = f64(Q.qlora_dequant(w[i])), f64(A[i]), f64(B[i])
         T, magT = x @ a, np.abs(x) @ np.abs(a)
         assert np.all(np.abs(f64(gotT) - T) <= BF16 * np.abs(T) + 1.01 * K * E24 * magT), i
-        want = x @ W.T + 0.25 * T @ b
-        tol = 1.01 * (K + r + 16) * E24 * (np.abs(x) @ np.abs(W).T + 0.25 * np.abs(T) @ np.abs(b))
-        tol += 1.01 * 0.25 * (BF16 * np.abs(T) + K * E24 * magT) @ np.abs(b)
+        want = x @ W.T + scale * T @ b
+        tol = 1.01 * (K + r + 16) * E24 * (np.abs(x) @ np.abs(W).T + scale * np.abs(T) @ np.abs(b))
+        tol += 1.01 * scale * (BF16 * np.abs(T) + K * E24 * magT) @ np.abs(b)
         assert np.all(np.abs(f64(got) - want) <= 1.01 * BF16 * (np.abs(want) + tol) + tol), i
         sums.append(want)
         tols.append(tol)
@@ -50,8 +47,30 @@ def test_large_adapters(case):
     want = a * sums[1]
     tol = 1.13 * tols[0] * (np.abs(sums[1]) + tols[1]) + np.abs(a) * tols[1] + 2.0 ** -15 * np.abs(want)
     assert np.all(np.abs(f64(H) - want) <= 1.01 * BF16 * (np.abs(want) + tol) + tol + 2.0 ** -126)
+
+
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_large_adapters(case):
+    require_gpu()
+    log("gated few", case)
+    X, w, A, B = _make(*case)
+    outs = Q.qlora_gated_fwd(X, w[0], w[1], A[0], B[0], A[1], B[1], 0.25, "silu")
+    _check(X, w, A, B, 0.25, outs)
     again = Q.qlora_gated_fwd(X, w[0], w[1], A[0], B[0], A[1], B[1], 0.25, "silu")
-    assert all(torch.equal(p, q) for p, q in zip(again, (H, G, U, Tg, Tu)))
+    assert all(torch.equal(p, q) for p, q in zip(again, outs))
+
+
+def test_first_and_last_rows_of_the_largest_block():
+    """260000 tokens of 8008 features: element by element, adapters' terms of the size of the products'."""
+    require_gpu()
+    M, tail = 260000, 300
+    X, w, A, B = _make(tail, 64, 8008, 8)
+    A = [a * 8 for a in A]
+    big = torch.zeros(M, 64, dtype=torch.bfloat16, device="cuda")
+    big[:tail], big[M - tail:] = X, X
+    outs = Q.qlora_gated_fwd(big, w[0], w[1], A[0], B[0], A[1], B[1], 1.0, "silu")
+    for rows in (slice(0, tail), slice(M - tail, M)):
+        _check(X, w, A, B, 1.0, [t[rows] for t in outs])
 
 
 def test_large_adapters_leave_room_for_the_weights():
