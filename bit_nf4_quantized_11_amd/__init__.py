@@ -699,7 +699,8 @@ def qlora_gated_workspace(M: int, d_in: int, d_out: int, r: int) -> int:
 def qlora_gated_fwd(X: torch.Tensor, gate: NF4Weight, up: NF4Weight, A_gate: torch.Tensor, B_gate: torch.Tensor,
                     A_up: torch.Tensor, B_up: torch.Tensor, scale: float, activation: str = "silu", save: bool = True,
                     H: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
-    """H = act(G) U with G = X deq(gate)^T + scale (X A_gate) B_gate and U likewise, X [M][in] bf16.  save: also bf16 of G
+    """H = act(G) U with G = X deq(gate)^T + scale (X A_gate) B_gate and U likewise, X [M][in] bf16 (fp32 up to the activation,
+    but for bf16 of scale X A, as in qlora_linear_fwd).  save: also bf16 of G
     and U, and of X A of each, for the backward.  Returns (H, G, U, T_gate, T_up), the last four None without save."""
     dev, kind = X.device, _activation(activation)
     if X.dim() != 2 or X.shape[1] != gate.cols or not X.is_cuda:

@@ -242,10 +242,10 @@ BwdWs bwd_layout(void* base, int64_t M, int64_t in, int64_t out, int32_t r) {
 
 // The gated block's tiles have 64 features of each projection.  K-slices as many as all CUs take at once, where there are more than
 // three as many as leave a fifth of them to X A (256 tokens of 8192 -> 2048, 32 tiles: 41 us in 6 slices, 46 in 8; 100 tokens of
-// 4096 -> 4096, 64 tiles: 30 in 3, 33 in 4).  Two pay as well (256 tokens of 2048 -> 5504, 86 tiles: 39 us in 2, 57 in 3 that no longer
+// 4096 -> 4096, 64 tiles: 30 in 3, 33 in 4).  Two pay as well (256 tokens of 2048 -> 5504, 86 tiles: 36 us in 2, 57 in 3 that no longer
 // run at once, 48 whole; 300 tokens of 4096 -> 4096 62 against 74), but past one half panel not where nearly every CU writes
 // sums for few stages (256 tokens of 1024 -> 8192, 128 tiles: 38 us in 2, 35 whole).  With more panels a slice has 8 stages at
-// least (500 tokens of 2048 -> 512: 25 us in 4, 28 in 8), else 4.
+// least (500 tokens of 2048 -> 512: 24 us in 4, 28 in 8), else 4.
 int64_t gated_split_stages(int64_t M, int64_t in, int64_t out) {
   if (M <= 64 || M > kSplitMaxTokens) return 0;
   const int64_t tiles = (M + 255) / 256 * ((out + 63) / 64), nkb = in / 64;

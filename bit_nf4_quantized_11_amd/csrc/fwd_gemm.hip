@@ -15,8 +15,9 @@
 // The gated block's forward, H = bf16(act(G) U) with G and U two such products of the same X, runs through the same code: the 128
 // features of a tile are 64 of the gate's weight and the same 64 of the up projection's, so the waves of one feature half
 // hold G and those of the other U, and meet in LDS after the reduction.  X is read once for both, and G and U
-// reach memory only where the backward wants them.  2048 tokens of 4096 -> 11008 with G, U and T: 448 us = 820 TFLOP/s, of which X A takes
-// 15 (a library product of the two weights in bf16 alone: 417).
+// reach memory only where the backward wants them.  2048 tokens of 4096 -> 11008 with G, U and T: 444 to 473 us by box =
+// 780 to 830 TFLOP/s, of which X A takes 15 (a library product of the two weights in bf16 alone: 417).  Of 875 thousand cycles (1.8 GHz
+// under this load) the matrix cores are busy in 41 %, the VALU, with decoding, in 33 %, and the waves, two to a SIMD, wait 30 % of their time.
 #include <algorithm>
 
 #include "common.h"
@@ -246,7 +247,7 @@ __global__ __launch_bounds__(NT) void k_fwd_nf4_gemm(FwdParams p, FRONT front) {
   // it+2 in S0); a single exit keeps the accumulators in one register set
   uint32_t it = 0;
   // (of the gated forms) a wave of tokens 128 .. 255 of a panel that has none of them stores its share of the stages alone,
-  // between as many barriers: 100 tokens of 4096 -> 11008 61 us, with its products of zeros 71
+  // between as many barriers: 100 tokens of 4096 -> 11008 62 us a call, with its products of zeros 71
   if (GATED && __builtin_amdgcn_readfirstlane(wave_t<GATED>()) && p.M - (int64_t)m0 <= 128) {
     for (; it + 1 < nkb; it += 2) {
       load(min(it0 + it + 2, last), S0);

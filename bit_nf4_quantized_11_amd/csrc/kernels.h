@@ -134,7 +134,9 @@ hipError_t launch_gemv_epilogue(const float* partial, const GemvPlan& pl, int64_
 // one format.  act: qlora_activation.  G, U in bf16 where wanted (both or neither).
 // A tile takes a CU for the whole reduction, so the tiles past a multiple of 256 would leave most CUs idle for as long as
 // 256 take: up to 128 of them, at the end of the last token panel, are cut into slices instead, fp32 sums
-// [slice][256][npad] per side, which a last launch joins.
+// [slice][256][npad] per side, which a last launch joins.  4096 -> 11008, cut against whole, by full rounds before them: one (300
+// tokens) 121 us against 152, two (700) 196 / 226, four (1500) 364 / 396, five (2048) 470 / 482, seven (2800) 640 / 648, thirteen (5000)
+// 1120 / 1122; 1024 -> 2816 the same within 1 % (sixteen stages to a tile).
 struct GatedTail {
   int tiles, slices;    // 0: none
   int64_t npad;

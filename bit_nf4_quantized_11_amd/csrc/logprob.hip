@@ -6,9 +6,9 @@
 //
 // Bound by HBM: the forward reads the logits once (a wave holds its share of a part of a row in registers, so its sums are
 // taken from its own maximum without a second look at memory), the backward reads and writes them once.
-// Rows of several parts, and few long ones, are joined by a second kernel.  4096 x 32000 logits of bf16: forward 45 us = 5.8
-// TB/s and 4.7 for the join, backward 95 us = 5.5 TB/s; of fp32 forward 86 us = 6.1 TB/s.  With the waves of a row waiting for one
-// maximum it was 65 us.  8 x 32000: 5.3 us, 8.0 with 20 alternatives (latency).
+// Rows of several parts, and few long ones, are joined by a second kernel.  4096 x 32000 logits of bf16: forward 41 us = 6.4
+// TB/s and 4.7 for the join, backward 97 us = 5.4 TB/s; of fp32 forward 87 us = 6.0 TB/s.  With the waves of a row waiting for one
+// maximum it was 65 us.  8 x 32000: 5.3 us, 8.2 to 8.7 with 20 alternatives (latency).
 //
 // The k largest: a wave's k-th largest of its lanes' maxima is a bound that at least k of its elements reach; so is the least of
 // all waves' ceil(k / waves)-th largest, which leaves fewer where the large ones are spread (k = 20 over 8 waves: about 46 of a
@@ -544,8 +544,8 @@ struct Part {
 // By what the rows alone say, not by the outputs that a call asks for, so that the sums do not depend on these.
 //   A row of up to 32 K logits is one part, held by as few threads as its length allows (1000 logits by a wave: 4096 rows 6 us, by
 // 512 threads 12).
-//   Of bf16 and 128 rows or more, parts have 16 K logits at most: 4096 rows of 32000 take 46 + 5 us with the join (66 + 9 with 20
-// alternatives), whole ones 51 (fp32, as many: 86 whole, 87 + 5); 8 rows are faster whole (8 us with 20 alternatives).
+//   Of bf16 and 128 rows or more, parts have 16 K logits at most: 4096 rows of 32000 take 41 + 5 us with the join (62 + 9 with 20
+// alternatives), whole ones 51 (fp32, as many: 87 whole, 87 + 5); 8 rows are faster whole (8 us with 20 alternatives).
 //   Longer rows have parts of that size, and smaller ones while all rows together have fewer than 128.
 Part part_for(int64_t rows, int64_t vocab, bool fp32) {
   const int64_t n = pieces(vocab, fp32);

@@ -3,8 +3,8 @@
 //   h = bf16(x + residual),  y = bf16(h w r),  r = 1 / sqrt(mean(h^2) + eps)
 //   dx = bf16(dh + r (w dy - h r^2 mean(w dy h))),  dw = sum over rows of dy h r
 //
-// Bound by HBM: 4 to 8 B per element in either direction: forward of 4096 x 4096 with a residual 22 us = 6.1 TB/s, backward with dh
-// 22.3 us = 6.2 TB/s and 4.0 for the weight's gradient, whose 256 partials are 4 MB more (2048 x 8192, 512 partials: 28 + 4.7 us).  For a few rows by a
+// Bound by HBM: 4 to 8 B per element in either direction: forward of 4096 x 4096 with a residual 20.4 us = 6.6 TB/s, backward with dh
+// 22.3 us = 6.0 TB/s and 3.9 for the weight's gradient, whose 256 partials are 4 MB more (2048 x 8192, 512 partials: 24.7 + 4.4 us).  For a few rows by a
 // launch and two dependent round trips (16 x 8192: 3.8 us).  A row stays in the registers of the T threads that
 // hold it (a wave for short rows, a workgroup for long ones), 8 elements to a load, so each tensor is read or written once.
 // The backward walks over rows with the weight's gradient in registers, one partial per workgroup, summed by a second
@@ -113,11 +113,11 @@ __global__ __launch_bounds__(T < NT ? NT : T) void k_rms_norm(NormArgs a) {
 }
 
 // AHEAD: the next row's loads are issued before this row's sums are waited for (4096 x 4096 with dh 25.4 -> 24 us, without 20.3 ->
-// 18.7), where the registers leave eight waves to a CU all the same (2048 x 8192 with dh: 28 us without, 29 with).
+// 18.7), where the registers leave eight waves to a CU all the same (2048 x 8192 with dh, both kernels: 33.5 us without, 34.4 with).
 constexpr bool bwd_ahead(int c, bool dh) { return c <= 2 || !dh; }
 // Threads of a workgroup, rows of t threads.  Two rows of 256, which halves the partial weight gradients (2048 x 8192 27.0 -> 23.7 us
 // in all, 1531 x 5000 16.2 -> 15.1, 4096 x 4096 with dh 26.5 -> 25.5), where the next rows' loads bridge the wait for each other
-// (2048 x 8192 with dh: 31.1 us apart, 31.7 in pairs).
+// (2048 x 8192 with dh: 33.5 us apart, 33.2 in pairs, no more than two runs differ).
 constexpr int bwd_threads(int t, int c, bool dh) { return t < NT ? NT : t == 256 && bwd_ahead(c, dh) ? 512 : t; }
 
 // The loads of a row in the backward.
@@ -232,7 +232,8 @@ __global__ __launch_bounds__(bwd_threads(T, C, DH)) void k_rms_norm_bwd(NormArgs
 }
 
 // Rows too long for the registers of a workgroup: dy and h are read a second time (from the caches) after the sums
-// (500 x 32768: 38 us; held in registers, most of which spill, 102).
+// (500 x 32768 with dh: 34.5 us, and 6.9 for the weight's gradient: 256 partials are 34 MB out and back beside 131 MB of operands; held in
+// registers, most of which spill, 102).
 template <bool DH>
 __global__ __launch_bounds__(1024) void k_rms_norm_bwd_long(NormArgs a) {
   constexpr int T = 1024, C = 4;

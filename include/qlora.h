@@ -407,7 +407,8 @@ qlora_status qlora_kv_attn(const qlora_heads* q, int64_t rows, const qlora_kv_ca
  * where there is a residual (both or neither), w is 1 where the weight is NULL.  y or sum may be x or residual (same
  * data and stride), not each other; no other overlap.
  * Requires: 8 <= dim <= 32768, dim % 8 == 0; strides multiples of 8, 0 .. 2^36 - 1, at least dim for outputs (of one row:
- * anything); pointers 16-byte aligned; weight bf16 [dim]; eps >= 0 and finite (with 0, a row of zeros gives NaN); 0 <= rows < 2^22.
+ * anything); pointers 16-byte aligned; weight bf16 [dim]; eps >= 0 and finite (with 0, a row of zeros
+ * gives NaN, and one of elements below 2^-75, whose squares vanish in fp32, infinities); 0 <= rows < 2^22.
  * rows = 0 is a no-op.                                                                                   */
 qlora_status qlora_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual, int64_t residual_stride,
                             int64_t rows, int32_t dim, const uint16_t* weight, float eps, uint16_t* y, int64_t y_stride,
@@ -431,7 +432,8 @@ typedef enum { QLORA_ACT_SILU = 0, QLORA_ACT_GELU = 1 } qlora_activation;
 
 /* The gated feed-forward block in front of its last projection, on two quantized weights [out][in] with adapters:
  *   G = X deq(gate)^T + scale (X A_gate) B_gate,   U = X deq(up)^T + scale (X A_up) B_up,   H = bf16(act(G) U)
- * in one launch of products (the tokens are read once for both weights; G and U stay in registers, fp32).  For the backward
+ * in one launch of products (the tokens are read once for both weights; G and U are fp32 up to the activation).  X A is summed in fp32, and
+ * scale (X A) rounded to bf16 for its product with B, as in qlora_linear_fwd.  For the backward
  * bf16 of G and U [M][out] (both or neither) and of T = X A of each [M][r] (both or neither) are written where their pointers
  * are not NULL.  M = 0 is a no-op.
  * Requires: what qlora_linear_fwd does of X, H, each weight and its adapters; both weights of one shape and format
